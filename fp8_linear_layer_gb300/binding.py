@@ -19,6 +19,8 @@ LIB_PATH = os.path.join(HERE, "libfp8ll.so")
 E4M3, E5M2 = 0, 1
 EPI_NONE, EPI_BIAS, EPI_BIAS_GELU, EPI_DGELU, EPI_DGELU_BGRAD = 0, 1, 2, 3, 4
 ACC_FULL, ACC_FAST = 0, 1
+ACT_NONE, ACT_GELU = 0, 1
+F32, BF16 = 0, 1
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED_DEVICE, ERR_LAUNCH, ERR_TIMEOUT, ERR_WORKSPACE, ERR_SCRATCH = 0, -1, -2, -3, -4, -5, -6
 
 # every symbol include/fp8ll.h declares
@@ -27,7 +29,10 @@ EXPORTS = ("fp8_scale_ld", "fp8_quantize", "fp8_quantize_dual", "fp8_cast_f32", 
            "fp8_status_string", "fp8_debug_starve_next_gemm", "fp8_mx_sf_bytes", "fp8_mx_quantize",
            "fp8_mx_gemm_fprop", "fp8_mx_gemm_dgrad", "fp8_mx_gemm_wgrad", "fp8_tensor_amax", "fp8_tensor_quantize",
            "fp8_amax_history_update", "fp8_tensor_gemm_fprop", "fp8_tensor_gemm_dgrad", "fp8_tensor_gemm_wgrad",
-           "fp8_bgrad_from_operand", "fp8_quantize_dbias", "fp8_mx_quantize_dbias")
+           "fp8_bgrad_from_operand", "fp8_quantize_dbias", "fp8_mx_quantize_dbias", "fp8_gemm_linear",
+           "fp8_mx_gemm_linear", "fp8_tensor_gemm_linear", "fp8_rmsnorm_quantize", "fp8_mx_rmsnorm_quantize",
+           "fp8_tensor_rmsnorm_quantize", "fp8_rmsnorm_workspace_size", "fp8_rmsnorm_backward",
+           "fp8_grad_norm_workspace_size", "fp8_grad_norm", "fp8_clip_grads")
 
 
 class Fp8Error(RuntimeError):
@@ -49,6 +54,11 @@ class MxOperandStruct(ctypes.Structure):
 class TensorOperandStruct(ctypes.Structure):
     _fields_ = [("q", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("ld_q", ctypes.c_int64),
                 ("fmt", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class GradStruct(ctypes.Structure):
+    _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("n", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 _lib = None
@@ -98,13 +108,31 @@ def lib():
         L.fp8_bgrad_from_operand.argtypes = [i64, i64, op, vp, i32, vp]
         L.fp8_quantize_dbias.argtypes = [vp, i64, i64, i64, i32, vp, vp, i64, vp, vp, i64, vp, vp, sz, vp]
         L.fp8_mx_quantize_dbias.argtypes = [vp, i64, i64, i64, i32, vp, vp, vp, vp, sz, vp]
+        f32 = ctypes.c_float
+        L.fp8_gemm_linear.argtypes = [i64, i64, i64, op, op, vp, i32, vp, i64, i32, vp, vp, vp]
+        L.fp8_mx_gemm_linear.argtypes = [i64, i64, i64, mop, mop, vp, i32, vp, i64, vp, vp, vp]
+        L.fp8_tensor_gemm_linear.argtypes = [i64, i64, i64, top, top, vp, i32, vp, i64, vp, vp, vp]
+        norm = [vp, vp, vp, i64, i64, i64, i64, f32, i32]
+        L.fp8_rmsnorm_quantize.argtypes = norm + [vp, vp, vp, vp, vp, i64, vp, vp, i64, vp]
+        L.fp8_mx_rmsnorm_quantize.argtypes = norm + [vp, vp, vp, vp, vp, vp, vp, vp]
+        L.fp8_tensor_rmsnorm_quantize.argtypes = norm + [vp, vp, vp, vp, vp, vp, vp, vp, vp]
+        L.fp8_rmsnorm_workspace_size.argtypes = [i64, i64]
+        L.fp8_rmsnorm_workspace_size.restype = sz
+        L.fp8_rmsnorm_backward.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, vp, vp, i32, vp, sz, vp]
+        gp = ctypes.POINTER(GradStruct)
+        L.fp8_grad_norm_workspace_size.argtypes = [i64]
+        L.fp8_grad_norm_workspace_size.restype = sz
+        L.fp8_grad_norm.argtypes = [i64, gp, vp, vp, sz, vp]
+        L.fp8_clip_grads.argtypes = [i64, gp, f32, vp, vp, sz, vp]
         for name in ("fp8_quantize", "fp8_quantize_dual", "fp8_cast_f32", "fp8_gemm_fprop", "fp8_gemm_dgrad",
                      "fp8_gemm_dgrad_noalloc", "fp8_gemm_dgrad_quant",
                      "fp8_gemm_wgrad", "fp8_mx_quantize", "fp8_mx_gemm_fprop", "fp8_mx_gemm_dgrad",
                      "fp8_mx_gemm_wgrad", "fp8_tensor_amax", "fp8_tensor_quantize", "fp8_amax_history_update",
                      "fp8_tensor_gemm_fprop", "fp8_tensor_gemm_dgrad", "fp8_tensor_gemm_wgrad",
                      "fp8_grouped_wgrad", "fp8_bgrad_from_operand", "fp8_quantize_dbias", "fp8_mx_quantize_dbias",
-                     "fp8_get_device_status",
+                     "fp8_gemm_linear", "fp8_mx_gemm_linear", "fp8_tensor_gemm_linear", "fp8_rmsnorm_quantize",
+                     "fp8_mx_rmsnorm_quantize", "fp8_tensor_rmsnorm_quantize", "fp8_rmsnorm_backward",
+                     "fp8_grad_norm", "fp8_clip_grads", "fp8_get_device_status",
                      "fp8_debug_starve_next_gemm"):
             getattr(L, name).restype = i32
         _lib = L

@@ -147,16 +147,16 @@ int grid_for(const GemmParams& p, const DeviceInfo* dev) {
     return p.total_tiles < dev->num_sms ? p.total_tiles : dev->num_sms;
 }
 
-// TMA descriptor for the stored pre-activation Z (bf16 [M][N], row stride
-// N * 2 bytes, which TMA needs to be a multiple of 16: N % 8 == 0) in boxes
-// of 64 columns x 128 rows with 128-byte swizzling; outside the matrix reads
-// as zero.
-bool encode_z(const void* z, int64_t M, int64_t N, CUtensorMap* zmap) {
+// TMA descriptor for the stored pre-activation Z or a residual (bf16 [M][ld],
+// N columns used; TMA needs the row stride to be a multiple of 16 bytes: ld % 8
+// == 0) in boxes of 64 columns x 128 rows with 128-byte swizzling; outside the
+// matrix reads as zero.
+bool encode_z(const void* z, int64_t M, int64_t N, int64_t ld, CUtensorMap* zmap) {
     EncodeTiledFn enc = encode_fn();
     if (!enc) return false;
     const cuuint32_t estr[2] = {1, 1};
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(M)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(N) * 2};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
     const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(kTileM)};
     return enc(zmap, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(z), dims, strides, box, estr,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -295,6 +295,49 @@ static bool overlaps(const void* a, int64_t na, const void* b, int64_t nb) {
     return x < y + static_cast<uintptr_t>(nb) && y < x + static_cast<uintptr_t>(na);
 }
 
+// The epilogue arguments the three linear GEMMs share: checks them, fills the
+// parameters and picks the epilogue (without a residual the forward GEMM's).
+struct LinearArgs {
+    const void* bias;
+    int act;
+    const void* residual;
+    int64_t ldr;
+    void* out;
+    void* aux;
+};
+
+static bool valid_linear(int64_t M, int64_t N, const LinearArgs& a) {
+    if (!valid_mn(M, N)) return false;
+    if (a.act != FP8LL_ACT_NONE && a.act != FP8LL_ACT_GELU) return false;
+    if (!a.out || !aligned16(a.out)) return false;
+    if (a.bias && (reinterpret_cast<uintptr_t>(a.bias) & 15u) != 0) return false;
+    if (a.act == FP8LL_ACT_NONE && a.aux) return false;
+    if (a.aux && (!aligned16(a.aux) || overlaps(a.aux, M * N * 2, a.out, M * N * 2))) return false;
+    if (a.residual) {
+        if ((reinterpret_cast<uintptr_t>(a.residual) & 1u) != 0 || a.ldr < N || a.ldr >= (1LL << 36)) return false;
+        const int64_t rbytes = ((M - 1) * a.ldr + N) * 2;
+        // the output may take the residual's place, element by element
+        const bool in_place = a.residual == a.out && a.ldr == N;
+        if (!in_place && overlaps(a.residual, rbytes, a.out, M * N * 2)) return false;
+        if (a.aux && overlaps(a.residual, rbytes, a.aux, M * N * 2)) return false;
+    }
+    return true;
+}
+
+static int fill_linear(const LinearArgs& a, GemmParams& p) {
+    p.out = a.out;
+    p.aux = a.act == FP8LL_ACT_GELU ? a.aux : nullptr;
+    p.bias = a.bias;
+    p.res = a.residual;
+    p.ldr = a.ldr;
+    if (!a.residual && a.act == FP8LL_ACT_NONE) return a.bias ? kEpiBias : kEpiNone;
+    if (!a.residual) return kEpiBiasGelu;
+    const bool gelu = a.act == FP8LL_ACT_GELU;
+    if (aligned16(a.residual) && a.ldr % 8 == 0 && p.N % 8 == 0)
+        return gelu ? kEpiLinearGelu : kEpiLinear;
+    return gelu ? kEpiLinearGeluAny : kEpiLinearAny;
+}
+
 extern "C" {
 
 int64_t fp8_scale_ld(int64_t rows) { return rows <= 0 ? 0 : (rows + 3) / 4 * 4; }
@@ -423,7 +466,7 @@ int fp8_gemm_dgrad(int64_t M, int64_t N, int64_t K, const fp8ll_operand_t* A, co
     // otherwise the epilogue reads them from global memory
     std::memset(&maps.z, 0, sizeof(maps.z));
     if (N % 8 == 0) {
-        if (!encode_z(aux_bf16, M, N, &maps.z)) return FP8LL_ERR_LAUNCH;
+        if (!encode_z(aux_bf16, M, N, N, &maps.z)) return FP8LL_ERR_LAUNCH;
         p.z_tma = 1;
     }
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -468,7 +511,7 @@ int fp8_gemm_dgrad_quant(int64_t M, int64_t N, int64_t K, const fp8ll_operand_t*
     p.qscale = scale;
     p.qsld = scale_ld;
     std::memset(&maps.z, 0, sizeof(maps.z));
-    if (!encode_z(aux_bf16, M, N, &maps.z)) return FP8LL_ERR_LAUNCH;  // N % 128 == 0: rows 16-byte aligned
+    if (!encode_z(aux_bf16, M, N, N, &maps.z)) return FP8LL_ERR_LAUNCH;  // N % 128 == 0: rows 16-byte aligned
     p.z_tma = 1;
     return launch_gemm_dgrad(maps, p, kEpiDgeluQuant, reinterpret_cast<cudaStream_t>(stream), grid_for(p, dev)) == 0
                ? FP8LL_OK
@@ -897,4 +940,75 @@ int fp8_tensor_gemm_wgrad(int64_t M, int64_t N, int64_t K, const fp8ll_tensor_op
                : FP8LL_ERR_LAUNCH;
 }
 
+int fp8_gemm_linear(int64_t M, int64_t N, int64_t K, const fp8ll_operand_t* A, const fp8ll_operand_t* B,
+                    const void* bias_bf16, int act, const void* residual_bf16, int64_t ldr, int acc_mode,
+                    void* out_bf16, void* aux_bf16, fp8ll_stream_t stream) {
+    const LinearArgs args{bias_bf16, act, residual_bf16, ldr, out_bf16, aux_bf16};
+    if (!valid_linear(M, N, args) || K < 128 || K % 128 != 0 || K >= (1LL << 36)) return FP8LL_ERR_INVALID_ARG;
+    if (acc_mode != FP8LL_ACC_FULL && acc_mode != FP8LL_ACC_FAST) return FP8LL_ERR_INVALID_ARG;
+    if (!valid_operand(A, M, K) || !valid_operand(B, N, K)) return FP8LL_ERR_INVALID_ARG;
+    DeviceInfo* dev = nullptr;
+    int rc = current_device(&dev);
+    if (rc != FP8LL_OK) return rc;
+    TensorMaps maps;
+    if (!encode_operand(A, M, K, 128, &maps.a, &maps.sa) || !encode_operand(B, N, K, kTileN, &maps.b, &maps.sb))
+        return FP8LL_ERR_LAUNCH;
+    GemmParams p;
+    init_params(p, M, N, A, B, dev);
+    p.num_groups = 1;
+    p.groups[0] = GroupEntry{0, static_cast<int32_t>(K / 128), 0, 0};
+    p.total_tiles = p.tiles_per_group;
+    const int epi = fill_linear(args, p);
+    // an aligned residual goes through shared memory by TMA
+    std::memset(&maps.z, 0, sizeof(maps.z));
+    if (epi == kEpiLinear || epi == kEpiLinearGelu) {
+        if (!encode_z(residual_bf16, M, N, ldr, &maps.z)) return FP8LL_ERR_LAUNCH;
+        p.z_tma = 1;
+    }
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    rc = epi >= kEpiLinear ? launch_gemm_linear(maps, p, epi, s, grid_for(p, dev))
+                           : launch_gemm_fprop(maps, p, epi, s, grid_for(p, dev));
+    return rc == 0 ? FP8LL_OK : FP8LL_ERR_LAUNCH;
+}
+
+int fp8_mx_gemm_linear(int64_t M, int64_t N, int64_t K, const fp8ll_mx_operand_t* A, const fp8ll_mx_operand_t* B,
+                       const void* bias_bf16, int act, const void* residual_bf16, int64_t ldr, void* out_bf16,
+                       void* aux_bf16, fp8ll_stream_t stream) {
+    const LinearArgs args{bias_bf16, act, residual_bf16, ldr, out_bf16, aux_bf16};
+    if (!valid_linear(M, N, args)) return FP8LL_ERR_INVALID_ARG;
+    TensorMaps maps;
+    GemmParams p;
+    DeviceInfo* dev = nullptr;
+    int rc = mx_setup(M, N, K, A, B, maps, p, &dev);
+    if (rc != FP8LL_OK) return rc;
+    const int epi = fill_linear(args, p);
+    return launch_gemm_mx(maps, p, epi, reinterpret_cast<cudaStream_t>(stream)) == 0 ? FP8LL_OK : FP8LL_ERR_LAUNCH;
+}
+
+int fp8_tensor_gemm_linear(int64_t M, int64_t N, int64_t K, const fp8ll_tensor_operand_t* A,
+                           const fp8ll_tensor_operand_t* B, const void* bias_bf16, int act, const void* residual_bf16,
+                           int64_t ldr, void* out_bf16, void* aux_bf16, fp8ll_stream_t stream) {
+    const LinearArgs args{bias_bf16, act, residual_bf16, ldr, out_bf16, aux_bf16};
+    if (!valid_linear(M, N, args)) return FP8LL_ERR_INVALID_ARG;
+    TensorMaps maps;
+    GemmParams p;
+    DeviceInfo* dev = nullptr;
+    int rc = tensor_setup(M, N, K, A, B, maps, p, &dev);
+    if (rc != FP8LL_OK) return rc;
+    const int epi = fill_linear(args, p);
+    return launch_gemm_tensor(maps, p, epi, reinterpret_cast<cudaStream_t>(stream)) == 0 ? FP8LL_OK
+                                                                                         : FP8LL_ERR_LAUNCH;
+}
+
 }  // extern "C"
+
+namespace fp8ll {
+
+int current_device_sms(int* num_sms) {
+    DeviceInfo* dev = nullptr;
+    const int rc = current_device(&dev);
+    if (rc == FP8LL_OK) *num_sms = dev->num_sms;
+    return rc;
+}
+
+}  // namespace fp8ll

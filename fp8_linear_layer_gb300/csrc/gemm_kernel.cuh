@@ -19,7 +19,8 @@
 //               k+1 run while block k is promoted.  An N=256 MMA does twice
 //               the work of an N=128 one for the same A operand read, and
 //               the tensor core only reaches its full rate at this width.
-//   warp 2      dgrad only: TMA loader of the stored pre-activation tile Z
+//   warp 2      dgrad only (and, for the residual, the linear epilogues): TMA
+//               loader of the stored pre-activation tile Z
 //               (128 x 256 bf16, four 64-column boxes, 128-byte swizzle) into
 //               a one-slot shared-memory buffer, issued as soon as the previous
 //               tile's epilogue has released it, so that it lands during the
@@ -99,7 +100,8 @@ static_assert(sizeof(SmemLayout) % 1024 == 0, "Z buffer alignment");
 
 template <int EPI>
 constexpr bool uses_z() {
-    return EPI == kEpiDgelu || EPI == kEpiDgeluBgrad || EPI == kEpiDgeluQuant;
+    return EPI == kEpiDgelu || EPI == kEpiDgeluBgrad || EPI == kEpiDgeluQuant || EPI == kEpiLinear ||
+           EPI == kEpiLinearGelu;  // the linear epilogues stage an aligned residual in Z's place
 }
 template <int EPI>
 constexpr size_t smem_bytes() {
@@ -231,7 +233,8 @@ __device__ __forceinline__ void quad_transpose(uint32_t (&a)[4], int cq) {
     }
 }
 
-// fprop: Z = acc + bias[j]; Y = gelu(Z) or Z; bf16 out (+ bf16 aux Z).
+// fprop: Z = acc + bias[j]; Y = gelu(Z) or Z; bf16 out (+ bf16 aux Z).  A null
+// bias (with GELU only) counts as zeros.
 // Each chunk's eight values are computed without branches (rows or columns
 // outside the matrix compute on zeros) so that their independent GELU
 // evaluations overlap; only the memory accesses are guarded.
@@ -248,7 +251,7 @@ __device__ __forceinline__ void store_fprop(const GemmParams& p, int row0, int c
     for (int c = 0; c < kChunks; ++c) {
         const int col = col0 + 8 * c;
         bw[c] = 0u;
-        if (EPI != kEpiNone && col < p.N) {
+        if ((EPI == kEpiBias || (EPI == kEpiBiasGelu && bias)) && col < p.N) {
             if (pairs)
                 bw[c] = __ldg(reinterpret_cast<const unsigned int*>(bias + col));
             else
@@ -463,6 +466,149 @@ __device__ __forceinline__ void store_dgrad(const GemmParams& p, int row0, int c
             const int col = col0 + 8 * (v >> 1) + (v & 1);
             if (col < p.N) band[col] = cs[i];
         }
+    }
+}
+
+// linear: Z = acc + bias, Y = act(Z) + residual, in fp32, rounded once to bf16
+// (+ bf16 aux Z).  Three places for the residual, each a kernel of its own (one
+// kernel with all of them slowed the 1x128 promotion loop by a fifth, 502 ->
+// 589 us at 8192 x 4096 over 14336, through its register allocation):
+//   kResStaged  the tile was staged in shared memory by TMA (rrow as store_dgrad's
+//               zrow) and is read in the accumulator fragment's own order; rows
+//               of the output 16-byte aligned.
+//   kResVector  rows of output and residual 16-byte aligned: read as 16-byte
+//               vectors and put in fragment order by the quad transpose, which
+//               is its own inverse.
+//   kResAny     any sizes and alignment, in pairs of elements or one by one.
+// A tile's residual is read by the CTA that stores the same tile of the output,
+// each element before the store of it: out may be the residual's own buffer.
+enum ResMode : int { kResStaged = 0, kResVector = 1, kResAny = 2 };
+
+// elements off and off + 1 of a bf16 array where `one` and `two` say they
+// exist; `pairs`: every offset is even and the array 4-byte aligned
+__device__ __forceinline__ uint32_t load_pair(const uint16_t* p, int64_t off, bool one, bool two, bool pairs) {
+    if (pairs) return one ? *reinterpret_cast<const uint32_t*>(p + off) : 0u;
+    return (one ? static_cast<uint32_t>(p[off]) : 0u) | (two ? static_cast<uint32_t>(p[off + 1]) << 16 : 0u);
+}
+
+__device__ __forceinline__ void store_pair(uint16_t* p, int64_t off, bool one, bool two, bool pairs, uint32_t w) {
+    if (pairs) {
+        if (one) *reinterpret_cast<uint32_t*>(p + off) = w;
+        return;
+    }
+    if (one) p[off] = static_cast<uint16_t>(w & 0xFFFFu);
+    if (two) p[off + 1] = static_cast<uint16_t>(w >> 16);
+}
+
+template <bool GELU, int RES>
+__device__ __forceinline__ void store_linear(const GemmParams& p, int row0, int col0,
+                                             const uint64_t (&acc)[4 * kChunks], int g8, const uint8_t* rrow) {
+    uint16_t* out = static_cast<uint16_t*>(p.out);
+    uint16_t* aux = GELU ? static_cast<uint16_t*>(p.aux) : nullptr;
+    const uint16_t* bias = static_cast<const uint16_t*>(p.bias);
+    const uint16_t* res = static_cast<const uint16_t*>(p.res);
+    const int cq = (col0 >> 1) & 3;
+    const int cbase = col0 - 2 * cq;
+    // bias pairs: of all chunks at once where the registers allow it, so that
+    // their loads are in flight together, else of one group of four at a time
+    const bool pairs = (p.N & 1) == 0;
+    const bool res_pairs = pairs && (p.ldr & 1) == 0 && (reinterpret_cast<uintptr_t>(res) & 3u) == 0;
+    constexpr int kAhead = RES == kResStaged ? kChunks : 4;
+    uint32_t bw[kAhead];
+    auto load_bias = [&](int c0) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int col = col0 + 8 * (c0 + i);
+            if (RES == kResAny)
+                bw[i] = bias ? load_pair(bias, col, col < p.N, col + 1 < p.N, pairs) : 0u;
+            else
+                bw[i] = bias && col < p.N ? __ldg(reinterpret_cast<const unsigned int*>(bias + col)) : 0u;
+        }
+    };
+    if (kAhead == kChunks) load_bias(0);
+#pragma unroll
+    for (int g = 0; g < kChunks / 4; ++g) {
+        const int vcol = cbase + 8 * (4 * g + cq);  // the lane's eight columns in the transposed order
+        if (kAhead == 4) load_bias(4 * g);
+        uint32_t yw[4][4], zw[4][4];  // [row][chunk]; yw holds the residual's pair until the sum replaces it
+        if (RES == kResVector) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (row0 + 8 * r < p.M && vcol < p.N)
+                    v = *reinterpret_cast<const uint4*>(res + (row0 + 8 * r) * p.ldr + vcol);
+                yw[r][0] = v.x; yw[r][1] = v.y; yw[r][2] = v.z; yw[r][3] = v.w;
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) quad_transpose(yw[r], cq);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int c = 4 * g + j;
+            uint32_t rw[4];
+            if (RES == kResStaged) load_z_smem(rrow, g8, c, rw);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                if (RES == kResVector) rw[r] = yw[r][j];
+                if (RES == kResAny) {
+                    const int col = col0 + 8 * c, row = row0 + 8 * r;
+                    const bool in = row < p.M;
+                    rw[r] = load_pair(res, row * p.ldr + col, in && col < p.N, in && col + 1 < p.N, res_pairs);
+                }
+                const float2 a = unpack_f32x2(acc[4 * c + r]);
+                const uint32_t b = bw[c % kAhead];
+                const float z0 = a.x + bf16_lo(b), z1 = a.y + bf16_hi(b);
+                const float2 y = GELU ? gelu_tanh2(z0, z1) : make_float2(z0, z1);
+                yw[r][j] = pack_bf16x2(y.x + bf16_lo(rw[r]), y.y + bf16_hi(rw[r]));
+                zw[r][j] = pack_bf16x2(z0, z1);
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int row = row0 + 8 * r;
+            if (RES == kResAny) {
+                if (row >= p.M) continue;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int col = col0 + 8 * (4 * g + j);
+                    const int64_t off = static_cast<int64_t>(row) * p.N + col;
+                    store_pair(out, off, col < p.N, col + 1 < p.N, pairs, yw[r][j]);
+                    if (aux) store_pair(aux, off, col < p.N, col + 1 < p.N, pairs, zw[r][j]);
+                }
+                continue;
+            }
+            quad_transpose(yw[r], cq);
+            if (aux) quad_transpose(zw[r], cq);
+            if (row >= p.M || vcol >= p.N) continue;
+            const int64_t off = static_cast<int64_t>(row) * p.N + vcol;
+            *reinterpret_cast<uint4*>(out + off) = make_uint4(yw[r][0], yw[r][1], yw[r][2], yw[r][3]);
+            if (aux) *reinterpret_cast<uint4*>(aux + off) = make_uint4(zw[r][0], zw[r][1], zw[r][2], zw[r][3]);
+        }
+    }
+}
+
+template <int EPI>
+constexpr bool is_linear() {
+    return EPI == kEpiLinear || EPI == kEpiLinearGelu || EPI == kEpiLinearAny || EPI == kEpiLinearGeluAny;
+}
+template <int EPI>
+constexpr bool is_gelu_linear() {
+    return EPI == kEpiLinearGelu || EPI == kEpiLinearGeluAny;
+}
+template <int EPI>
+constexpr bool is_any_linear() {
+    return EPI == kEpiLinearAny || EPI == kEpiLinearGeluAny;
+}
+
+// asks for the residual of a thread's tile rows in L2 while the K loop runs
+// (each lane of a quad one of the quad's four rows, 128 columns: three lines)
+__device__ __forceinline__ void prefetch_residual(const GemmParams& p, int prow, int pc0) {
+    if (prow < p.M && pc0 < p.N) {
+        const uint16_t* row = static_cast<const uint16_t*>(p.res) + prow * p.ldr;
+        const int pc1 = min(pc0 + kHalfN - 1, p.N - 1);
+        prefetch_l2(row + pc0);
+        prefetch_l2(row + min(pc0 + 64, pc1));
+        prefetch_l2(row + pc1);
     }
 }
 
@@ -751,7 +897,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < 4 * kChunks; ++j) acc[j] = 0ull;
             const uint32_t tq = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                                 static_cast<uint32_t>(half * kHalfN);
-            if (uses_z<EPI>() && !z_staged) {
+            if (is_linear<EPI>()) {
+                if (is_any_linear<EPI>()) prefetch_residual(p, m0 + q * 32 + g8 + 8 * cq, n0 + half * kHalfN);
+            } else if (uses_z<EPI>() && !z_staged) {
                 // the stored pre-activations of this tile are read once the K loop
                 // is done: ask for them in L2 now (each lane of a quad one of the
                 // quad's four rows; a row's 128 columns span at most three lines)
@@ -814,6 +962,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 store_wgrad(p, ge.out_index, row0, col0, acc);
             } else if (EPI == kEpiNone || EPI == kEpiBias || EPI == kEpiBiasGelu) {
                 store_fprop<EPI>(p, row0, col0, acc);
+            } else if (is_linear<EPI>()) {
+                if (is_any_linear<EPI>()) {
+                    store_linear<is_gelu_linear<EPI>(), kResAny>(p, row0, col0, acc, g8, nullptr);
+                } else {
+                    ok = mbar_wait_warp(smem_addr(&sm.zfull), zph, budget);
+                    if (!ok) break;
+                    store_linear<is_gelu_linear<EPI>(), kResStaged>(
+                        p, row0, col0, acc, g8,
+                        zs + half * (kHalfN / kZBoxCols) * kZBoxBytes + (q * 32 + g8) * 128 + 4 * cq);
+                    // read with ordinary loads, refilled by TMA: order before the release
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    mbar_arrive_lane0(smem_addr(&sm.zempty), lane);
+                    zph ^= 1u;
+                }
             } else {
                 // bias-gradient partials of this warp's 32 rows -> workspace band (4*mt + q)
                 float* band = (EPI == kEpiDgeluBgrad) ? p.workspace + (static_cast<int64_t>(mt) * 4 + q) * p.N

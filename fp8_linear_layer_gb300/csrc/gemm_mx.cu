@@ -292,6 +292,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             int mt, nt;
             decode_mx_tile(p, t, mt, nt);
             const int m0 = mt * kMxRows + static_cast<int>(rank) * kBM, n0 = nt * kBN;
+            if (is_linear<EPI>())
+                prefetch_residual(p, m0 + q * 32 + g8 + 8 * cq, n0 + half * kHalfN);
             if (EPI == kEpiDgelu || EPI == kEpiDgeluBgrad) {
                 const int prow = m0 + q * 32 + g8 + 8 * cq;
                 const int pc0 = n0 + half * kHalfN;
@@ -335,6 +337,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 store_wgrad(p, 0, row0, col0, acc);
             } else if (EPI == kEpiNone || EPI == kEpiBias || EPI == kEpiBiasGelu) {
                 store_fprop<EPI>(p, row0, col0, acc);
+            } else if (is_linear<EPI>()) {
+                store_linear<is_gelu_linear<EPI>(), is_any_linear<EPI>() ? kResAny : kResVector>(p, row0, col0, acc, g8,
+                                                                                                  nullptr);
             } else {
                 float* band = (EPI == kEpiDgeluBgrad) ? p.workspace + (static_cast<int64_t>(m0 / kBM) * 4 + q) * p.N
                                                       : nullptr;
@@ -399,6 +404,10 @@ int launch_gemm_mx(const TensorMaps& maps, const GemmParams& p, int epi, cudaStr
         case kEpiDgelu: return launch_mx_impl<kEpiDgelu>(maps, p, stream);
         case kEpiDgeluBgrad: return launch_mx_impl<kEpiDgeluBgrad>(maps, p, stream);
         case kEpiWgrad: return launch_mx_impl<kEpiWgrad>(maps, p, stream);
+        case kEpiLinear: return launch_mx_impl<kEpiLinear>(maps, p, stream);
+        case kEpiLinearGelu: return launch_mx_impl<kEpiLinearGelu>(maps, p, stream);
+        case kEpiLinearAny: return launch_mx_impl<kEpiLinearAny>(maps, p, stream);
+        case kEpiLinearGeluAny: return launch_mx_impl<kEpiLinearGeluAny>(maps, p, stream);
         default: return -3;
     }
 }

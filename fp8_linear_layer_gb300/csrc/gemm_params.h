@@ -18,6 +18,11 @@ enum EpiKind : int {
     kEpiDgeluBgrad = 4,
     kEpiWgrad = 5,  // fp32 out (+)= C
     kEpiDgeluQuant = 6,  // dgrad: dZ = C * gelu'(Z) -> bf16, plus its e5m2 row cast (codes + 1x128 scales)
+    // Z = C + bias; Y = act(Z) + residual, act none or gelu; bias and aux = Z optional
+    kEpiLinear = 7,       // the residual's and the output's rows 16-byte aligned
+    kEpiLinearGelu = 8,
+    kEpiLinearAny = 9,    // any sizes and alignment
+    kEpiLinearGeluAny = 10,
 };
 
 // One schedulable group of output tiles: all tiles of a group share the same
@@ -38,7 +43,7 @@ struct GemmParams {
     int32_t total_tiles;
     int32_t accumulate;   // wgrad: 1 = out +=, 0 = out =
     int32_t debug_starve; // test hook: producer issues no loads
-    int32_t z_tma;        // dgrad: 1 = stored Z tiles staged in shared memory by TMA (maps.z)
+    int32_t z_tma;        // dgrad: 1 = stored Z tiles staged in shared memory by TMA (maps.z); linear: the residual's
     uint32_t idesc;       // tcgen05 instruction descriptor (formats, tile shape)
     uint64_t budget_ns;   // wall-clock budget of each pipeline wait
     void* out;            // bf16 [M][N] (fprop/dgrad) or fp32 [G][M][N] (wgrad)
@@ -55,12 +60,14 @@ struct GemmParams {
     uint8_t* qout;        // kEpiDgeluQuant: e5m2 codes of the bf16 dZ, [M][N]
     float* qscale;        // kEpiDgeluQuant: their scales, [N/128][qsld]
     int64_t qsld;
+    const void* res;      // kEpiLinear*: bf16 residual [M][ldr]
+    int64_t ldr;
     GroupEntry groups[kMaxGroups];
 };
 
 struct TensorMaps {
     CUtensorMap a, b, sa, sb;
-    CUtensorMap z;  // dgrad with z_tma: Z bf16 [M][N] in 64 x 128 boxes, 128-byte swizzle
+    CUtensorMap z;  // with z_tma: Z or the residual, bf16 [M][N] in 64 x 128 boxes, 128-byte swizzle
 };
 
 }  // namespace fp8ll

@@ -16,6 +16,10 @@
  *   fp8_gemm_wgrad      fp32 out (+)= A B^T
  *   fp8_grouped_wgrad   per-group fp32 out_g (+)= A_g B_g^T, groups along K
  *   fp8_bgrad_from_operand  bias gradient as row sums of a 1x128-scaled operand
+ *   fp8_gemm_linear     Y = act(A B^T + bias) + residual (also few rows)
+ *   fp8_rmsnorm_*       RMS norm with the residual's addition and an fp8 output,
+ *                       and its backward pass
+ *   fp8_grad_norm, fp8_clip_grads  global gradient norm and clipping
  *
  * Conventions shared by every entry point
  *   - One row-major "NT" convention: C[M][N] = A[M][K] . B[N][K]^T; both
@@ -409,6 +413,116 @@ int fp8_tensor_gemm_dgrad(int64_t M, int64_t N, int64_t K, const fp8ll_tensor_op
                           void* workspace, size_t workspace_bytes, fp8ll_stream_t stream);
 int fp8_tensor_gemm_wgrad(int64_t M, int64_t N, int64_t K, const fp8ll_tensor_operand_t* A,
                           const fp8ll_tensor_operand_t* B, float* out, int accumulate, fp8ll_stream_t stream);
+
+/* ---- the residual block around the layer ----------------------------------
+ * Activations of fp8_gemm_linear: none, or the tanh GELU above. */
+enum { FP8LL_ACT_NONE = 0, FP8LL_ACT_GELU = 1 };
+
+/* Types of fp8ll_grad_t. */
+enum { FP8LL_F32 = 0, FP8LL_BF16 = 1 };
+
+/* Matrix product with bias, activation and residual in its epilogue:
+ *   Z = A B^T + bias;  Y = act(Z) + residual     (fp32, rounded once to bf16)
+ *   A, B, M, N, K, acc_mode: as fp8_gemm_fprop (M, N >= 1, any value).
+ *   bias_bf16:     [N], 16-byte aligned, or NULL.
+ *   residual_bf16: [M][ldr], 2-byte aligned, ldr >= N, or NULL.  It may be the
+ *                  output's own buffer when ldr == N, else they must not overlap.
+ *   out_bf16:      [M][N] contiguous, 16-byte aligned.
+ *   aux_bf16:      [M][N] receives Z with FP8LL_ACT_GELU, or NULL; must be NULL
+ *                  with FP8LL_ACT_NONE.
+ * The gradient of act = GELU is fp8_gemm_dgrad's epilogue (with this Z); the
+ * residual's gradient is dY itself; dX = dZ W + dX_residual is this call again.
+ * A product of few rows runs a kernel of its own that streams B once through
+ * all SMs, so its sums are ordered differently from fp8_gemm_fprop's. */
+int fp8_gemm_linear(int64_t M, int64_t N, int64_t K, const fp8ll_operand_t* A, const fp8ll_operand_t* B,
+                    const void* bias_bf16, int act, const void* residual_bf16, int64_t ldr, int acc_mode,
+                    void* out_bf16, void* aux_bf16, fp8ll_stream_t stream);
+int fp8_mx_gemm_linear(int64_t M, int64_t N, int64_t K, const fp8ll_mx_operand_t* A, const fp8ll_mx_operand_t* B,
+                       const void* bias_bf16, int act, const void* residual_bf16, int64_t ldr, void* out_bf16,
+                       void* aux_bf16, fp8ll_stream_t stream);
+int fp8_tensor_gemm_linear(int64_t M, int64_t N, int64_t K, const fp8ll_tensor_operand_t* A,
+                           const fp8ll_tensor_operand_t* B, const void* bias_bf16, int act, const void* residual_bf16,
+                           int64_t ldr, void* out_bf16, void* aux_bf16, fp8ll_stream_t stream);
+
+/* Root-mean-square norm of a residual stream, cast to fp8 for the GEMMs:
+ *   h = bf16(x + residual)               (h = x without a residual)
+ *   rstd = 1 / sqrt(mean(h^2) + eps)     per row, of the rounded h
+ *   y = fl32(fl32(h * rstd) * gamma)     -> codes and scales by the cast rules,
+ *                                           from fp32 (no bf16 rounding first)
+ *   x, residual: bf16 [rows][ldx / ldr], 16-byte aligned, leading dimensions
+ *                >= cols and % 8 == 0; residual may be NULL.
+ *   gamma: bf16 [cols], 16-byte aligned.  eps: finite, >= 0.
+ *   cols % 128 == 0, cols <= 32768; rows: any.
+ *   h: bf16 [rows][cols], required with a residual (may be x or the residual
+ *      itself when that is contiguous), else NULL or a copy of x.
+ *   rstd: fp32 [rows], for the backward pass.
+ * Outputs, at least one of:
+ *   y:      bf16 [rows][cols].
+ *   q_rows: codes [rows][cols], scales as fp8_quantize / fp8_mx_quantize
+ *           (transpose = 0) / fp8_tensor_quantize lay them out.
+ *   q_cols: the transposed codes [cols][rows], blocked down the rows (transpose
+ *           = 1), for the weight gradient; rows % 128 == 0, rows / 128 <= 65535.
+ * The per-tensor form casts with *amax_in, writes *scale and, if amax_out is
+ * not NULL, max|y| (for the history of the next step).
+ * No output may overlap another or an input, but for h as above.
+ * rows == 0 or cols == 0 is a no-op.  A row of zeros gives zeros with scale 1. */
+int fp8_rmsnorm_quantize(const void* x_bf16, const void* residual_bf16, const void* gamma_bf16, int64_t rows,
+                         int64_t cols, int64_t ldx, int64_t ldr, float eps, int fmt, void* h_bf16, float* rstd,
+                         void* y_bf16, uint8_t* q_rows, float* scale_rows, int64_t scale_ld_rows, uint8_t* q_cols,
+                         float* scale_cols, int64_t scale_ld_cols, fp8ll_stream_t stream);
+int fp8_mx_rmsnorm_quantize(const void* x_bf16, const void* residual_bf16, const void* gamma_bf16, int64_t rows,
+                            int64_t cols, int64_t ldx, int64_t ldr, float eps, int fmt, void* h_bf16, float* rstd,
+                            void* y_bf16, uint8_t* q_rows, uint8_t* sf_rows, uint8_t* q_cols, uint8_t* sf_cols,
+                            fp8ll_stream_t stream);
+int fp8_tensor_rmsnorm_quantize(const void* x_bf16, const void* residual_bf16, const void* gamma_bf16, int64_t rows,
+                                int64_t cols, int64_t ldx, int64_t ldr, float eps, int fmt, const float* amax_in,
+                                void* h_bf16, float* rstd, void* y_bf16, uint8_t* q_rows, uint8_t* q_cols,
+                                float* scale, float* amax_out, fp8ll_stream_t stream);
+
+/* Bytes of workspace fp8_rmsnorm_backward needs (partial sums of dgamma). */
+size_t fp8_rmsnorm_workspace_size(int64_t rows, int64_t cols);
+
+/* Backward pass of the norm, with xhat = h rstd and d = dy gamma:
+ *   dx = rstd (d - xhat mean(d xhat)) + residual_grad   (bf16 [rows][cols])
+ *   dgamma[c] (+)= sum over rows of dy xhat             (fp32 [cols], 16-byte aligned)
+ * dx is the gradient of both x and the residual.
+ *   dy, h, residual_grad: bf16, 16-byte aligned, leading dimensions >= cols and
+ *   % 8 == 0; residual_grad may be NULL.  rstd: the forward call's.
+ *   cols % 8 == 0, cols <= 32768; rows: any (0 zeroes dgamma or keeps it).
+ *   dx may be dy or residual_grad itself when that is contiguous; no other
+ *   output, nor the workspace (16-byte aligned), may overlap anything.
+ * The sums run in fp32 in a fixed order: results are deterministic. */
+int fp8_rmsnorm_backward(const void* dy_bf16, const void* h_bf16, const void* gamma_bf16, const float* rstd,
+                         const void* residual_grad_bf16, int64_t rows, int64_t cols, int64_t lddy, int64_t ldh,
+                         int64_t ldres, void* dx_bf16, float* dgamma, int accumulate, void* workspace,
+                         size_t workspace_bytes, fp8ll_stream_t stream);
+
+/* One gradient tensor: n elements of fp32 or bf16, contiguous, aligned to the
+ * element.  out: where the clipped gradient goes, of the same type (grad itself
+ * for in place; otherwise it must overlap no tensor of the list). */
+typedef struct {
+    const void* grad;
+    void* out;
+    int64_t n;
+    int32_t dtype; /* FP8LL_F32 or FP8LL_BF16 */
+    int32_t reserved;
+} fp8ll_grad_t;
+
+/* Bytes of workspace of the two calls below for `count` tensors. */
+size_t fp8_grad_norm_workspace_size(int64_t count);
+
+/* *norm (fp32, device) = sqrt of the sum of squares over all tensors.  grads:
+ * HOST array (copied before the call returns).  Squares are summed in fp32 per
+ * CTA, then in fp64, in a fixed order.  No tensors, or empty ones: 0. */
+int fp8_grad_norm(int64_t count, const fp8ll_grad_t* grads, float* norm, void* workspace, size_t workspace_bytes,
+                  fp8ll_stream_t stream);
+
+/* The same norm, then out = grad * min(1, max_norm / (norm + 1e-6)) for every
+ * tensor (max_norm >= 0).  Nothing is read back to the host.  A norm that is
+ * not finite is reported as it is: NaN makes every gradient NaN, infinity makes
+ * the finite ones 0. */
+int fp8_clip_grads(int64_t count, const fp8ll_grad_t* grads, float max_norm, float* norm, void* workspace,
+                   size_t workspace_bytes, fp8ll_stream_t stream);
 
 /* Synchronizes `stream`, then returns and clears the device status word of
  * the current device: FP8LL_OK, or the first FP8LL_ERR_TIMEOUT recorded by a

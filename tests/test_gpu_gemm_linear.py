@@ -1,0 +1,184 @@
+"""The matrix product with bias, activation and residual in its epilogue, in
+the three recipes, against the oracle's fp64 product."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import workloads
+from helpers import FULL_C, assert_within, bf16_to_f64, bf16_ulp
+
+pytestmark = pytest.mark.gpu
+E4M3, E5M2 = 0, 1
+RECIPES = ["block", "mx", "tensor"]
+
+
+def operands(fp8, recipe, a, b, fmt_a, fmt_b):
+    """(A, B, product in fp64, sum of magnitudes) of two bf16 matrices."""
+    ab, bb = workloads.bits(a), workloads.bits(b)
+    if recipe == "block":
+        qa, sa = oracle.quantize(ab, fmt_a)
+        qb, sb = oracle.quantize(bb, fmt_b)
+        return (fp8.quantize(a.cuda(), fmt_a), fp8.quantize(b.cuda(), fmt_b),
+                *oracle.gemm(qa, sa, fmt_a, qb, sb, fmt_b))
+    if recipe == "mx":
+        qa, ea = oracle.mx_quantize(ab, fmt_a)
+        qb, eb = oracle.mx_quantize(bb, fmt_b)
+        return (fp8.mx_quantize(a.cuda(), fmt_a), fp8.mx_quantize(b.cuda(), fmt_b),
+                *oracle.mx_gemm(qa, ea, fmt_a, qb, eb, fmt_b))
+    ma, mb = float(a.float().abs().max()), float(b.float().abs().max())
+    qa, sa, _ = oracle.tensor_quantize(ab, fmt_a, ma)
+    qb, sb, _ = oracle.tensor_quantize(bb, fmt_b, mb)
+    A, _ = fp8.tensor_quantize(a.cuda(), fmt_a, fp8.tensor_amax(a.cuda()))
+    B, _ = fp8.tensor_quantize(b.cuda(), fmt_b, fp8.tensor_amax(b.cuda()))
+    return (A, B, *oracle.tensor_gemm(qa, sa, fmt_a, qb, sb, fmt_b))
+
+
+def product(fp8, recipe):
+    return {"block": fp8.gemm_linear, "mx": fp8.mx_gemm_linear, "tensor": fp8.tensor_gemm_linear}[recipe]
+
+
+def gelu(z):
+    return z / (1.0 + np.exp(-np.clip(2 * np.sqrt(2 / np.pi) * (z + 0.044715 * z ** 3), -700, 700)))
+
+
+def check(y, z, acc, S, bias, act, residual):
+    """The bounds of the forward GEMM's tests: c S for the product, the fp32 evaluation of gelu (96 ulp), an fp32
+    rounding of each sum, and the output's own rounding."""
+    zo = acc + (bf16_to_f64(bias) if bias is not None else 0.0)
+    yo = gelu(zo) if act else zo
+    r = bf16_to_f64(residual) if residual is not None else 0.0
+    want = yo + r
+    slope = 1.13 if act else 1.0
+    err = slope * FULL_C * S + (1e-5 * np.abs(zo) if act else 0.0) + 2.0 ** -23 * (np.abs(zo) + np.abs(r))
+    got = bf16_to_f64(y)
+    assert_within(got, want, err + bf16_ulp(np.maximum(np.abs(got), np.abs(want))), "Y")
+    if z is not None:
+        gz = bf16_to_f64(z)
+        assert_within(gz, zo, FULL_C * S + 2.0 ** -23 * np.abs(zo) + bf16_ulp(np.maximum(np.abs(gz), np.abs(zo))), "Z")
+
+
+SHAPES = [(1, 1, 128), (1, 256, 4096), (2, 40, 256), (3, 1000, 896), (8, 129, 1280), (9, 72, 2048), (16, 512, 7168),
+          (17, 264, 384), (33, 2110, 512), (64, 96, 1024), (100, 301, 640), (129, 264, 256), (300, 520, 384)]
+
+
+@pytest.mark.parametrize("recipe", RECIPES)
+@pytest.mark.parametrize("M,N,K", SHAPES)
+def test_epilogues(fp8, recipe, M, N, K):
+    seed = M + N + K
+    fa = E5M2 if M % 3 == 0 else E4M3
+    fb = E5M2 if N % 5 == 0 else E4M3
+    a = workloads.normal_bf16((M, K), seed, "a")
+    b = workloads.normal_bf16((N, K), seed, "b", std=0.05)
+    bias = workloads.normal_bf16((N,), seed, "bias").cuda()
+    res = workloads.normal_bf16((M, N), seed, "res", std=3.0).cuda()
+    A, B, acc, S = operands(fp8, recipe, a, b, fa, fb)
+    for act in (fp8.ACT_NONE, fp8.ACT_GELU):
+        for bi in (None, bias):
+            for r in (None, res):
+                for aux in ((False, True) if act else (False,)):
+                    out = torch.full((M, N), float("nan"), dtype=torch.bfloat16, device="cuda")
+                    y, z = product(fp8, recipe)(A, B, bi, act, r, out=out, want_aux=aux)
+                    torch.cuda.synchronize()
+                    assert fp8.device_status() == 0 and (z is not None) == aux
+                    check(y, z, acc, S, bi, act, r)
+
+
+@pytest.mark.parametrize("recipe", RECIPES)
+@pytest.mark.parametrize("M,N", [(5, 264), (5, 263), (200, 264), (200, 262), (200, 263)])
+def test_residual_strides_and_in_place(fp8, recipe, M, N):
+    K = 384
+    a = workloads.normal_bf16((M, K), 5, "a")
+    b = workloads.normal_bf16((N, K), 5, "b", std=0.05)
+    A, B, acc, S = operands(fp8, recipe, a, b, E4M3, E4M3)
+    base = workloads.normal_bf16((M, N + 24), 5, "res").cuda()
+    call = product(fp8, recipe)
+    seen = []
+    for off, ld in ((0, N + 24), (8, N + 24), (2, N + 24), (1, N + 24)):  # rows aligned to 16, 16, 4 and 2 bytes
+        r = base[:, off:off + N]
+        y, _ = call(A, B, None, fp8.ACT_NONE, r)
+        torch.cuda.synchronize()
+        check(y, None, acc, S, None, 0, r)
+        packed, _ = call(A, B, None, fp8.ACT_NONE, r.contiguous())
+        inplace = r.contiguous()
+        got, _ = call(A, B, None, fp8.ACT_NONE, inplace, out=inplace)
+        torch.cuda.synchronize()
+        # one arithmetic for every layout of the residual
+        assert torch.equal(packed, y) and torch.equal(got, y) and got.data_ptr() == inplace.data_ptr()
+        seen.append(y)
+    assert not torch.equal(seen[0], seen[1])
+    assert fp8.device_status() == 0
+
+
+@pytest.mark.parametrize("recipe", RECIPES)
+def test_without_a_residual_it_is_the_forward_product(fp8, recipe):
+    # large enough for the tile kernel: the same kernel, the same bits
+    M, N, K = 384, 520, 512
+    a, b = workloads.normal_bf16((M, K), 9, "a"), workloads.normal_bf16((N, K), 9, "b", std=0.05)
+    bias = workloads.normal_bf16((N,), 9, "bias").cuda()
+    A, B, _, _ = operands(fp8, recipe, a, b, E4M3, E4M3)
+    fprop = {"block": fp8.gemm_fprop, "mx": fp8.mx_gemm_fprop, "tensor": fp8.tensor_gemm_fprop}[recipe]
+    for epi, act, bi in ((fp8.EPI_NONE, 0, None), (fp8.EPI_BIAS, 0, bias), (fp8.EPI_BIAS_GELU, 1, bias)):
+        want, wz = fprop(A, B, bi, epi)
+        got, gz = product(fp8, recipe)(A, B, bi, act, want_aux=bool(act))
+        assert torch.equal(want, got) and (wz is None or torch.equal(wz, gz))
+    zero, _ = fprop(A, B, torch.zeros_like(bias), fp8.EPI_BIAS_GELU)
+    none, _ = product(fp8, recipe)(A, B, None, fp8.ACT_GELU)
+    assert torch.equal(zero, none)
+
+
+@pytest.mark.parametrize("recipe", RECIPES)
+@pytest.mark.parametrize("M", [4, 300])
+def test_the_gradients_of_a_block(fp8, recipe, M):
+    # Y = X W^T + R: dX + what reaches X around the product is the same call on dY and W down its columns
+    N, K = 256, 384
+    dy = workloads.normal_bf16((M, N), 3, "dy", std=1e-2)
+    w = workloads.normal_bf16((N, K), 3, "w", std=0.05)
+    skip = workloads.normal_bf16((M, K), 3, "skip", std=1e-2).cuda()
+    A, B, acc, S = operands(fp8, recipe, dy, w.t().contiguous(), E5M2, E4M3)
+    dx, _ = product(fp8, recipe)(A, B, None, fp8.ACT_NONE, skip)
+    torch.cuda.synchronize()
+    check(dx, None, acc, S, None, 0, skip)
+
+
+@pytest.mark.parametrize("recipe", RECIPES)
+@pytest.mark.parametrize("M", [3, 200])
+def test_nan_stays_in_its_row(fp8, recipe, M):
+    N, K = 136, 256
+    a, b = workloads.normal_bf16((M, K), 4, "a"), workloads.normal_bf16((N, K), 4, "b")
+    A, B, _, _ = operands(fp8, recipe, a, b, E4M3, E4M3)
+    want, _ = product(fp8, recipe)(A, B)
+    A.q[1, 5] = 0x7F  # a NaN code
+    got, _ = product(fp8, recipe)(A, B)
+    torch.cuda.synchronize()
+    keep = [i for i in range(M) if i != 1]
+    assert bool(got[1].isnan().all()) and torch.equal(got[keep], want[keep])
+
+
+def test_refusals(fp8):
+    import ctypes
+    E = fp8.binding.ERR_INVALID_ARG
+    M, N, K = 8, 64, 256
+    A = fp8.quantize(torch.zeros(M, K, dtype=torch.bfloat16, device="cuda"), E4M3)
+    B = fp8.quantize(torch.zeros(N, K, dtype=torch.bfloat16, device="cuda"), E4M3)
+    buf = torch.zeros(8 * M * N, dtype=torch.bfloat16, device="cuda")
+    p = buf.data_ptr()
+    vp = ctypes.c_void_p
+    L = fp8.lib()
+    oa, ob = A.operand(), B.operand()
+    out, aux, bias, res = p, p + 2 * M * N, p + 4 * M * N, p + 6 * M * N
+
+    def call(M=M, N=N, K=K, bias=bias, act=0, res=res, ldr=N, acc=0, out=out, aux=None):
+        return L.fp8_gemm_linear(M, N, K, ctypes.byref(oa), ctypes.byref(ob), vp(bias), act, vp(res), ldr, acc, vp(out),
+                                 vp(aux), None)
+
+    assert call() == 0
+    for bad in (dict(M=0), dict(N=0), dict(K=200), dict(act=2), dict(bias=bias + 2), dict(out=None), dict(out=out + 8),
+                dict(ldr=N - 1), dict(res=res + 1), dict(acc=2), dict(aux=aux), dict(act=1, aux=out),
+                dict(act=1, aux=aux + 8), dict(res=out + 16), dict(res=out, ldr=N + 1), dict(act=1, aux=aux, res=aux)):
+        assert call(**bad) == E, bad
+    torch.cuda.synchronize()
+    with pytest.raises(AssertionError):
+        fp8.gemm_linear(A, B, want_aux=True)
+    with pytest.raises(AssertionError):
+        fp8.gemm_linear(A, B, residual=torch.zeros(N, M, dtype=torch.bfloat16, device="cuda").t())
