@@ -10,7 +10,9 @@
 #include <cuda_runtime.h>
 
 #include "fp8ll.h"
+#include "gemm_rows.h"
 #include "internal.h"
+#include "rmsnorm.h"
 
 namespace fp8ll {
 
@@ -306,6 +308,8 @@ struct LinearArgs {
     void* aux;
 };
 
+static bool valid_k(int64_t K) { return K >= 128 && K % 128 == 0 && K < (1LL << 31); }
+
 static bool valid_linear(int64_t M, int64_t N, const LinearArgs& a) {
     if (!valid_mn(M, N)) return false;
     if (a.act != FP8LL_ACT_NONE && a.act != FP8LL_ACT_GELU) return false;
@@ -322,6 +326,28 @@ static bool valid_linear(int64_t M, int64_t N, const LinearArgs& a) {
         if (a.aux && overlaps(a.residual, rbytes, a.aux, M * N * 2)) return false;
     }
     return true;
+}
+
+// the kernel for few rows: the parameters all recipes share (its MMAs take the
+// weights as their M side, so B's format comes first in the descriptor)
+static RowsParams rows_params(int64_t M, int64_t N, int64_t K, int fmt_a, int fmt_b, const LinearArgs& a,
+                              const DeviceInfo* dev) {
+    RowsParams p = {};
+    p.M = static_cast<int32_t>(M);
+    p.N = static_cast<int32_t>(N);
+    p.nkb = static_cast<int32_t>(K / 128);
+    p.idesc = (static_cast<uint32_t>(fmt_b) << 7) | (static_cast<uint32_t>(fmt_a) << 10) | ((128u >> 4) << 24);
+    p.gelu = a.act == FP8LL_ACT_GELU;
+    p.status = dev->status;
+    const int starve = g_starve_ms.exchange(0);
+    p.debug_starve = starve > 0;
+    p.budget_ns = starve > 0 ? static_cast<uint64_t>(starve) * 1000000ull : kDefaultBudgetNs;
+    p.bias = static_cast<const uint16_t*>(a.bias);
+    p.res = static_cast<const uint16_t*>(a.residual);
+    p.ldr = a.ldr;
+    p.out = static_cast<uint16_t*>(a.out);
+    p.aux = static_cast<uint16_t*>(a.aux);
+    return p;
 }
 
 static int fill_linear(const LinearArgs& a, GemmParams& p) {
@@ -944,12 +970,22 @@ int fp8_gemm_linear(int64_t M, int64_t N, int64_t K, const fp8ll_operand_t* A, c
                     const void* bias_bf16, int act, const void* residual_bf16, int64_t ldr, int acc_mode,
                     void* out_bf16, void* aux_bf16, fp8ll_stream_t stream) {
     const LinearArgs args{bias_bf16, act, residual_bf16, ldr, out_bf16, aux_bf16};
-    if (!valid_linear(M, N, args) || K < 128 || K % 128 != 0 || K >= (1LL << 36)) return FP8LL_ERR_INVALID_ARG;
+    if (!valid_linear(M, N, args) || !valid_k(K)) return FP8LL_ERR_INVALID_ARG;
     if (acc_mode != FP8LL_ACC_FULL && acc_mode != FP8LL_ACC_FAST) return FP8LL_ERR_INVALID_ARG;
     if (!valid_operand(A, M, K) || !valid_operand(B, N, K)) return FP8LL_ERR_INVALID_ARG;
     DeviceInfo* dev = nullptr;
     int rc = current_device(&dev);
     if (rc != FP8LL_OK) return rc;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (rows_kernel_taken(M, N, K, dev->num_sms)) {
+        RowsParams r = rows_params(M, N, K, A->fmt, B->fmt, args, dev);
+        r.idesc |= 1u << 4;  // fp32 accumulators
+        RowsMaps rm;
+        if (!encode_operand(B, N, K, kRowsFeatures, &rm.w, &rm.sw) ||
+            !encode_operand(A, M, K, static_cast<uint32_t>(rows_tokens(M)), &rm.x, &rm.sx))
+            return FP8LL_ERR_LAUNCH;
+        return launch_gemm_rows(rm, r, kRecipeBlock, s, dev->num_sms) == 0 ? FP8LL_OK : FP8LL_ERR_LAUNCH;
+    }
     TensorMaps maps;
     if (!encode_operand(A, M, K, 128, &maps.a, &maps.sa) || !encode_operand(B, N, K, kTileN, &maps.b, &maps.sb))
         return FP8LL_ERR_LAUNCH;
@@ -965,7 +1001,6 @@ int fp8_gemm_linear(int64_t M, int64_t N, int64_t K, const fp8ll_operand_t* A, c
         if (!encode_z(residual_bf16, M, N, ldr, &maps.z)) return FP8LL_ERR_LAUNCH;
         p.z_tma = 1;
     }
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     rc = epi >= kEpiLinear ? launch_gemm_linear(maps, p, epi, s, grid_for(p, dev))
                            : launch_gemm_fprop(maps, p, epi, s, grid_for(p, dev));
     return rc == 0 ? FP8LL_OK : FP8LL_ERR_LAUNCH;
@@ -979,7 +1014,25 @@ int fp8_mx_gemm_linear(int64_t M, int64_t N, int64_t K, const fp8ll_mx_operand_t
     TensorMaps maps;
     GemmParams p;
     DeviceInfo* dev = nullptr;
-    int rc = mx_setup(M, N, K, A, B, maps, p, &dev);
+    if (!valid_k(K) || !valid_mx_operand(A, M, K) || !valid_mx_operand(B, N, K)) return FP8LL_ERR_INVALID_ARG;
+    int rc = current_device(&dev);
+    if (rc != FP8LL_OK) return rc;
+    if (rows_kernel_taken(M, N, K, dev->num_sms)) {
+        RowsParams r = rows_params(M, N, K, A->fmt, B->fmt, args, dev);
+        r.idesc |= 1u << 23;  // UE8M0 scales
+        r.groups_w = mx_sf_groups(N);
+        r.groups_x = mx_sf_groups(M);
+        RowsMaps rm;
+        if (!encode_codes(B->q, B->ld_q, N, K, kRowsFeatures, &rm.w) ||
+            !encode_codes(A->q, A->ld_q, M, K, static_cast<uint32_t>(rows_tokens(M)), &rm.x) ||
+            !encode_sf_atoms(B->sf, (K / 128) * r.groups_w, 1, &rm.sw) ||
+            !encode_sf_atoms(A->sf, (K / 128) * r.groups_x, 1, &rm.sx))
+            return FP8LL_ERR_LAUNCH;
+        return launch_gemm_rows(rm, r, kRecipeMx, reinterpret_cast<cudaStream_t>(stream), dev->num_sms) == 0
+                   ? FP8LL_OK
+                   : FP8LL_ERR_LAUNCH;
+    }
+    rc = mx_setup(M, N, K, A, B, maps, p, &dev);
     if (rc != FP8LL_OK) return rc;
     const int epi = fill_linear(args, p);
     return launch_gemm_mx(maps, p, epi, reinterpret_cast<cudaStream_t>(stream)) == 0 ? FP8LL_OK : FP8LL_ERR_LAUNCH;
@@ -993,7 +1046,23 @@ int fp8_tensor_gemm_linear(int64_t M, int64_t N, int64_t K, const fp8ll_tensor_o
     TensorMaps maps;
     GemmParams p;
     DeviceInfo* dev = nullptr;
-    int rc = tensor_setup(M, N, K, A, B, maps, p, &dev);
+    if (!valid_k(K) || !valid_tensor_operand(A, M, K) || !valid_tensor_operand(B, N, K)) return FP8LL_ERR_INVALID_ARG;
+    int rc = current_device(&dev);
+    if (rc != FP8LL_OK) return rc;
+    if (rows_kernel_taken(M, N, K, dev->num_sms)) {
+        RowsParams r = rows_params(M, N, K, A->fmt, B->fmt, args, dev);
+        r.idesc |= 1u << 4;  // fp32 accumulators
+        r.tsw = B->scale;
+        r.tsx = A->scale;
+        RowsMaps rm = {};
+        if (!encode_codes(B->q, B->ld_q, N, K, kRowsFeatures, &rm.w) ||
+            !encode_codes(A->q, A->ld_q, M, K, static_cast<uint32_t>(rows_tokens(M)), &rm.x))
+            return FP8LL_ERR_LAUNCH;
+        return launch_gemm_rows(rm, r, kRecipeTensor, reinterpret_cast<cudaStream_t>(stream), dev->num_sms) == 0
+                   ? FP8LL_OK
+                   : FP8LL_ERR_LAUNCH;
+    }
+    rc = tensor_setup(M, N, K, A, B, maps, p, &dev);
     if (rc != FP8LL_OK) return rc;
     const int epi = fill_linear(args, p);
     return launch_gemm_tensor(maps, p, epi, reinterpret_cast<cudaStream_t>(stream)) == 0 ? FP8LL_OK

@@ -1,0 +1,63 @@
+// gemm_rows.h -- host interface of the linear GEMM for few rows of A.
+#pragma once
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+namespace fp8ll {
+
+constexpr int kRowsFeatures = 128;  // rows of B per output tile: the MMA's M
+
+// tokens (rows of A) per output tile: the MMA's N
+inline int rows_tokens(int64_t M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128; }
+
+// CTAs that share the K blocks of an output tile: as many as run at once (two
+// per SM, one at 128 tokens) with two blocks each, at most 8
+inline int rows_cluster(int64_t M, int64_t N, int64_t nkb, int num_sms) {
+    const int nt = rows_tokens(M);
+    const int64_t tiles = (N + kRowsFeatures - 1) / kRowsFeatures * ((M + nt - 1) / nt);
+    const int64_t slots = static_cast<int64_t>(num_sms) * (nt == 128 ? 1 : 2);
+    int c = 1;
+    while (c < 8 && tiles * 2 * c <= slots && nkb >= 4 * c) c *= 2;
+    return c;
+}
+
+// Whether this kernel is taken.  Up to 64 tokens always (1x128 / MXFP8 at 64
+// tokens: 17.6 / 16.5 us against the tile kernels' 24.2 / 18.5 at 14336 features
+// over 4096, 17.6 / 16.7 against 69.7 / 44.2 at 4096 over 14336).  Beyond that
+// where a K split shortens the chain of blocks that few tiles would leave to
+// few SMs: 256 x 2112 over 7168 takes 15.3 / 12.4 us against 37.3 / 25.0, 256 x
+// 4096 over 14336 40.1 / 30.4 against 70.5 / 44.7; a split in two of a short K
+// does not pay (256 x 4096 over 1024: 11.4 / 10.2 against 9.4 / 8.5).
+inline bool rows_kernel_taken(int64_t M, int64_t N, int64_t K, int num_sms) {
+    if (M <= 64) return true;
+    const int c = rows_cluster(M, N, K / 128, num_sms);
+    return c >= 4 || (c == 2 && K / 128 >= 32);
+}
+
+struct RowsMaps {
+    CUtensorMap w, x;    // codes: boxes of 128 rows of B, of rows_tokens(M) rows of A, 128 bytes each
+    CUtensorMap sw, sx;  // 1x128: their scales, one K block; MXFP8: one 512-byte scale atom
+};
+
+struct RowsParams {
+    int32_t M, N, nkb;
+    int32_t cluster;        // CTAs that share the K blocks of an output tile (set by the launcher)
+    uint32_t idesc;         // tcgen05 instruction descriptor without the MMA's N
+    int32_t gelu;
+    int32_t debug_starve;   // test hook: the producer issues no loads
+    uint64_t budget_ns;     // wall-clock budget of each pipeline wait
+    int* status;
+    int64_t groups_w, groups_x;  // MXFP8: 128-row groups per K block of the scale arrays
+    const float* tsw;       // per tensor: the scales
+    const float* tsx;
+    const uint16_t* bias;   // bf16 [N] or null
+    const uint16_t* res;    // bf16 [M][ldr] or null
+    int64_t ldr;
+    uint16_t* out;          // bf16 [M][N]
+    uint16_t* aux;          // bf16 [M][N] or null
+};
+
+int launch_gemm_rows(const RowsMaps& maps, RowsParams p, int recipe, cudaStream_t stream, int num_sms);
+
+}  // namespace fp8ll

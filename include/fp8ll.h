@@ -423,7 +423,7 @@ enum { FP8LL_F32 = 0, FP8LL_BF16 = 1 };
 
 /* Matrix product with bias, activation and residual in its epilogue:
  *   Z = A B^T + bias;  Y = act(Z) + residual     (fp32, rounded once to bf16)
- *   A, B, M, N, K, acc_mode: as fp8_gemm_fprop (M, N >= 1, any value).
+ *   A, B, M, N, K, acc_mode: as fp8_gemm_fprop (M, N >= 1, any value; K < 2^31).
  *   bias_bf16:     [N], 16-byte aligned, or NULL.
  *   residual_bf16: [M][ldr], 2-byte aligned, ldr >= N, or NULL.  It may be the
  *                  output's own buffer when ldr == N, else they must not overlap.
@@ -432,8 +432,9 @@ enum { FP8LL_F32 = 0, FP8LL_BF16 = 1 };
  *                  with FP8LL_ACT_NONE.
  * The gradient of act = GELU is fp8_gemm_dgrad's epilogue (with this Z); the
  * residual's gradient is dY itself; dX = dZ W + dX_residual is this call again.
- * A product of few rows runs a kernel of its own that streams B once through
- * all SMs, so its sums are ordered differently from fp8_gemm_fprop's. */
+ * Products of few rows, or of too few output tiles for the SMs, run a kernel of
+ * its own that splits K, so their sums are ordered differently from
+ * fp8_gemm_fprop's.  Which kernel runs depends on the sizes and the device only. */
 int fp8_gemm_linear(int64_t M, int64_t N, int64_t K, const fp8ll_operand_t* A, const fp8ll_operand_t* B,
                     const void* bias_bf16, int act, const void* residual_bf16, int64_t ldr, int acc_mode,
                     void* out_bf16, void* aux_bf16, fp8ll_stream_t stream);

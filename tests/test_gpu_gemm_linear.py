@@ -59,7 +59,7 @@ def check(y, z, acc, S, bias, act, residual):
 
 
 SHAPES = [(1, 1, 128), (1, 256, 4096), (2, 40, 256), (3, 1000, 896), (8, 129, 1280), (9, 72, 2048), (16, 512, 7168),
-          (17, 264, 384), (33, 2110, 512), (64, 96, 1024), (100, 301, 640), (129, 264, 256), (300, 520, 384)]
+          (17, 264, 384), (33, 2110, 512), (64, 96, 1024), (100, 301, 640), (129, 264, 256), (300, 520, 384), (150, 200, 4096), (257, 129, 2048), (128, 1030, 4096)]
 
 
 @pytest.mark.parametrize("recipe", RECIPES)
@@ -85,7 +85,7 @@ def test_epilogues(fp8, recipe, M, N, K):
 
 
 @pytest.mark.parametrize("recipe", RECIPES)
-@pytest.mark.parametrize("M,N", [(5, 264), (5, 263), (200, 264), (200, 262), (200, 263)])
+@pytest.mark.parametrize("M,N", [(5, 264), (5, 263), (200, 264), (200, 263), (3000, 264), (3000, 262), (3000, 263)])
 def test_residual_strides_and_in_place(fp8, recipe, M, N):
     K = 384
     a = workloads.normal_bf16((M, K), 5, "a")
@@ -113,7 +113,7 @@ def test_residual_strides_and_in_place(fp8, recipe, M, N):
 @pytest.mark.parametrize("recipe", RECIPES)
 def test_without_a_residual_it_is_the_forward_product(fp8, recipe):
     # large enough for the tile kernel: the same kernel, the same bits
-    M, N, K = 384, 520, 512
+    M, N, K = 1000, 2048, 512
     a, b = workloads.normal_bf16((M, K), 9, "a"), workloads.normal_bf16((N, K), 9, "b", std=0.05)
     bias = workloads.normal_bf16((N,), 9, "bias").cuda()
     A, B, _, _ = operands(fp8, recipe, a, b, E4M3, E4M3)
@@ -182,3 +182,41 @@ def test_refusals(fp8):
         fp8.gemm_linear(A, B, want_aux=True)
     with pytest.raises(AssertionError):
         fp8.gemm_linear(A, B, residual=torch.zeros(N, M, dtype=torch.bfloat16, device="cuda").t())
+
+
+@pytest.mark.parametrize("recipe", RECIPES)
+@pytest.mark.parametrize("M", [5, 100, 3000])
+def test_a_starved_pipeline_times_out_and_writes_nothing(fp8, recipe, M):
+    N, K = 264, 1024
+    a, b = workloads.normal_bf16((M, K), 6, "a"), workloads.normal_bf16((N, K), 6, "b")
+    A, B, _, _ = operands(fp8, recipe, a, b, E4M3, E4M3)
+    res = torch.ones((M, N), dtype=torch.bfloat16, device="cuda")
+    want, _ = product(fp8, recipe)(A, B, None, fp8.ACT_NONE, res)
+    torch.cuda.synchronize()
+    out = torch.full((M, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    fp8.debug_starve_next_gemm(20)
+    product(fp8, recipe)(A, B, None, fp8.ACT_NONE, res, out=out)
+    torch.cuda.synchronize()
+    assert fp8.device_status() == fp8.binding.ERR_TIMEOUT and bool((out == 7.0).all())
+    got, _ = product(fp8, recipe)(A, B, None, fp8.ACT_NONE, res)
+    torch.cuda.synchronize()
+    assert fp8.device_status() == 0 and torch.equal(got, want)
+
+
+@pytest.mark.parametrize("recipe", RECIPES)
+@pytest.mark.parametrize("N,K", [(128, 16384), (256, 2048), (1000, 7168), (20000, 256)])
+def test_few_rows_split_over_k_the_same_way_every_time(fp8, recipe, N, K):
+    M = 6
+    a, b = workloads.normal_bf16((M, K), 8, "a"), workloads.normal_bf16((N, K), 8, "b", std=0.05)
+    A, B, acc, S = operands(fp8, recipe, a, b, E4M3, E4M3)
+    first, _ = product(fp8, recipe)(A, B)
+    again, _ = product(fp8, recipe)(A, B)
+    torch.cuda.synchronize()
+    check(first, None, acc, S, None, 0, None)
+    assert torch.equal(first, again)
+    # a token's outputs do not depend on the others beside it
+    one = {"block": lambda: fp8.quantize(a[3:4].cuda(), E4M3), "mx": lambda: fp8.mx_quantize(a[3:4].cuda(), E4M3),
+           "tensor": lambda: fp8.Fp8TensorScaled(A.q[3:4], A.scale, E4M3)}[recipe]()
+    alone, _ = product(fp8, recipe)(one, B)
+    torch.cuda.synchronize()
+    assert torch.equal(alone, first[3:4]) and fp8.device_status() == 0
