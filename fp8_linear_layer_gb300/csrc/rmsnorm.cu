@@ -10,11 +10,10 @@
 // before any bf16 rounding, so an element is rounded once.
 //
 // Rows kernel: one row per CTA at a time, T threads with V 16-byte vectors of
-// the row each, held as packed bf16 between the sum of squares and the cast.
-// 16 neighbouring threads hold one 128-block, so block and MX maxima are
-// shuffles.  Columns kernel: 128 x 128 tiles of h staged in shared memory as
-// the transposed casts do it, with the row's rstd and the column's gamma
-// applied on the way to the codes.
+// the row each, held as packed bf16 between the sum of squares and the cast;
+// the next row is loaded meanwhile.  16 neighbouring threads hold one
+// 128-block, so block and MX maxima are shuffles.  Columns kernel: reads h
+// again, while much of it is in L2, and casts it down its columns.
 #include <cuda_runtime.h>
 
 #include "common.cuh"
@@ -53,186 +52,319 @@ __device__ __forceinline__ float block_sum(float v, float* part) {
     return s;
 }
 
-template <int FMT, int RECIPE, int V>
-__global__ void __launch_bounds__(1024) rmsnorm_rows_kernel(const __grid_constant__ RmsNormParams p) {
+// y = fl(fl(h rstd) gamma) of eight packed bf16 values, as four pairs
+__device__ __forceinline__ void norm8(const uint4& h, const uint4& g, uint64_t rstd2, uint64_t (&y)[4]) {
+    const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, gw[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        y[i] = mul_f32x2(mul_f32x2(pack_f32x2(bf16_lo(hw[i]), bf16_hi(hw[i])), rstd2),
+                         pack_f32x2(bf16_lo(gw[i]), bf16_hi(gw[i])));
+}
+
+__device__ __forceinline__ float amax8(const uint64_t (&y)[4]) {
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 v = unpack_f32x2(y[i]);
+        m = fmaxf(m, fmaxf(fabsf(v.x), fabsf(v.y)));
+    }
+    return m;
+}
+
+template <int FMT>
+__device__ __forceinline__ uint2 encode8_pairs(const uint64_t (&y)[4], float inv) {
+    const uint64_t inv2 = pack_f32x2(inv, inv);
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 v = unpack_f32x2(mul_f32x2(y[i], inv2));
+        w[i] = Fp8Fmt<FMT>::cvt2(v.x, v.y);
+    }
+    return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+}
+
+// max|y| over the block into *amax_out, one atomic per block: non-negative
+// floats order like their bits, and a maximum does not depend on the order
+__device__ __forceinline__ void fold_amax(float top, float* part, float* amax_out) {
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    __syncthreads();  // part's last use as sums is over
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = top;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < static_cast<int>(blockDim.x >> 5); ++w) top = fmaxf(top, part[w]);
+        atomicMax(reinterpret_cast<unsigned*>(amax_out), __float_as_uint(top));
+    }
+}
+
+// GREG: gamma stays in registers for all rows of the CTA
+template <int FMT, int RECIPE, int V, int MAXT, bool GREG>
+__global__ void __launch_bounds__(MAXT) rmsnorm_rows_kernel(const __grid_constant__ RmsNormParams p) {
     __shared__ float part[2][32];
     const int nv = static_cast<int>(p.cols / 8);
     const int T = blockDim.x;
+    const int lane = threadIdx.x & 31;
     const int64_t mx_groups = 2 * ((p.rows + 255) / 256);
-    // MXFP8: the scale bytes of rows beyond the matrix hold 127
-    const int64_t all_rows = RECIPE == kRecipeMx && p.qr ? mx_groups * 128 : p.rows;
     float inv_t = 1.0f, s_t = 1.0f, top = 0.0f;
     if (RECIPE == kRecipeTensor) {
         block_scale<FMT>(*p.amax_in, inv_t, s_t);
         if (blockIdx.x == 0 && threadIdx.x == 0) *p.scale = s_t;
     }
-    int k = 0;
-    for (int64_t r = blockIdx.x; r < all_rows; r += gridDim.x, ++k) {
-        if (RECIPE == kRecipeMx && r >= p.rows) {
-            for (int64_t i = threadIdx.x; i < p.cols / 32; i += T)
-                p.sfr[mx_sf_offset(i >> 2, mx_groups, r, static_cast<int>(i & 3))] = 127;
-            continue;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    uint4 xv[V], rv[V];  // the next row, loaded while the current one is reduced and cast
+    auto fetch = [&](int64_t r) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int i = threadIdx.x + v * T;
+            const bool in = i < nv && r < p.rows;
+            xv[v] = in ? __ldcs(reinterpret_cast<const uint4*>(p.x + r * p.ldx + 8 * i)) : zero;
+            rv[v] = in && p.residual ? __ldcs(reinterpret_cast<const uint4*>(p.residual + r * p.ldr + 8 * i)) : zero;
         }
+    };
+    auto load_gamma = [&](int v) {
+        const int i = threadIdx.x + v * T;
+        return i < nv ? __ldg(reinterpret_cast<const uint4*>(p.gamma + 8 * i)) : zero;
+    };
+    int64_t r = blockIdx.x;
+    fetch(r);
+    uint4 gv[GREG ? V : 1];
+    if (GREG) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) gv[v] = load_gamma(v);
+    }
+    for (int k = 0; r < p.rows; r += gridDim.x, ++k) {
         uint4 hv[V];
         float sq = 0.0f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int i = threadIdx.x + v * T;
-            hv[v] = make_uint4(0, 0, 0, 0);
-            if (i < nv) {
-                hv[v] = *reinterpret_cast<const uint4*>(p.x + r * p.ldx + 8 * i);
-                if (p.residual) {
-                    const uint4 rv = *reinterpret_cast<const uint4*>(p.residual + r * p.ldr + 8 * i);
-                    float a[8], b[8];
-                    unpack8(hv[v], a);
-                    unpack8(rv, b);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) a[e] += b[e];
-                    hv[v] = pack8(a);
-                }
-                if (p.h) *reinterpret_cast<uint4*>(p.h + r * p.cols + 8 * i) = hv[v];
-            }
+            hv[v] = xv[v];
             float f[8];
             unpack8(hv[v], f);
+            if (p.residual) {
+                float b[8];
+                unpack8(rv[v], b);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[e] += b[e];
+                hv[v] = pack8(f);
+                unpack8(hv[v], f);
+            }
+            if (p.h && i < nv) *reinterpret_cast<uint4*>(p.h + r * p.cols + 8 * i) = hv[v];
 #pragma unroll
             for (int e = 0; e < 8; ++e) sq = fmaf(f[e], f[e], sq);
         }
+        fetch(r + gridDim.x);
         sq = block_sum(sq, part[k & 1]);
         const float rstd = rsqrtf(__fdiv_rn(sq, static_cast<float>(p.cols)) + p.eps);
         if (threadIdx.x == 0) p.rstd[r] = rstd;
-        if (!p.qr && !p.y && !(RECIPE == kRecipeTensor && p.amax_out)) continue;
+        const uint64_t rstd2 = pack_f32x2(rstd, rstd);
+        uint64_t y[V][4];
+        float amax[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            norm8(hv[v], GREG ? gv[GREG ? v : 0] : load_gamma(v), rstd2, y[v]);
+            amax[v] = amax8(y[v]);  // 0 beyond the row
+            if (RECIPE == kRecipeTensor) top = fmaxf(top, amax[v]);
+        }
+        if (p.y) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int i = threadIdx.x + v * T;
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 f = unpack_f32x2(y[v][e]);
+                    w[e] = pack_bf16x2(f.x, f.y);
+                }
+                if (i < nv) *reinterpret_cast<uint4*>(p.y + r * p.cols + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+        if (!p.qr) continue;
+        float inv[V];
+        if (RECIPE == kRecipeTensor) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) inv[v] = inv_t;
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                amax[v] = fmaxf(amax[v], __shfl_xor_sync(0xffffffffu, amax[v], 1));
+                amax[v] = fmaxf(amax[v], __shfl_xor_sync(0xffffffffu, amax[v], 2));
+            }
+        }
+        if (RECIPE == kRecipeMx) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int i = threadIdx.x + v * T;
+                const int e = mx_exponent<FMT>(amax[v]);
+                inv[v] = mx_inverse_scale(e);
+                if (i < nv && (i & 3) == 0)
+                    p.sfr[mx_sf_offset(i >> 4, mx_groups, r, (i >> 2) & 3)] = static_cast<uint8_t>(e + 127);
+            }
+        }
+        if (RECIPE == kRecipeBlock) {
+            // lane j of a 16-lane group divides for vector j % V only, and hands the factor to the others
+            float mine = amax[0];
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                amax[v] = fmaxf(amax[v], __shfl_xor_sync(0xffffffffu, amax[v], 4));
+                amax[v] = fmaxf(amax[v], __shfl_xor_sync(0xffffffffu, amax[v], 8));
+                if (v == 0 || (lane & (V - 1)) == v) mine = amax[v];
+            }
+            float inv_mine, s_mine;
+            block_scale<FMT>(mine, inv_mine, s_mine);
+            const int vm = lane & (V - 1);
+            const int im = threadIdx.x + vm * T;
+            if ((lane & 15) < V && im < nv) p.sr[(im >> 4) * p.sldr + r] = s_mine;
+#pragma unroll
+            for (int v = 0; v < V; ++v) inv[v] = __shfl_sync(0xffffffffu, inv_mine, (lane & 16) + v);
+        }
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int i = threadIdx.x + v * T;
-            const bool in = i < nv;
-            float f[8], g[8];
-            unpack8(hv[v], f);
-            unpack8(in ? __ldg(reinterpret_cast<const uint4*>(p.gamma + 8 * i)) : make_uint4(0, 0, 0, 0), g);
-            float amax = 0.0f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                f[e] = __fmul_rn(__fmul_rn(f[e], rstd), g[e]);
-                amax = fmaxf(amax, fabsf(f[e]));
-            }
-            if (p.y && in) *reinterpret_cast<uint4*>(p.y + r * p.cols + 8 * i) = pack8(f);
-            if (RECIPE == kRecipeTensor) {
-                if (in) top = fmaxf(top, amax);
-                if (p.qr && in) *reinterpret_cast<uint2*>(p.qr + r * p.cols + 8 * i) = encode8<FMT>(f, inv_t);
-            } else if (p.qr) {
-                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-                float inv, s;
-                if (RECIPE == kRecipeBlock) {
-                    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 4));
-                    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 8));
-                    block_scale<FMT>(amax, inv, s);
-                    if (in && (i & 15) == 0) p.sr[(i >> 4) * p.sldr + r] = s;
-                } else {
-                    const int e = mx_exponent<FMT>(amax);
-                    inv = mx_inverse_scale(e);
-                    if (in && (i & 3) == 0)
-                        p.sfr[mx_sf_offset(i >> 4, mx_groups, r, (i >> 2) & 3)] = static_cast<uint8_t>(e + 127);
-                }
-                if (in) *reinterpret_cast<uint2*>(p.qr + r * p.cols + 8 * i) = encode8<FMT>(f, inv);
-            }
+            if (i < nv) __stcs(reinterpret_cast<uint2*>(p.qr + r * p.cols + 8 * i), encode8_pairs<FMT>(y[v], inv[v]));
         }
     }
-    if (RECIPE == kRecipeTensor && p.amax_out) {
+    if (RECIPE == kRecipeMx && p.qr) {
+        // the scale bytes of rows beyond the matrix hold 127
+        for (r = p.rows + blockIdx.x; r < mx_groups * 128; r += gridDim.x)
+            for (int64_t i = threadIdx.x; i < p.cols / 128; i += T)
+                *reinterpret_cast<uint32_t*>(p.sfr + mx_sf_offset(i, mx_groups, r, 0)) = 0x7F7F7F7Fu;
+    }
+    if (RECIPE == kRecipeTensor && p.amax_out) fold_amax(top, part[0], p.amax_out);
+}
+
+// Column codes of y from h, rstd and gamma, in 128 x 128 tiles of h staged in
+// shared memory as the transposed casts do it (each 32-row band rotated by eight
+// words): persistent CTAs with two staged tiles, the next one on its way by
+// cp.async while one is cast.  Thread t takes the column pair t / 4 and the
+// 32-row part t % 4.  |y| = fl(fl(|h| rstd) |gamma|) grows with fl(|h| rstd), so
+// a column's maximum needs one product per element and gamma once.
+constexpr int kColsCtas = 3;
+struct ColsStage {
+    uint32_t tile[128][64];
+    float rstd[4][36];  // part p's 32 rows, banks apart
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+template <int FMT, int RECIPE>
+__global__ void __launch_bounds__(256, kColsCtas) rmsnorm_cols_kernel(const __grid_constant__ RmsNormParams p) {
+    extern __shared__ __align__(16) uint8_t stage_raw[];
+    ColsStage* stage = reinterpret_cast<ColsStage*>(stage_raw);
+    const uint16_t* h = p.h ? p.h : p.x;
+    const int64_t ldh = p.h ? p.cols : p.ldx;
+    const int64_t ncb = p.cols / 128, ntiles = (p.rows / 128) * ncb;
+    // the last rows first: the rows kernel left them in L2
+    float inv_t = 1.0f, s_t = 1.0f;
+    if (RECIPE == kRecipeTensor) block_scale<FMT>(*p.amax_in, inv_t, s_t);
+    auto fetch = [&](int64_t t, int buf) {
+        const int64_t q = ntiles - 1 - t, rb = q / ncb, r0 = rb * 128, c0 = (q - rb * ncb) * 128;
 #pragma unroll
-        for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-        // non-negative floats order like their bits; a maximum does not depend on the order
-        if ((threadIdx.x & 31) == 0) atomicMax(reinterpret_cast<unsigned*>(p.amax_out), __float_as_uint(top));
+        for (int it = 0; it < 8; ++it) {
+            const int i = threadIdx.x + it * 256;
+            const int rr = i >> 4, ch = i & 15;
+            cp_async16(smem_addr(&stage[buf].tile[rr][(ch * 4 + 8 * (rr >> 5)) & 63]), h + (r0 + rr) * ldh + c0 + ch * 8);
+        }
+        if (threadIdx.x < 32)
+            cp_async16(smem_addr(&stage[buf].rstd[threadIdx.x >> 3][4 * (threadIdx.x & 7)]),
+                       p.rstd + r0 + 4 * threadIdx.x);
+    };
+    const int cp = threadIdx.x >> 2, part = threadIdx.x & 3;
+    const int wcol = (cp + 8 * part) & 63;
+    int64_t t = blockIdx.x;
+    if (t < ntiles) fetch(t, 0);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    for (int k = 0; t < ntiles; ++k, t += gridDim.x) {
+        const ColsStage& st = stage[k & 1];
+        __syncthreads();  // every thread is done with the tile that the next one replaces
+        if (t + gridDim.x < ntiles) fetch(t + gridDim.x, (k + 1) & 1);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        __syncthreads();
+        const int64_t q = ntiles - 1 - t, rb = q / ncb, r0 = rb * 128, c0 = (q - rb * ncb) * 128;
+        const int64_t c = c0 + 2 * cp;
+        const uint32_t gw = __ldg(reinterpret_cast<const unsigned int*>(p.gamma + c));
+        const float g_lo = bf16_lo(gw), g_hi = bf16_hi(gw);
+        float inv_lo = inv_t, inv_hi = inv_t, s_lo, s_hi;
+        if (RECIPE != kRecipeTensor) {
+            float a_lo = 0.0f, a_hi = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const uint32_t w = st.tile[32 * part + i][wcol];
+                const float s = st.rstd[part][i];
+                const float2 v = unpack_f32x2(mul_f32x2(pack_f32x2(bf16_lo(w), bf16_hi(w)), pack_f32x2(s, s)));
+                a_lo = fmaxf(a_lo, fabsf(v.x));
+                a_hi = fmaxf(a_hi, fabsf(v.y));
+            }
+            a_lo = __fmul_rn(a_lo, fabsf(g_lo));
+            a_hi = __fmul_rn(a_hi, fabsf(g_hi));
+            if (RECIPE == kRecipeBlock) {
+#pragma unroll
+                for (int off = 1; off <= 2; off <<= 1) {
+                    a_lo = fmaxf(a_lo, __shfl_xor_sync(0xffffffffu, a_lo, off));
+                    a_hi = fmaxf(a_hi, __shfl_xor_sync(0xffffffffu, a_hi, off));
+                }
+                // even parts divide for the even column, odd parts for the odd one
+                float inv_mine, s_mine;
+                block_scale<FMT>(part & 1 ? a_hi : a_lo, inv_mine, s_mine);
+                const float other = __shfl_xor_sync(0xffffffffu, inv_mine, 1);
+                inv_lo = part & 1 ? other : inv_mine;
+                inv_hi = part & 1 ? inv_mine : other;
+                if (part < 2) p.sc[rb * p.sldc + c + part] = s_mine;
+            } else {
+                const int e_lo = mx_exponent<FMT>(a_lo), e_hi = mx_exponent<FMT>(a_hi);
+                inv_lo = mx_inverse_scale(e_lo);
+                inv_hi = mx_inverse_scale(e_hi);
+                const int64_t groups = 2 * ((p.cols + 255) / 256);
+                p.sfc[mx_sf_offset(rb, groups, c, part)] = static_cast<uint8_t>(e_lo + 127);
+                p.sfc[mx_sf_offset(rb, groups, c + 1, part)] = static_cast<uint8_t>(e_hi + 127);
+                // an odd number of 128-column groups: the group beyond the matrix holds 127
+                if (c0 + 128 == p.cols && (p.cols & 255) != 0 && threadIdx.x < 128)
+                    *reinterpret_cast<uint32_t*>(p.sfc + mx_sf_offset(rb, groups, p.cols + threadIdx.x, 0)) =
+                        0x7F7F7F7Fu;
+            }
+        }
+        const uint64_t g2 = pack_f32x2(g_lo, g_hi), inv2 = pack_f32x2(inv_lo, inv_hi);
+        uint32_t wl[8], wh[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float2 v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t w = st.tile[32 * part + 4 * i + j][wcol];
+                const float s = st.rstd[part][4 * i + j];
+                v[j] = unpack_f32x2(mul_f32x2(
+                    mul_f32x2(mul_f32x2(pack_f32x2(bf16_lo(w), bf16_hi(w)), pack_f32x2(s, s)), g2), inv2));
+            }
+            wl[i] = Fp8Fmt<FMT>::cvt2(v[0].x, v[1].x) | (static_cast<uint32_t>(Fp8Fmt<FMT>::cvt2(v[2].x, v[3].x)) << 16);
+            wh[i] = Fp8Fmt<FMT>::cvt2(v[0].y, v[1].y) | (static_cast<uint32_t>(Fp8Fmt<FMT>::cvt2(v[2].y, v[3].y)) << 16);
+        }
+        uint4* dl = reinterpret_cast<uint4*>(p.qc + c * p.rows + r0 + 32 * part);
+        uint4* dh = reinterpret_cast<uint4*>(p.qc + (c + 1) * p.rows + r0 + 32 * part);
+        __stcs(dl, make_uint4(wl[0], wl[1], wl[2], wl[3]));
+        __stcs(dl + 1, make_uint4(wl[4], wl[5], wl[6], wl[7]));
+        __stcs(dh, make_uint4(wh[0], wh[1], wh[2], wh[3]));
+        __stcs(dh + 1, make_uint4(wh[4], wh[5], wh[6], wh[7]));
     }
 }
 
-// Column codes of one 128 x 128 tile of y, as the transposed casts lay them
-// out: thread t takes the column pair t / 4 and the 32-row part t % 4.  |y| =
-// fl(fl(|h| rstd) |gamma|) grows with fl(|h| rstd), so the block maximum needs
-// one product per element and gamma once.
 template <int FMT, int RECIPE>
-__global__ void __launch_bounds__(256, 4) rmsnorm_cols_kernel(const __grid_constant__ RmsNormParams p) {
-    __shared__ __align__(16) uint32_t tile[128][64];
-    __shared__ float rs[4][33];
-    const uint16_t* h = p.h ? p.h : p.x;
-    const int64_t ldh = p.h ? p.cols : p.ldx;
-    const int64_t rb = blockIdx.y;
-    const int64_t r0 = rb * 128, c0 = static_cast<int64_t>(blockIdx.x) * 128;
-#pragma unroll
-    for (int it = 0; it < 8; ++it) {
-        const int i = threadIdx.x + it * 256;
-        const int rr = i >> 4, ch = i & 15;
-        *reinterpret_cast<uint4*>(&tile[rr][(ch * 4 + 8 * (rr >> 5)) & 63]) =
-            *reinterpret_cast<const uint4*>(h + (r0 + rr) * ldh + c0 + ch * 8);
+int launch_cols(const RmsNormParams& p, cudaStream_t stream, int num_sms) {
+    auto kern = rmsnorm_cols_kernel<FMT, RECIPE>;
+    static unsigned long long configured = 0;  // one bit per device ordinal
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return -3;
+    if (!(configured & (1ull << dev))) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * sizeof(ColsStage)) !=
+            cudaSuccess)
+            return -3;
+        configured |= 1ull << dev;
     }
-    if (threadIdx.x < 128) rs[threadIdx.x >> 5][threadIdx.x & 31] = p.rstd[r0 + threadIdx.x];
-    __syncthreads();
-    const int cp = threadIdx.x >> 2, part = threadIdx.x & 3;
-    const int64_t c = c0 + 2 * cp;
-    const uint32_t gw = *reinterpret_cast<const uint32_t*>(p.gamma + c);
-    const float g_lo = bf16_lo(gw), g_hi = bf16_hi(gw);
-    const int wcol = (cp + 8 * part) & 63;
-    float inv_lo = 1.0f, inv_hi = 1.0f, s_lo = 1.0f, s_hi = 1.0f;
-    if (RECIPE == kRecipeTensor) {
-        block_scale<FMT>(*p.amax_in, inv_lo, s_lo);
-        inv_hi = inv_lo;
-    } else {
-        float a_lo = 0.0f, a_hi = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            const uint32_t w = tile[32 * part + i][wcol];
-            const float s = rs[part][i];
-            a_lo = fmaxf(a_lo, fabsf(__fmul_rn(bf16_lo(w), s)));
-            a_hi = fmaxf(a_hi, fabsf(__fmul_rn(bf16_hi(w), s)));
-        }
-        a_lo = __fmul_rn(a_lo, fabsf(g_lo));
-        a_hi = __fmul_rn(a_hi, fabsf(g_hi));
-        if (RECIPE == kRecipeBlock) {
-#pragma unroll
-            for (int off = 1; off <= 2; off <<= 1) {
-                a_lo = fmaxf(a_lo, __shfl_xor_sync(0xffffffffu, a_lo, off));
-                a_hi = fmaxf(a_hi, __shfl_xor_sync(0xffffffffu, a_hi, off));
-            }
-            block_scale<FMT>(a_lo, inv_lo, s_lo);
-            block_scale<FMT>(a_hi, inv_hi, s_hi);
-            if (part == 0) {
-                p.sc[rb * p.sldc + c] = s_lo;
-                p.sc[rb * p.sldc + c + 1] = s_hi;
-            }
-        } else {
-            const int e_lo = mx_exponent<FMT>(a_lo), e_hi = mx_exponent<FMT>(a_hi);
-            inv_lo = mx_inverse_scale(e_lo);
-            inv_hi = mx_inverse_scale(e_hi);
-            const int64_t groups = 2 * ((p.cols + 255) / 256);
-            p.sfc[mx_sf_offset(rb, groups, c, part)] = static_cast<uint8_t>(e_lo + 127);
-            p.sfc[mx_sf_offset(rb, groups, c + 1, part)] = static_cast<uint8_t>(e_hi + 127);
-            // an odd number of 128-column groups: the group beyond the matrix holds 127
-            if (c0 + 128 == p.cols && (p.cols & 255) != 0 && threadIdx.x < 128)
-                *reinterpret_cast<uint32_t*>(p.sfc + mx_sf_offset(rb, groups, p.cols + threadIdx.x, 0)) = 0x7F7F7F7Fu;
-        }
-    }
-    uint32_t wl[8], wh[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        uint32_t lo16[2], hi16[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int k = 4 * i + 2 * j;
-            const uint32_t w0 = tile[32 * part + k][wcol], w1 = tile[32 * part + k + 1][wcol];
-            const float s0 = rs[part][k], s1 = rs[part][k + 1];
-            lo16[j] = encode2<FMT>(__fmul_rn(__fmul_rn(bf16_lo(w0), s0), g_lo),
-                                   __fmul_rn(__fmul_rn(bf16_lo(w1), s1), g_lo), inv_lo);
-            hi16[j] = encode2<FMT>(__fmul_rn(__fmul_rn(bf16_hi(w0), s0), g_hi),
-                                   __fmul_rn(__fmul_rn(bf16_hi(w1), s1), g_hi), inv_hi);
-        }
-        wl[i] = lo16[0] | (lo16[1] << 16);
-        wh[i] = hi16[0] | (hi16[1] << 16);
-    }
-    uint4* dl = reinterpret_cast<uint4*>(p.qc + c * p.rows + r0 + 32 * part);
-    uint4* dh = reinterpret_cast<uint4*>(p.qc + (c + 1) * p.rows + r0 + 32 * part);
-    dl[0] = make_uint4(wl[0], wl[1], wl[2], wl[3]);
-    dl[1] = make_uint4(wl[4], wl[5], wl[6], wl[7]);
-    dh[0] = make_uint4(wh[0], wh[1], wh[2], wh[3]);
-    dh[1] = make_uint4(wh[4], wh[5], wh[6], wh[7]);
+    const int64_t tiles = p.rows / 128 * (p.cols / 128), cap = static_cast<int64_t>(num_sms) * kColsCtas;
+    kern<<<static_cast<unsigned>(tiles < cap ? tiles : cap), 256, 2 * sizeof(ColsStage), stream>>>(p);
+    return cudaGetLastError() == cudaSuccess ? 0 : -3;
 }
 
 // threads and vectors per thread of a row of nv 16-byte vectors
@@ -244,25 +376,26 @@ void row_shape(int64_t cols, int& T, int& V) {
 
 template <int FMT, int RECIPE>
 int launch_norm(const RmsNormParams& p, cudaStream_t stream, int num_sms) {
-    int T, V;
-    row_shape(p.cols, T, V);
     if (RECIPE == kRecipeTensor && p.amax_out &&
         cudaMemsetAsync(p.amax_out, 0, sizeof(float), stream) != cudaSuccess)
         return -3;
-    int64_t grid = RECIPE == kRecipeMx && p.qr ? (p.rows + 255) / 256 * 256 : p.rows;
-    const int64_t cap = static_cast<int64_t>(num_sms) * (2048 / T);
+    int T, V;
+    row_shape(p.cols, T, V);
+    int64_t grid = RECIPE == kRecipeMx ? (p.rows + 255) / 256 * 256 : p.rows;
+    const int64_t cap = static_cast<int64_t>(num_sms) * ((V == 1 ? 1024 : 768) / T < 1 ? 1 : (V == 1 ? 1024 : 768) / T);
     if (grid > cap) grid = cap;
     const unsigned g = static_cast<unsigned>(grid);
     switch (V) {
-        case 1: rmsnorm_rows_kernel<FMT, RECIPE, 1><<<g, T, 0, stream>>>(p); break;
-        case 2: rmsnorm_rows_kernel<FMT, RECIPE, 2><<<g, T, 0, stream>>>(p); break;
-        default: rmsnorm_rows_kernel<FMT, RECIPE, 4><<<g, T, 0, stream>>>(p); break;
+        case 1: rmsnorm_rows_kernel<FMT, RECIPE, 1, 128, true><<<g, T, 0, stream>>>(p); break;
+        case 2: rmsnorm_rows_kernel<FMT, RECIPE, 2, 256, true><<<g, T, 0, stream>>>(p); break;
+        default:
+            if (T <= 512)
+                rmsnorm_rows_kernel<FMT, RECIPE, 4, 512, true><<<g, T, 0, stream>>>(p);
+            else
+                rmsnorm_rows_kernel<FMT, RECIPE, 4, 1024, false><<<g, T, 0, stream>>>(p);
     }
-    if (p.qc) {
-        const dim3 tiles(static_cast<unsigned>(p.cols / 128), static_cast<unsigned>(p.rows / 128));
-        rmsnorm_cols_kernel<FMT, RECIPE><<<tiles, 256, 0, stream>>>(p);
-    }
-    return cudaGetLastError() == cudaSuccess ? 0 : -3;
+    if (cudaGetLastError() != cudaSuccess) return -3;
+    return p.qc ? launch_cols<FMT, RECIPE>(p, stream, num_sms) : 0;
 }
 
 // ---------------------------------------------------------------- backward
@@ -270,93 +403,203 @@ int launch_norm(const RmsNormParams& p, cudaStream_t stream, int num_sms) {
 //   d = dy gamma, xhat = h rstd, m = mean_c (d xhat)
 //   dx = rstd (d - xhat m) + dres        dgamma_c = sum_r dy xhat
 //
-// A CTA walks rows; a thread keeps the same columns for all of them, so dgamma
-// is summed in its registers and written once per CTA as a band of partial
-// sums, which the finalize adds in a fixed order.
-template <int V>
-__global__ void __launch_bounds__(1024) rmsnorm_grad_kernel(const __grid_constant__ RmsNormGradParams p) {
+// T threads walk rows together; a thread keeps the same columns for all of
+// them, so dgamma is summed in its registers (SMEM: in shared memory, where a
+// row is too wide for them) and written once per CTA as a band of partial sums,
+// which the finalize adds in a fixed order.  PRE: the next row's dy and h are
+// loaded while the current row is reduced.  LANES: a warp or half a warp per
+// row, 256 / LANES rows per CTA, whose sums meet in shared memory at the end
+// (0: the whole CTA per row).  Products in packed pairs, each rounded as a
+// scalar one would be.
+__device__ __forceinline__ void unpack_pairs(const uint4& w, uint64_t (&f)[4]) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[e] = pack_f32x2(bf16_lo(u[e]), bf16_hi(u[e]));
+}
+
+template <int V, int MAXT, bool SMEM, bool PRE, int LANES>
+__global__ void __launch_bounds__(MAXT, 1) rmsnorm_grad_kernel(const __grid_constant__ RmsNormGradParams p) {
+    static_assert(LANES == 0 || !SMEM, "a warp's sums stay in registers");
+    constexpr bool WARP = LANES != 0;
+    constexpr int kRowsPerCta = WARP ? 256 / (WARP ? LANES : 1) : 1;
     __shared__ float part[2][32];
+    extern __shared__ __align__(16) float acc_smem[];  // SMEM: [cols], LANES: [kRowsPerCta][cols]
     const int nv = static_cast<int>(p.cols / 8);
-    const int T = blockDim.x;
-    float acc[V][8];
+    const int T = WARP ? LANES : blockDim.x;
+    const int tid = WARP ? threadIdx.x % (WARP ? LANES : 1) : threadIdx.x;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    uint64_t acc[SMEM ? 1 : V][4];
+    if (SMEM) {
+        for (int i = tid; i < nv; i += T) {
+            reinterpret_cast<uint4*>(acc_smem)[2 * i] = zero;
+            reinterpret_cast<uint4*>(acc_smem)[2 * i + 1] = zero;
+        }
+    } else {
 #pragma unroll
-    for (int v = 0; v < V; ++v)
+        for (int v = 0; v < V; ++v)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) acc[v][e] = 0.0f;
-    int k = 0;
-    for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x, ++k) {
-        uint4 dv[V], hv[V];
-        const float rstd = p.rstd[r];
-        float dot = 0.0f;
+            for (int e = 0; e < 4; ++e) acc[SMEM ? 0 : v][e] = 0ull;
+    }
+    uint4 dn[PRE ? V : 1], hn[PRE ? V : 1];  // the next row
+    auto load = [&](const uint16_t* base, int64_t ld, int64_t r, int v) {
+        const int i = tid + v * T;
+        return i < nv && r < p.rows ? __ldcs(reinterpret_cast<const uint4*>(base + r * ld + 8 * i)) : zero;
+    };
+    auto fetch = [&](int64_t r) {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int i = threadIdx.x + v * T;
-            dv[v] = hv[v] = make_uint4(0, 0, 0, 0);
-            if (i < nv) {
-                dv[v] = *reinterpret_cast<const uint4*>(p.dy + r * p.lddy + 8 * i);
-                hv[v] = *reinterpret_cast<const uint4*>(p.h + r * p.ldh + 8 * i);
-            }
+            dn[PRE ? v : 0] = load(p.dy, p.lddy, r, v);
+            hn[PRE ? v : 0] = load(p.h, p.ldh, r, v);
+        }
+    };
+    auto gamma = [&](int v) {
+        const int i = tid + v * T;
+        return i < nv ? __ldg(reinterpret_cast<const uint4*>(p.gamma + 8 * i)) : zero;
+    };
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kRowsPerCta;
+    const int own = WARP ? static_cast<int>(threadIdx.x) / (WARP ? LANES : 1) : 0;  // the row within the CTA
+    int64_t r = static_cast<int64_t>(blockIdx.x) * kRowsPerCta + own;
+    const int second = LANES == 16 ? own & 1 : 0;  // the halves of a warp leave the loop together
+    if (PRE) fetch(r);
+    for (int k = 0; r - second < p.rows; r += step, ++k) {
+        uint4 dv[V], hv[V], sv[V];
+        const float rstd = r < p.rows ? p.rstd[r] : 0.0f;
+        const uint64_t rstd2 = pack_f32x2(rstd, rstd);
+        uint64_t dot2 = 0ull;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            dv[v] = PRE ? dn[PRE ? v : 0] : load(p.dy, p.lddy, r, v);
+            hv[v] = PRE ? hn[PRE ? v : 0] : load(p.h, p.ldh, r, v);
+            if (PRE) sv[v] = p.dres ? load(p.dres, p.ldres, r, v) : zero;
         }
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int i = threadIdx.x + v * T;
-            float d[8], h[8], g[8];
-            unpack8(dv[v], d);
-            unpack8(hv[v], h);
-            unpack8(i < nv ? __ldg(reinterpret_cast<const uint4*>(p.gamma + 8 * i)) : make_uint4(0, 0, 0, 0), g);
+            const int i = tid + v * T;
+            uint64_t d[4], h[4], g[4];
+            unpack_pairs(dv[v], d);
+            unpack_pairs(hv[v], h);
+            unpack_pairs(gamma(v), g);
+            if (SMEM && i < nv) {
+                ulonglong2* a = reinterpret_cast<ulonglong2*>(acc_smem + 8 * i);
+                ulonglong2 a0 = a[0], a1 = a[1];
+                a0.x = fma_f32x2(d[0], mul_f32x2(h[0], rstd2), a0.x);
+                a0.y = fma_f32x2(d[1], mul_f32x2(h[1], rstd2), a0.y);
+                a1.x = fma_f32x2(d[2], mul_f32x2(h[2], rstd2), a1.x);
+                a1.y = fma_f32x2(d[3], mul_f32x2(h[3], rstd2), a1.y);
+                a[0] = a0;
+                a[1] = a1;
+            }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float xhat = h[e] * rstd;
-                acc[v][e] = fmaf(d[e], xhat, acc[v][e]);
-                dot = fmaf(d[e] * g[e], xhat, dot);
+            for (int e = 0; e < 4; ++e) {
+                const uint64_t xhat = mul_f32x2(h[e], rstd2);
+                if (!SMEM) acc[SMEM ? 0 : v][e] = fma_f32x2(d[e], xhat, acc[SMEM ? 0 : v][e]);
+                dot2 = fma_f32x2(mul_f32x2(d[e], g[e]), xhat, dot2);
             }
         }
-        const float m = __fdiv_rn(block_sum(dot, part[k & 1]), static_cast<float>(p.cols));
+        if (PRE) fetch(r + step);
+        const float2 dot = unpack_f32x2(dot2);
+        float sum = dot.x + dot.y;
+        if (WARP) {
+#pragma unroll
+            for (int off = LANES / 2; off >= 1; off >>= 1)
+                sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, off));
+        } else {
+            sum = block_sum(sum, part[k & 1]);
+        }
+        const float m = -__fdiv_rn(sum, static_cast<float>(p.cols));
+        const uint64_t m2 = pack_f32x2(m, m);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int i = threadIdx.x + v * T;
-            if (i >= nv) continue;
-            float d[8], h[8], g[8], s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            unpack8(dv[v], d);
-            unpack8(hv[v], h);
-            unpack8(__ldg(reinterpret_cast<const uint4*>(p.gamma + 8 * i)), g);
-            if (p.dres) unpack8(*reinterpret_cast<const uint4*>(p.dres + r * p.ldres + 8 * i), s);
+            const int i = tid + v * T;
+            if (i >= nv || r >= p.rows) continue;
+            uint64_t d[4], h[4], g[4], s[4];
+            unpack_pairs(dv[v], d);
+            unpack_pairs(hv[v], h);
+            unpack_pairs(gamma(v), g);
+            if (!PRE) sv[v] = p.dres ? load(p.dres, p.ldres, r, v) : zero;
+            unpack_pairs(sv[v], s);
+            uint32_t w[4];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) d[e] = fmaf(rstd, fmaf(-h[e] * rstd, m, d[e] * g[e]), s[e]);
-            *reinterpret_cast<uint4*>(p.dx + r * p.cols + 8 * i) = pack8(d);
+            for (int e = 0; e < 4; ++e) {
+                const uint64_t x =
+                    fma_f32x2(rstd2, fma_f32x2(mul_f32x2(h[e], rstd2), m2, mul_f32x2(d[e], g[e])), s[e]);
+                const float2 f = unpack_f32x2(x);
+                w[e] = pack_bf16x2(f.x, f.y);
+            }
+            __stcs(reinterpret_cast<uint4*>(p.dx + r * p.cols + 8 * i), make_uint4(w[0], w[1], w[2], w[3]));
         }
     }
+    float* band = p.partials + static_cast<int64_t>(blockIdx.x) * p.cols;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        const int i = threadIdx.x + v * T;
+        const int i = tid + v * T;
         if (i >= nv) continue;
-        float4* o = reinterpret_cast<float4*>(p.partials + static_cast<int64_t>(blockIdx.x) * p.cols + 8 * i);
-        o[0] = make_float4(acc[v][0], acc[v][1], acc[v][2], acc[v][3]);
-        o[1] = make_float4(acc[v][4], acc[v][5], acc[v][6], acc[v][7]);
+        // SMEM: a thread wrote the columns of shared memory that it reads here
+        const ulonglong2* a = reinterpret_cast<const ulonglong2*>(acc_smem + 8 * i);
+        ulonglong2* o = reinterpret_cast<ulonglong2*>((WARP ? acc_smem + own * p.cols : band) + 8 * i);
+        o[0] = SMEM ? a[0] : make_ulonglong2(acc[SMEM ? 0 : v][0], acc[SMEM ? 0 : v][1]);
+        o[1] = SMEM ? a[1] : make_ulonglong2(acc[SMEM ? 0 : v][2], acc[SMEM ? 0 : v][3]);
+    }
+    if (WARP) {
+        __syncthreads();
+        for (int c = threadIdx.x; c < p.cols; c += 256) {
+            float t = acc_smem[c];
+#pragma unroll
+            for (int w = 1; w < kRowsPerCta; ++w) t = __fadd_rn(t, acc_smem[w * p.cols + c]);
+            band[c] = t;
+        }
     }
 }
 
-// dgamma[c] (+)= sum over the bands: 32 columns per CTA, eight threads per
-// column take every eighth band, their sums are added in order
-__global__ void __launch_bounds__(256) rmsnorm_grad_finalize_kernel(const float* __restrict__ ws, int64_t bands,
-                                                                    int64_t cols, float* __restrict__ out,
-                                                                    int accumulate) {
-    __shared__ float part[8][32];
+// dgamma[c] (+)= sum over the bands: 32 columns per CTA, 32 threads per column
+// take every 32nd band, their sums are added in order
+__global__ void __launch_bounds__(1024) rmsnorm_grad_finalize_kernel(const float* __restrict__ ws, int bands,
+                                                                     int64_t cols, float* __restrict__ out,
+                                                                     int accumulate) {
+    __shared__ float part[32][33];
     const int cl = threadIdx.x & 31, sl = threadIdx.x >> 5;
     const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + cl;
     float s = 0.0f;
     if (c < cols) {
 #pragma unroll 8
-        for (int64_t b = sl; b < bands; b += 8) s += ws[b * cols + c];
+        for (int b = sl; b < bands; b += 32) s += ws[b * cols + c];
     }
     part[sl][cl] = s;
     __syncthreads();
     if (sl == 0 && c < cols) {
         float t = part[0][cl];
 #pragma unroll
-        for (int i = 1; i < 8; ++i) t += part[i][cl];
+        for (int i = 1; i < 32; ++i) t += part[i][cl];
         out[c] = accumulate ? out[c] + t : t;
     }
+}
+
+// T threads per CTA (a warp per row: 256), `resident` CTAs per SM at once: each
+// CTA leaves one band of partial sums
+template <int V, int MAXT, bool SMEM, bool PRE, int LANES>
+int launch_grad(const RmsNormGradParams& p, int T, int num_sms, int resident, cudaStream_t stream) {
+    auto kern = rmsnorm_grad_kernel<V, MAXT, SMEM, PRE, LANES>;
+    constexpr int rows_per_cta = LANES ? 256 / (LANES ? LANES : 1) : 1;
+    const size_t smem = SMEM || LANES ? static_cast<size_t>(p.cols) * 4 * rows_per_cta : 0;
+    if (SMEM) {
+        static unsigned long long configured = 0;  // one bit per device ordinal
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return -3;
+        if (!(configured & (1ull << dev))) {
+            if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     static_cast<int>(kNormMaxCols * 4)) != cudaSuccess)
+                return -3;
+            configured |= 1ull << dev;
+        }
+    }
+    int64_t cap = static_cast<int64_t>(num_sms) * (resident < 1 ? 1 : resident);
+    if (cap > kGradMaxBands) cap = kGradMaxBands;
+    const int64_t want = (p.rows + rows_per_cta - 1) / rows_per_cta;
+    const int bands = static_cast<int>(want < cap ? want : cap);
+    kern<<<bands, T, smem, stream>>>(p);
+    rmsnorm_grad_finalize_kernel<<<static_cast<unsigned>((p.cols + 31) / 32), 1024, 0, stream>>>(
+        p.partials, bands, p.cols, p.dgamma, p.accumulate);
+    return cudaGetLastError() == cudaSuccess ? 0 : -3;
 }
 
 }  // namespace
@@ -374,19 +617,22 @@ int launch_rmsnorm(const RmsNormParams& p, int recipe, int fmt, cudaStream_t str
 }
 
 int launch_rmsnorm_grad(const RmsNormGradParams& p, cudaStream_t stream, int num_sms) {
-    int T, V;
-    row_shape(p.cols, T, V);
-    int64_t cap = static_cast<int64_t>(num_sms) * (1024 / T);
-    if (cap > kGradMaxBands) cap = kGradMaxBands;
-    const int bands = static_cast<int>(p.rows < cap ? p.rows : cap);
-    switch (V) {
-        case 1: rmsnorm_grad_kernel<1><<<bands, T, 0, stream>>>(p); break;
-        case 2: rmsnorm_grad_kernel<2><<<bands, T, 0, stream>>>(p); break;
-        default: rmsnorm_grad_kernel<4><<<bands, T, 0, stream>>>(p); break;
-    }
-    rmsnorm_grad_finalize_kernel<<<static_cast<unsigned>((p.cols + 31) / 32), 256, 0, stream>>>(
-        p.partials, bands, p.cols, p.dgamma, p.accumulate);
-    return cudaGetLastError() == cudaSuccess ? 0 : -3;
+    const int64_t nv = p.cols / 8;
+    auto threads = [nv](int V) { return static_cast<int>(((nv + V - 1) / V + 31) / 32 * 32); };
+    // up to 1024 columns a row needs no more than a warp: 25.8 us at 32768 x 512
+    // against 35.8 with 64 threads per row and a barrier
+    if (nv <= 16) return launch_grad<1, 256, false, true, 16>(p, 256, num_sms, 4, stream);
+    if (nv <= 32) return launch_grad<1, 256, false, true, 32>(p, 256, num_sms, 4, stream);
+    if (nv <= 64) return launch_grad<2, 256, false, true, 32>(p, 256, num_sms, 2, stream);
+    if (nv <= 128) return launch_grad<4, 256, false, true, 32>(p, 256, num_sms, 1, stream);
+    // two vectors a thread while the CTA stays within 512 threads, else dgamma
+    // moves to shared memory: 102.6 us at 4096 x 14336 against 132.9 with spilled
+    // registers
+    int T = threads(2);
+    if (T <= 512) return launch_grad<2, 512, false, true, 0>(p, T, num_sms, 512 / T, stream);
+    T = threads(4);
+    if (T <= 512) return launch_grad<4, 512, true, true, 0>(p, T, num_sms, 1, stream);
+    return launch_grad<8, 512, true, false, 0>(p, threads(8), num_sms, 1, stream);
 }
 
 }  // namespace fp8ll

@@ -183,7 +183,8 @@ def check_backward(got_dx, got_dg, dy, h, gamma, rstd, res, before=None):
 
 
 @pytest.mark.parametrize("rows,cols", [(1, 8), (1, 4096), (2, 24), (7, 520), (333, 1000), (1000, 2048), (64, 7168),
-                                       (5, 14336), (3, 16392), (4, 32768), (2500, 136)])
+                                       (5, 14336), (3, 16392), (4, 32768), (2500, 136), (5001, 128),
+                                       (700, 504), (31, 1024), (33, 8192), (9, 8200)])
 @pytest.mark.parametrize("with_residual", [False, True])
 def test_backward(fp8, rows, cols, with_residual):
     pad = 8 if rows % 2 else 0
