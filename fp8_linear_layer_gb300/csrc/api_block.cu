@@ -238,7 +238,7 @@ size_t fp8_grad_norm_workspace_size(int64_t count) {
 
 static int grad_call(int64_t count, const fp8ll_grad_t* grads, int scale, float max_norm, float* norm,
                      void* workspace, size_t workspace_bytes, fp8ll_stream_t stream) {
-    if (count < 0 || count > (1 << 20) || (count > 0 && !grads) || !norm || !aligned(norm, 4))
+    if (count < 0 || count > kClipMaxTensors || (count > 0 && !grads) || !norm || !aligned(norm, 4))
         return FP8LL_ERR_INVALID_ARG;
     if (scale && !(max_norm >= 0.0f)) return FP8LL_ERR_INVALID_ARG;
     const int64_t need = static_cast<int64_t>(fp8_grad_norm_workspace_size(count));

@@ -18,6 +18,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "launch.cuh"
 #include "mx_rule.cuh"
 #include "rmsnorm.h"
 
@@ -101,6 +102,7 @@ __device__ __forceinline__ void fold_amax(float top, float* part, float* amax_ou
 template <int FMT, int RECIPE, int V, int MAXT, bool GREG>
 __global__ void __launch_bounds__(MAXT) rmsnorm_rows_kernel(const __grid_constant__ RmsNormParams p) {
     __shared__ float part[2][32];
+    release_dependents();
     const int nv = static_cast<int>(p.cols / 8);
     const int T = blockDim.x;
     const int lane = threadIdx.x & 31;
@@ -252,6 +254,7 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
 template <int FMT, int RECIPE>
 __global__ void __launch_bounds__(256, kColsCtas) rmsnorm_cols_kernel(const __grid_constant__ RmsNormParams p) {
     extern __shared__ __align__(16) uint8_t stage_raw[];
+    await_dependency();
     ColsStage* stage = reinterpret_cast<ColsStage*>(stage_raw);
     const uint16_t* h = p.h ? p.h : p.x;
     const int64_t ldh = p.h ? p.cols : p.ldx;
@@ -363,8 +366,10 @@ int launch_cols(const RmsNormParams& p, cudaStream_t stream, int num_sms) {
         configured |= 1ull << dev;
     }
     const int64_t tiles = p.rows / 128 * (p.cols / 128), cap = static_cast<int64_t>(num_sms) * kColsCtas;
-    kern<<<static_cast<unsigned>(tiles < cap ? tiles : cap), 256, 2 * sizeof(ColsStage), stream>>>(p);
-    return cudaGetLastError() == cudaSuccess ? 0 : -3;
+    return launch_dependent(kern, static_cast<unsigned>(tiles < cap ? tiles : cap), 256, 2 * sizeof(ColsStage), stream,
+                            p) == cudaSuccess
+               ? 0
+               : -3;
 }
 
 // threads and vectors per thread of a row of nv 16-byte vectors
@@ -424,6 +429,7 @@ __global__ void __launch_bounds__(MAXT, 1) rmsnorm_grad_kernel(const __grid_cons
     constexpr int kRowsPerCta = WARP ? 256 / (WARP ? LANES : 1) : 1;
     __shared__ float part[2][32];
     extern __shared__ __align__(16) float acc_smem[];  // SMEM: [cols], LANES: [kRowsPerCta][cols]
+    release_dependents();
     const int nv = static_cast<int>(p.cols / 8);
     const int T = WARP ? LANES : blockDim.x;
     const int tid = WARP ? threadIdx.x % (WARP ? LANES : 1) : threadIdx.x;
@@ -556,6 +562,7 @@ __global__ void __launch_bounds__(MAXT, 1) rmsnorm_grad_kernel(const __grid_cons
 __global__ void __launch_bounds__(1024) rmsnorm_grad_finalize_kernel(const float* __restrict__ ws, int bands,
                                                                      int64_t cols, float* __restrict__ out,
                                                                      int accumulate) {
+    await_dependency();
     __shared__ float part[32][33];
     const int cl = threadIdx.x & 31, sl = threadIdx.x >> 5;
     const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + cl;
@@ -597,9 +604,11 @@ int launch_grad(const RmsNormGradParams& p, int T, int num_sms, int resident, cu
     const int64_t want = (p.rows + rows_per_cta - 1) / rows_per_cta;
     const int bands = static_cast<int>(want < cap ? want : cap);
     kern<<<bands, T, smem, stream>>>(p);
-    rmsnorm_grad_finalize_kernel<<<static_cast<unsigned>((p.cols + 31) / 32), 1024, 0, stream>>>(
-        p.partials, bands, p.cols, p.dgamma, p.accumulate);
-    return cudaGetLastError() == cudaSuccess ? 0 : -3;
+    if (cudaGetLastError() != cudaSuccess) return -3;
+    return launch_dependent(rmsnorm_grad_finalize_kernel, static_cast<unsigned>((p.cols + 31) / 32), 1024, 0, stream,
+                            p.partials, bands, p.cols, p.dgamma, p.accumulate) == cudaSuccess
+               ? 0
+               : -3;
 }
 
 }  // namespace

@@ -513,8 +513,8 @@ typedef struct {
 size_t fp8_grad_norm_workspace_size(int64_t count);
 
 /* *norm (fp32, device) = sqrt of the sum of squares over all tensors.  grads:
- * HOST array (copied before the call returns).  Squares are summed in fp32 per
- * CTA, then in fp64, in a fixed order.  No tensors, or empty ones: 0. */
+ * HOST array (copied before the call returns).  Squares are summed in fp32, in a
+ * fixed order.  No tensors, or empty ones: 0. */
 int fp8_grad_norm(int64_t count, const fp8ll_grad_t* grads, float* norm, void* workspace, size_t workspace_bytes,
                   fp8ll_stream_t stream);
 
