@@ -12,8 +12,21 @@ from typing import Optional, Sequence
 import torch
 
 from . import binding as B
-from .binding import (ACC_FULL, ACT_GELU, ACT_NONE, Fp8MxTensor, Fp8Tensor, Fp8TensorScaled, _check, _ptr, _stream,
-                      empty_fp8, empty_mx, lib)
+from .binding import (ACC_FULL, ACT_GELU, ACT_NONE, Fp8MxTensor, Fp8Tensor, Fp8TensorScaled, _check, empty_fp8,
+                      empty_mx, lib)
+
+_bf16, _f32 = torch.bfloat16, torch.float32
+
+
+def _stream() -> int:
+    """torch's current stream as the address that the library takes (the same
+    stream as ``torch.cuda.current_stream()``, without building its object: a
+    call of few tokens is bound by what the host does)."""
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+
+
+def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
 
 
 # -------------------------------------------------------------------- norm ----
@@ -65,24 +78,38 @@ def empty_tensor_rmsnorm(rows: int, cols: int, fmt: int, rows_too: bool = True, 
     return out
 
 
+def _rows(t, shape):
+    """Leading dimension of a bf16 matrix of this shape with packed rows."""
+    ld, one = t.stride()
+    assert t.dtype is _bf16 and t.shape == shape and (one == 1 or shape[1] == 1)
+    return ld if shape[0] > 1 else shape[1]
+
+
+def _packed(t, dtype, shape):
+    """Address of a contiguous tensor of this type and shape (or none)."""
+    if t is None:
+        return None
+    assert t.dtype is dtype and t.shape == shape and t.is_contiguous()
+    return t.data_ptr()
+
+
 def _norm_args(x, gamma, eps, fmt, residual, out):
-    assert x.dtype == torch.bfloat16 and x.dim() == 2 and x.stride(1) == 1
-    rows, cols = x.shape
-    assert gamma.dtype == torch.bfloat16 and gamma.is_contiguous() and gamma.numel() == cols
+    shape = x.shape
+    rows, cols = shape
+    ldx, ldr = _rows(x, shape), 0
     if residual is not None:
-        assert residual.dtype == torch.bfloat16 and residual.shape == x.shape and residual.stride(1) == 1
+        ldr = _rows(residual, shape)
         assert out.h is not None, "the sum x + residual needs its place (h)"
-    for t in (out.h, out.y):
-        assert t is None or (t.dtype == torch.bfloat16 and t.shape == x.shape and t.is_contiguous())
-    assert out.rstd.dtype == torch.float32 and out.rstd.is_contiguous() and out.rstd.numel() == rows
-    for t, shape in ((out.rows, (rows, cols)), (out.cols, (cols, rows))):
-        assert t is None or (t.fmt == fmt and tuple(t.q.shape) == shape and t.q.is_contiguous())
-    return (_ptr(x), _ptr(residual), _ptr(gamma), rows, cols, x.stride(0) if rows > 1 else cols,
-            (residual.stride(0) if rows > 1 else cols) if residual is not None else 0, float(eps), int(fmt))
+    return (x.data_ptr(), _ptr(residual), _packed(gamma, _bf16, (cols,)), rows, cols, ldx, ldr, eps, fmt)
 
 
-def _operand_ptrs(t, scale):
-    return (None, None) if t is None else (_ptr(t.q), _ptr(getattr(t, scale)))
+def _norm_outs(shape, out):
+    return _packed(out.h, _bf16, shape), _packed(out.rstd, _f32, (shape[0],)), _packed(out.y, _bf16, shape)
+
+
+def _codes(t, fmt, rows, cols):
+    assert t.fmt == fmt
+    return _packed(t.q, torch.uint8, (rows, cols))
 
 
 def rmsnorm_quantize(x: torch.Tensor, gamma: torch.Tensor, eps: float, fmt: int,
@@ -95,11 +122,15 @@ def rmsnorm_quantize(x: torch.Tensor, gamma: torch.Tensor, eps: float, fmt: int,
     if out is None:
         out = empty_rmsnorm(x.shape[0], x.shape[1], fmt, rows, cols, residual is not None, y, x.device)
     args = _norm_args(x, gamma, eps, fmt, residual, out)
-    qr, sr = _operand_ptrs(out.rows, "scale")
-    qc, sc = _operand_ptrs(out.cols, "scale")
-    _check(lib().fp8_rmsnorm_quantize(*args, _ptr(out.h), _ptr(out.rstd), _ptr(out.y), qr, sr,
-                                      out.rows.scale.stride(0) if qr else 0, qc, sc,
-                                      out.cols.scale.stride(0) if qc else 0, _stream()), "fp8_rmsnorm_quantize")
+    m, k = x.shape
+    qr = sr = qc = sc = None
+    ldr = ldc = 0
+    if out.rows is not None:
+        qr, sr, ldr = _codes(out.rows, fmt, m, k), out.rows.scale.data_ptr(), out.rows.scale.stride(0)
+    if out.cols is not None:
+        qc, sc, ldc = _codes(out.cols, fmt, k, m), out.cols.scale.data_ptr(), out.cols.scale.stride(0)
+    _check(lib().fp8_rmsnorm_quantize(*args, *_norm_outs(x.shape, out), qr, sr, ldr, qc, sc, ldc, _stream()),
+           "fp8_rmsnorm_quantize")
     return out
 
 
@@ -110,8 +141,13 @@ def mx_rmsnorm_quantize(x: torch.Tensor, gamma: torch.Tensor, eps: float, fmt: i
     if out is None:
         out = empty_mx_rmsnorm(x.shape[0], x.shape[1], fmt, rows, cols, residual is not None, y, x.device)
     args = _norm_args(x, gamma, eps, fmt, residual, out)
-    _check(lib().fp8_mx_rmsnorm_quantize(*args, _ptr(out.h), _ptr(out.rstd), _ptr(out.y),
-                                         *_operand_ptrs(out.rows, "sf"), *_operand_ptrs(out.cols, "sf"), _stream()),
+    m, k = x.shape
+    qr = sr = qc = sc = None
+    if out.rows is not None:
+        qr, sr = _codes(out.rows, fmt, m, k), out.rows.sf.data_ptr()
+    if out.cols is not None:
+        qc, sc = _codes(out.cols, fmt, k, m), out.cols.sf.data_ptr()
+    _check(lib().fp8_mx_rmsnorm_quantize(*args, *_norm_outs(x.shape, out), qr, sr, qc, sc, _stream()),
            "fp8_mx_rmsnorm_quantize")
     return out
 
@@ -125,13 +161,19 @@ def tensor_rmsnorm_quantize(x: torch.Tensor, gamma: torch.Tensor, eps: float, fm
     if out is None:
         out = empty_tensor_rmsnorm(x.shape[0], x.shape[1], fmt, rows, cols, residual is not None, y, x.device)
     args = _norm_args(x, gamma, eps, fmt, residual, out)
-    assert amax_in.dtype == torch.float32 and amax_in.numel() == 1
-    made = [t for t in (out.rows, out.cols) if t is not None]
-    assert len(made) < 2 or made[0].scale.data_ptr() == made[1].scale.data_ptr(), "both orientations share one scale"
-    scale = made[0].scale if made else torch.empty((1,), dtype=torch.float32, device=x.device)
-    _check(lib().fp8_tensor_rmsnorm_quantize(*args, _ptr(amax_in), _ptr(out.h), _ptr(out.rstd), _ptr(out.y),
-                                             _ptr(out.rows.q) if out.rows is not None else None,
-                                             _ptr(out.cols.q) if out.cols is not None else None, _ptr(scale),
+    assert amax_in.dtype is _f32 and amax_in.numel() == 1
+    m, k = x.shape
+    qr = qc = scale = spare = None
+    if out.rows is not None:
+        qr, scale = _codes(out.rows, fmt, m, k), out.rows.scale.data_ptr()
+    if out.cols is not None:
+        qc = _codes(out.cols, fmt, k, m)
+        assert scale in (None, out.cols.scale.data_ptr()), "both orientations share one scale"
+        scale = out.cols.scale.data_ptr()
+    if scale is None:  # only the bf16 form was asked for
+        spare = torch.empty((1,), dtype=_f32, device=x.device)
+        scale = spare.data_ptr()
+    _check(lib().fp8_tensor_rmsnorm_quantize(*args, amax_in.data_ptr(), *_norm_outs(x.shape, out), qr, qc, scale,
                                              _ptr(out.amax), _stream()), "fp8_tensor_rmsnorm_quantize")
     return out
 
@@ -149,29 +191,22 @@ def rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, gamma: torch.Tensor, rst
     """(dx, dgamma) of y = h rstd gamma: dx (bf16) is the gradient of h, with the
     gradient that reaches h around the norm (``residual_grad``) added; dgamma
     (fp32) is written, or added to with ``accumulate``."""
-    assert h.dim() == 2 and dy.shape == h.shape and dy.dtype == h.dtype == torch.bfloat16
-    assert dy.stride(1) == 1 and h.stride(1) == 1
-    rows, cols = h.shape
-    assert gamma.dtype == torch.bfloat16 and gamma.is_contiguous() and gamma.numel() == cols
-    assert rstd.dtype == torch.float32 and rstd.is_contiguous() and rstd.numel() == rows
+    shape = h.shape
+    rows, cols = shape
     r = residual_grad
-    assert r is None or (r.dtype == torch.bfloat16 and r.shape == h.shape and r.stride(1) == 1)
+    ldd, ldh, ldr = _rows(dy, shape), _rows(h, shape), 0 if r is None else _rows(r, shape)
     if out is None:
-        out = torch.empty((rows, cols), dtype=torch.bfloat16, device=h.device)
+        out = torch.empty((rows, cols), dtype=_bf16, device=h.device)
     if dgamma is None:
         assert not accumulate, "accumulate needs dgamma"
-        dgamma = torch.empty((cols,), dtype=torch.float32, device=h.device)
+        dgamma = torch.empty((cols,), dtype=_f32, device=h.device)
     if workspace is None:
         workspace = rmsnorm_workspace(rows, cols, h.device)
-    assert out.dtype == torch.bfloat16 and out.shape == h.shape and out.is_contiguous()
-    assert dgamma.dtype == torch.float32 and dgamma.is_contiguous() and dgamma.numel() == cols
-
-    def ld(t):
-        return t.stride(0) if rows > 1 else cols
-
-    _check(lib().fp8_rmsnorm_backward(_ptr(dy), _ptr(h), _ptr(gamma), _ptr(rstd), _ptr(r), rows, cols, ld(dy), ld(h),
-                                      ld(r) if r is not None else 0, _ptr(out), _ptr(dgamma), int(bool(accumulate)),
-                                      _ptr(workspace), workspace.numel() * workspace.element_size(), _stream()),
+    assert workspace.is_contiguous()
+    _check(lib().fp8_rmsnorm_backward(dy.data_ptr(), h.data_ptr(), _packed(gamma, _bf16, (cols,)),
+                                      _packed(rstd, _f32, (rows,)), _ptr(r), rows, cols, ldd, ldh, ldr,
+                                      _packed(out, _bf16, shape), _packed(dgamma, _f32, (cols,)), int(accumulate),
+                                      workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream()),
            "fp8_rmsnorm_backward")
     return out, dgamma
 
@@ -180,19 +215,14 @@ def rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, gamma: torch.Tensor, rst
 
 def _linear_args(M, N, bias, act, residual, out, aux, want_aux, device):
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=device)
+        out = torch.empty((M, N), dtype=_bf16, device=device)
     if aux is None and want_aux:
         assert act == ACT_GELU, "only an activation has a pre-activation to keep"
-        aux = torch.empty((M, N), dtype=torch.bfloat16, device=device)
-    for t in (out, aux):
-        assert t is None or (t.dtype == torch.bfloat16 and tuple(t.shape) == (M, N) and t.is_contiguous())
-    assert bias is None or (bias.dtype == torch.bfloat16 and bias.is_contiguous() and bias.numel() == N)
-    ldr = 0
-    if residual is not None:
-        assert residual.dtype == torch.bfloat16 and tuple(residual.shape) == (M, N)
-        assert N == 1 or residual.stride(1) == 1
-        ldr = residual.stride(0) if M > 1 else N
-    return out, aux, (_ptr(bias), int(act), _ptr(residual), ldr)
+        aux = torch.empty((M, N), dtype=_bf16, device=device)
+    shape = (M, N)
+    return (out, aux, (_packed(bias, _bf16, (N,)), act, _ptr(residual),
+                       0 if residual is None else _rows(residual, shape)),
+            (_packed(out, _bf16, shape), _packed(aux, _bf16, shape)))
 
 
 def gemm_linear(A: Fp8Tensor, W: Fp8Tensor, bias: Optional[torch.Tensor] = None, act: int = ACT_NONE,
@@ -202,11 +232,11 @@ def gemm_linear(A: Fp8Tensor, W: Fp8Tensor, bias: Optional[torch.Tensor] = None,
     Z-or-None), Z = A W^T + bias with ``want_aux`` or ``aux`` (GELU only).
     ``out`` may be the residual itself.  Few rows run a kernel of their own."""
     M, N = A.rows, W.rows
-    out, aux, args = _linear_args(M, N, bias, act, residual, out, aux, want_aux, A.q.device)
+    out, aux, args, dst = _linear_args(M, N, bias, act, residual, out, aux, want_aux, A.q.device)
     assert A.k == W.k
     oa, ob = A.operand(), W.operand()
-    _check(lib().fp8_gemm_linear(M, N, A.k, ctypes.byref(oa), ctypes.byref(ob), *args, int(acc), _ptr(out),
-                                 _ptr(aux), _stream()), "fp8_gemm_linear")
+    _check(lib().fp8_gemm_linear(M, N, A.k, ctypes.byref(oa), ctypes.byref(ob), *args, int(acc), *dst, _stream()),
+           "fp8_gemm_linear")
     return out, aux
 
 
@@ -215,11 +245,11 @@ def mx_gemm_linear(A: Fp8MxTensor, W: Fp8MxTensor, bias: Optional[torch.Tensor] 
                    aux: Optional[torch.Tensor] = None, want_aux: bool = False):
     """``gemm_linear`` on MXFP8 operands."""
     M, N = A.rows, W.rows
-    out, aux, args = _linear_args(M, N, bias, act, residual, out, aux, want_aux, A.q.device)
+    out, aux, args, dst = _linear_args(M, N, bias, act, residual, out, aux, want_aux, A.q.device)
     assert A.k == W.k
     oa, ob = A.operand(), W.operand()
-    _check(lib().fp8_mx_gemm_linear(M, N, A.k, ctypes.byref(oa), ctypes.byref(ob), *args, _ptr(out), _ptr(aux),
-                                    _stream()), "fp8_mx_gemm_linear")
+    _check(lib().fp8_mx_gemm_linear(M, N, A.k, ctypes.byref(oa), ctypes.byref(ob), *args, *dst, _stream()),
+           "fp8_mx_gemm_linear")
     return out, aux
 
 
@@ -229,11 +259,11 @@ def tensor_gemm_linear(A: Fp8TensorScaled, W: Fp8TensorScaled, bias: Optional[to
                        want_aux: bool = False):
     """``gemm_linear`` on per-tensor scaled operands."""
     M, N = A.rows, W.rows
-    out, aux, args = _linear_args(M, N, bias, act, residual, out, aux, want_aux, A.q.device)
+    out, aux, args, dst = _linear_args(M, N, bias, act, residual, out, aux, want_aux, A.q.device)
     assert A.k == W.k
     oa, ob = A.operand(), W.operand()
-    _check(lib().fp8_tensor_gemm_linear(M, N, A.k, ctypes.byref(oa), ctypes.byref(ob), *args, _ptr(out), _ptr(aux),
-                                        _stream()), "fp8_tensor_gemm_linear")
+    _check(lib().fp8_tensor_gemm_linear(M, N, A.k, ctypes.byref(oa), ctypes.byref(ob), *args, *dst, _stream()),
+           "fp8_tensor_gemm_linear")
     return out, aux
 
 
@@ -242,8 +272,9 @@ def tensor_gemm_linear(A: Fp8TensorScaled, W: Fp8TensorScaled, bias: Optional[to
 class GradList:
     """The gradient tensors of a model (fp32 or bf16, contiguous), with where
     their clipped values go (``out``: the tensors themselves by default), the
-    norm's place on the device and the workspace: built once, used every step.
-    It holds the tensors; what they contain is read at each call."""
+    norm's place on the device (``norm``, overwritten by each call) and the
+    workspace: built once, used every step, by one call at a time.  It holds the
+    tensors and their memory; what they contain is read at each call."""
 
     def __init__(self, grads: Sequence[torch.Tensor], out: Optional[Sequence[torch.Tensor]] = None):
         self.grads = list(grads)
@@ -260,16 +291,17 @@ class GradList:
         self.norm = torch.empty((1,), dtype=torch.float32, device=device)
         self.workspace = torch.empty((int(lib().fp8_grad_norm_workspace_size(len(self.grads))) // 4,),
                                      dtype=torch.float32, device=device)
-
-    def _tail(self):
-        return _ptr(self.norm), _ptr(self.workspace), self.workspace.numel() * 4, _stream()
+        # the memory that the table points to stays allocated as long as the list,
+        # whatever becomes of the tensors
+        self._storages = [t.untyped_storage() for t in self.grads + self.out]
+        self._tail = (self.norm.data_ptr(), self.workspace.data_ptr(), self.workspace.numel() * 4)
 
 
 def grad_norm(grads) -> torch.Tensor:
     """The L2 norm over all elements of all tensors (a ``GradList`` or a
     sequence of tensors), as a 1-element fp32 device tensor."""
     g = grads if isinstance(grads, GradList) else GradList(grads)
-    _check(lib().fp8_grad_norm(len(g.grads), g.table, *g._tail()), "fp8_grad_norm")
+    _check(lib().fp8_grad_norm(len(g.grads), g.table, *g._tail, _stream()), "fp8_grad_norm")
     return g.norm
 
 
@@ -277,5 +309,5 @@ def clip_grads(grads, max_norm: float) -> torch.Tensor:
     """Scales every tensor by min(1, max_norm / (norm + 1e-6)), norm the L2 norm
     over all of them, and returns the norm (device, 1 element)."""
     g = grads if isinstance(grads, GradList) else GradList(grads)
-    _check(lib().fp8_clip_grads(len(g.grads), g.table, float(max_norm), *g._tail()), "fp8_clip_grads")
+    _check(lib().fp8_clip_grads(len(g.grads), g.table, float(max_norm), *g._tail, _stream()), "fp8_clip_grads")
     return g.norm
