@@ -298,7 +298,8 @@ static bool overlaps(const void* a, int64_t na, const void* b, int64_t nb) {
 }
 
 // The epilogue arguments the three linear GEMMs share: checks them, fills the
-// parameters and picks the epilogue (without a residual the forward GEMM's).
+// parameters and picks the epilogue (without a residual, on aligned rows, the
+// forward GEMM's).
 struct LinearArgs {
     const void* bias;
     int act;
@@ -356,11 +357,11 @@ static int fill_linear(const LinearArgs& a, GemmParams& p) {
     p.bias = a.bias;
     p.res = a.residual;
     p.ldr = a.ldr;
-    if (!a.residual && a.act == FP8LL_ACT_NONE) return a.bias ? kEpiBias : kEpiNone;
-    if (!a.residual) return kEpiBiasGelu;
     const bool gelu = a.act == FP8LL_ACT_GELU;
-    if (aligned16(a.residual) && a.ldr % 8 == 0 && p.N % 8 == 0)
-        return gelu ? kEpiLinearGelu : kEpiLinear;
+    if (p.N % 8 == 0) {  // rows of the output 16-byte aligned
+        if (!a.residual) return gelu ? kEpiBiasGelu : a.bias ? kEpiBias : kEpiNone;
+        if (aligned16(a.residual) && a.ldr % 8 == 0) return gelu ? kEpiLinearGelu : kEpiLinear;
+    }
     return gelu ? kEpiLinearGeluAny : kEpiLinearAny;
 }
 
@@ -977,14 +978,14 @@ int fp8_gemm_linear(int64_t M, int64_t N, int64_t K, const fp8ll_operand_t* A, c
     int rc = current_device(&dev);
     if (rc != FP8LL_OK) return rc;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (rows_kernel_taken(M, N, K, dev->num_sms)) {
+    if (rows_kernel_taken(M, N, K)) {
         RowsParams r = rows_params(M, N, K, A->fmt, B->fmt, args, dev);
         r.idesc |= 1u << 4;  // fp32 accumulators
         RowsMaps rm;
         if (!encode_operand(B, N, K, kRowsFeatures, &rm.w, &rm.sw) ||
             !encode_operand(A, M, K, static_cast<uint32_t>(rows_tokens(M)), &rm.x, &rm.sx))
             return FP8LL_ERR_LAUNCH;
-        return launch_gemm_rows(rm, r, kRecipeBlock, s, dev->num_sms) == 0 ? FP8LL_OK : FP8LL_ERR_LAUNCH;
+        return launch_gemm_rows(rm, r, kRecipeBlock, s) == 0 ? FP8LL_OK : FP8LL_ERR_LAUNCH;
     }
     TensorMaps maps;
     if (!encode_operand(A, M, K, 128, &maps.a, &maps.sa) || !encode_operand(B, N, K, kTileN, &maps.b, &maps.sb))
@@ -1017,7 +1018,7 @@ int fp8_mx_gemm_linear(int64_t M, int64_t N, int64_t K, const fp8ll_mx_operand_t
     if (!valid_k(K) || !valid_mx_operand(A, M, K) || !valid_mx_operand(B, N, K)) return FP8LL_ERR_INVALID_ARG;
     int rc = current_device(&dev);
     if (rc != FP8LL_OK) return rc;
-    if (rows_kernel_taken(M, N, K, dev->num_sms)) {
+    if (rows_kernel_taken(M, N, K)) {
         RowsParams r = rows_params(M, N, K, A->fmt, B->fmt, args, dev);
         r.idesc |= 1u << 23;  // UE8M0 scales
         r.groups_w = mx_sf_groups(N);
@@ -1028,7 +1029,7 @@ int fp8_mx_gemm_linear(int64_t M, int64_t N, int64_t K, const fp8ll_mx_operand_t
             !encode_sf_atoms(B->sf, (K / 128) * r.groups_w, 1, &rm.sw) ||
             !encode_sf_atoms(A->sf, (K / 128) * r.groups_x, 1, &rm.sx))
             return FP8LL_ERR_LAUNCH;
-        return launch_gemm_rows(rm, r, kRecipeMx, reinterpret_cast<cudaStream_t>(stream), dev->num_sms) == 0
+        return launch_gemm_rows(rm, r, kRecipeMx, reinterpret_cast<cudaStream_t>(stream)) == 0
                    ? FP8LL_OK
                    : FP8LL_ERR_LAUNCH;
     }
@@ -1049,7 +1050,7 @@ int fp8_tensor_gemm_linear(int64_t M, int64_t N, int64_t K, const fp8ll_tensor_o
     if (!valid_k(K) || !valid_tensor_operand(A, M, K) || !valid_tensor_operand(B, N, K)) return FP8LL_ERR_INVALID_ARG;
     int rc = current_device(&dev);
     if (rc != FP8LL_OK) return rc;
-    if (rows_kernel_taken(M, N, K, dev->num_sms)) {
+    if (rows_kernel_taken(M, N, K)) {
         RowsParams r = rows_params(M, N, K, A->fmt, B->fmt, args, dev);
         r.idesc |= 1u << 4;  // fp32 accumulators
         r.tsw = B->scale;
@@ -1058,7 +1059,7 @@ int fp8_tensor_gemm_linear(int64_t M, int64_t N, int64_t K, const fp8ll_tensor_o
         if (!encode_codes(B->q, B->ld_q, N, K, kRowsFeatures, &rm.w) ||
             !encode_codes(A->q, A->ld_q, M, K, static_cast<uint32_t>(rows_tokens(M)), &rm.x))
             return FP8LL_ERR_LAUNCH;
-        return launch_gemm_rows(rm, r, kRecipeTensor, reinterpret_cast<cudaStream_t>(stream), dev->num_sms) == 0
+        return launch_gemm_rows(rm, r, kRecipeTensor, reinterpret_cast<cudaStream_t>(stream)) == 0
                    ? FP8LL_OK
                    : FP8LL_ERR_LAUNCH;
     }

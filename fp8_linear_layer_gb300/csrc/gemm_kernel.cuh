@@ -104,8 +104,26 @@ constexpr bool uses_z() {
            EPI == kEpiLinearGelu;  // the linear epilogues stage an aligned residual in Z's place
 }
 template <int EPI>
+constexpr bool is_linear() {
+    return EPI == kEpiLinear || EPI == kEpiLinearGelu || EPI == kEpiLinearAny || EPI == kEpiLinearGeluAny;
+}
+template <int EPI>
+constexpr bool is_gelu_linear() {
+    return EPI == kEpiLinearGelu || EPI == kEpiLinearGeluAny;
+}
+template <int EPI>
+constexpr bool is_any_linear() {
+    return EPI == kEpiLinearAny || EPI == kEpiLinearGeluAny;
+}
+
+// the linear epilogue of any sizes stages 8 rows x 128 columns per epilogue warp
+template <int EPI>
+constexpr size_t any_stage_bytes() {
+    return is_any_linear<EPI>() ? static_cast<size_t>(kEpiWarps) * 8 * 68 * 4 : 0;
+}
+template <int EPI>
 constexpr size_t smem_bytes() {
-    return sizeof(SmemLayout) + (uses_z<EPI>() ? kZBytes : 0) + 1024;
+    return sizeof(SmemLayout) + (uses_z<EPI>() ? kZBytes : any_stage_bytes<EPI>()) + 1024;
 }
 static_assert(smem_bytes<kEpiDgelu>() <= 232448, "shared memory budget");
 
@@ -479,25 +497,127 @@ __device__ __forceinline__ void store_dgrad(const GemmParams& p, int row0, int c
 //   kResVector  rows of output and residual 16-byte aligned: read as 16-byte
 //               vectors and put in fragment order by the quad transpose, which
 //               is its own inverse.
-//   kResAny     any sizes and alignment, in pairs of elements or one by one.
+//   kResAny     any sizes and alignment, and no residual: eight rows of the
+//               warp's 128 columns at a time go through shared memory, so that
+//               rows of the residual, of Y and of Z are read and written in
+//               words along the row whatever their alignment (element by element
+//               from the fragments, 1594 x 4399 over 1664 on MXFP8 took 68 us).
 // A tile's residual is read by the CTA that stores the same tile of the output,
 // each element before the store of it: out may be the residual's own buffer.
 enum ResMode : int { kResStaged = 0, kResVector = 1, kResAny = 2 };
 
-// elements off and off + 1 of a bf16 array where `one` and `two` say they
-// exist; `pairs`: every offset is even and the array 4-byte aligned
-__device__ __forceinline__ uint32_t load_pair(const uint16_t* p, int64_t off, bool one, bool two, bool pairs) {
-    if (pairs) return one ? *reinterpret_cast<const uint32_t*>(p + off) : 0u;
-    return (one ? static_cast<uint32_t>(p[off]) : 0u) | (two ? static_cast<uint32_t>(p[off + 1]) << 16 : 0u);
+constexpr int kAnyRowWords = 68;  // 64 words of a row, padded: the fragments' eight rows fall in distinct banks
+constexpr uint32_t kAnyWarpBytes = 8 * kAnyRowWords * 4;
+static_assert(any_stage_bytes<kEpiLinearAny>() == kEpiWarps * kAnyWarpBytes, "staging of all epilogue warps");
+
+// Eight rows (those below `rows`) of n elements of type T -- pairs of bf16 where
+// every row is 4-byte aligned, else single ones -- between global memory and the
+// stage, by a whole warp along the rows.  All loads of four rows are in flight
+// before the first is stored.
+template <typename T>
+__device__ __forceinline__ void load_rows(const T* g, int64_t ld, int rows, int n, int lane, uint32_t* stage) {
+    constexpr int kPer = 8 / sizeof(T);  // 2 words or 4 halves per lane and row
+    T* st = reinterpret_cast<T*>(stage);
+#pragma unroll
+    for (int i0 = 0; i0 < 8; i0 += 4) {
+        T v[4][kPer];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < kPer; ++j)
+                v[i][j] = i0 + i < rows && lane + 32 * j < n ? g[(i0 + i) * ld + lane + 32 * j] : T(0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < kPer; ++j)
+                st[(i0 + i) * (kAnyRowWords * 4 / sizeof(T)) + lane + 32 * j] = v[i][j];
+    }
 }
 
-__device__ __forceinline__ void store_pair(uint16_t* p, int64_t off, bool one, bool two, bool pairs, uint32_t w) {
-    if (pairs) {
-        if (one) *reinterpret_cast<uint32_t*>(p + off) = w;
-        return;
+template <typename T>
+__device__ __forceinline__ void store_rows(T* g, int64_t ld, int rows, int n, int lane, const uint32_t* stage) {
+    constexpr int kPer = 8 / sizeof(T);
+    const T* st = reinterpret_cast<const T*>(stage);
+#pragma unroll
+    for (int i0 = 0; i0 < 8; i0 += 4) {
+        T v[4][kPer];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) v[i][j] = st[(i0 + i) * (kAnyRowWords * 4 / sizeof(T)) + lane + 32 * j];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < kPer; ++j)
+                if (i0 + i < rows && lane + 32 * j < n) g[(i0 + i) * ld + lane + 32 * j] = v[i][j];
     }
-    if (one) p[off] = static_cast<uint16_t>(w & 0xFFFFu);
-    if (two) p[off + 1] = static_cast<uint16_t>(w >> 16);
+}
+
+// The epilogue of one warp for any sizes; stage: its kAnyWarpBytes of shared
+// memory.  The bias is added to the accumulators in place.
+template <bool GELU>
+__device__ __forceinline__ void store_linear_any(const GemmParams& p, int row0, int col0,
+                                                 uint64_t (&acc)[4 * kChunks], int lane, uint32_t* stage) {
+    const uint16_t* bias = static_cast<const uint16_t*>(p.bias);
+    const uint16_t* res = static_cast<const uint16_t*>(p.res);
+    const int g8 = lane >> 2, cq = lane & 3;
+    const int cbase = col0 - 2 * cq, rbase = row0 - g8;  // the warp's first column and row
+    const int n = p.N - cbase < kHalfN ? p.N - cbase : kHalfN;
+    if (n <= 0 || rbase >= p.M) return;
+    const bool out_words = (p.N & 1) == 0;
+    const bool res_words = out_words && (p.ldr & 1) == 0 && (reinterpret_cast<uintptr_t>(res) & 3u) == 0;
+    if (bias) {
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+            const int col = col0 + 8 * c;
+            const float b0 = col < p.N ? __uint_as_float(static_cast<uint32_t>(bias[col]) << 16) : 0.0f;
+            const float b1 = col + 1 < p.N ? __uint_as_float(static_cast<uint32_t>(bias[col + 1]) << 16) : 0.0f;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float2 a = unpack_f32x2(acc[4 * c + r]);
+                acc[4 * c + r] = pack_f32x2(a.x + b0, a.y + b1);
+            }
+        }
+    }
+    auto put = [&](void* base, int row, int rows) {
+        if (out_words)
+            store_rows(static_cast<uint32_t*>(base) + (static_cast<int64_t>(row) * p.N + cbase) / 2, p.N / 2, rows, n / 2,
+                       lane, stage);
+        else
+            store_rows(static_cast<uint16_t*>(base) + static_cast<int64_t>(row) * p.N + cbase, p.N, rows, n, lane, stage);
+        __syncwarp();
+    };
+    uint32_t* mine = stage + g8 * kAnyRowWords + cq;  // the thread's word of chunk c: mine[4 c]
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const int row = rbase + 8 * r, rows = p.M - row;  // of the eight that exist
+        if (rows <= 0) break;
+        if (res) {
+            if (res_words)
+                load_rows(reinterpret_cast<const uint32_t*>(res + row * p.ldr + cbase), p.ldr / 2, rows, n / 2, lane, stage);
+            else
+                load_rows(res + row * p.ldr + cbase, p.ldr, rows, n, lane, stage);
+            __syncwarp();
+        }
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+            const uint32_t rw = res ? mine[4 * c] : 0u;
+            const float2 z = unpack_f32x2(acc[4 * c + r]);
+            const float2 y = GELU ? gelu_tanh2(z.x, z.y) : z;
+            mine[4 * c] = pack_bf16x2(y.x + bf16_lo(rw), y.y + bf16_hi(rw));
+        }
+        __syncwarp();
+        put(p.out, row, rows);
+        if (GELU && p.aux) {
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) {
+                const float2 z = unpack_f32x2(acc[4 * c + r]);
+                mine[4 * c] = pack_bf16x2(z.x, z.y);
+            }
+            __syncwarp();
+            put(p.aux, row, rows);
+        }
+    }
 }
 
 template <bool GELU, int RES>
@@ -511,18 +631,13 @@ __device__ __forceinline__ void store_linear(const GemmParams& p, int row0, int 
     const int cbase = col0 - 2 * cq;
     // bias pairs: of all chunks at once where the registers allow it, so that
     // their loads are in flight together, else of one group of four at a time
-    const bool pairs = (p.N & 1) == 0;
-    const bool res_pairs = pairs && (p.ldr & 1) == 0 && (reinterpret_cast<uintptr_t>(res) & 3u) == 0;
     constexpr int kAhead = RES == kResStaged ? kChunks : 4;
     uint32_t bw[kAhead];
     auto load_bias = [&](int c0) {
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
             const int col = col0 + 8 * (c0 + i);
-            if (RES == kResAny)
-                bw[i] = bias ? load_pair(bias, col, col < p.N, col + 1 < p.N, pairs) : 0u;
-            else
-                bw[i] = bias && col < p.N ? __ldg(reinterpret_cast<const unsigned int*>(bias + col)) : 0u;
+            bw[i] = bias && col < p.N ? __ldg(reinterpret_cast<const unsigned int*>(bias + col)) : 0u;
         }
     };
     if (kAhead == kChunks) load_bias(0);
@@ -550,11 +665,6 @@ __device__ __forceinline__ void store_linear(const GemmParams& p, int row0, int 
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 if (RES == kResVector) rw[r] = yw[r][j];
-                if (RES == kResAny) {
-                    const int col = col0 + 8 * c, row = row0 + 8 * r;
-                    const bool in = row < p.M;
-                    rw[r] = load_pair(res, row * p.ldr + col, in && col < p.N, in && col + 1 < p.N, res_pairs);
-                }
                 const float2 a = unpack_f32x2(acc[4 * c + r]);
                 const uint32_t b = bw[c % kAhead];
                 const float z0 = a.x + bf16_lo(b), z1 = a.y + bf16_hi(b);
@@ -566,17 +676,6 @@ __device__ __forceinline__ void store_linear(const GemmParams& p, int row0, int 
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int row = row0 + 8 * r;
-            if (RES == kResAny) {
-                if (row >= p.M) continue;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int col = col0 + 8 * (4 * g + j);
-                    const int64_t off = static_cast<int64_t>(row) * p.N + col;
-                    store_pair(out, off, col < p.N, col + 1 < p.N, pairs, yw[r][j]);
-                    if (aux) store_pair(aux, off, col < p.N, col + 1 < p.N, pairs, zw[r][j]);
-                }
-                continue;
-            }
             quad_transpose(yw[r], cq);
             if (aux) quad_transpose(zw[r], cq);
             if (row >= p.M || vcol >= p.N) continue;
@@ -587,23 +686,10 @@ __device__ __forceinline__ void store_linear(const GemmParams& p, int row0, int 
     }
 }
 
-template <int EPI>
-constexpr bool is_linear() {
-    return EPI == kEpiLinear || EPI == kEpiLinearGelu || EPI == kEpiLinearAny || EPI == kEpiLinearGeluAny;
-}
-template <int EPI>
-constexpr bool is_gelu_linear() {
-    return EPI == kEpiLinearGelu || EPI == kEpiLinearGeluAny;
-}
-template <int EPI>
-constexpr bool is_any_linear() {
-    return EPI == kEpiLinearAny || EPI == kEpiLinearGeluAny;
-}
-
 // asks for the residual of a thread's tile rows in L2 while the K loop runs
 // (each lane of a quad one of the quad's four rows, 128 columns: three lines)
 __device__ __forceinline__ void prefetch_residual(const GemmParams& p, int prow, int pc0) {
-    if (prow < p.M && pc0 < p.N) {
+    if (p.res && prow < p.M && pc0 < p.N) {
         const uint16_t* row = static_cast<const uint16_t*>(p.res) + prow * p.ldr;
         const int pc1 = min(pc0 + kHalfN - 1, p.N - 1);
         prefetch_l2(row + pc0);
@@ -731,7 +817,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = sm.tmem_base;
-    uint8_t* const zs = reinterpret_cast<uint8_t*>(&sm) + sizeof(SmemLayout);  // Z tile (dgrad only)
+    uint8_t* const zs = reinterpret_cast<uint8_t*>(&sm) + sizeof(SmemLayout);  // Z, residual or output staging
     const bool z_staged = uses_z<EPI>() && p.z_tma != 0;
 
     if (warp < kFirstEpiWarp) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtrl));
@@ -964,7 +1050,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 store_fprop<EPI>(p, row0, col0, acc);
             } else if (is_linear<EPI>()) {
                 if (is_any_linear<EPI>()) {
-                    store_linear<is_gelu_linear<EPI>(), kResAny>(p, row0, col0, acc, g8, nullptr);
+                    store_linear_any<is_gelu_linear<EPI>()>(p, row0, col0, acc, lane,
+                                                            reinterpret_cast<uint32_t*>(zs + ew * kAnyWarpBytes));
                 } else {
                     ok = mbar_wait_warp(smem_addr(&sm.zfull), zph, budget);
                     if (!ok) break;

@@ -67,8 +67,9 @@ struct __align__(1024) MxSmem {
     uint64_t sf_drain;             // leader: the copier's last copies completed
     uint32_t tmem_base;
 };
-constexpr size_t kMxSmemBytes = sizeof(MxSmem) + 1024;
-static_assert(kMxSmemBytes <= 232448, "shared memory budget");
+template <int EPI>
+constexpr size_t kMxSmemBytes = sizeof(MxSmem) + any_stage_bytes<EPI>() + 1024;
+static_assert(kMxSmemBytes<kEpiLinearAny> <= 232448 && sizeof(MxSmem) % 16 == 0, "shared memory budget");
 
 // no-swizzle shared-memory descriptor for a 32-row x 16-byte scale atom
 // (8-row x 16-byte core matrices, 128 bytes apart)
@@ -338,8 +339,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             } else if (EPI == kEpiNone || EPI == kEpiBias || EPI == kEpiBiasGelu) {
                 store_fprop<EPI>(p, row0, col0, acc);
             } else if (is_linear<EPI>()) {
-                store_linear<is_gelu_linear<EPI>(), is_any_linear<EPI>() ? kResAny : kResVector>(p, row0, col0, acc, g8,
-                                                                                                  nullptr);
+                if (is_any_linear<EPI>())
+                    store_linear_any<is_gelu_linear<EPI>()>(
+                        p, row0, col0, acc, lane,
+                        reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(&sm) + sizeof(MxSmem) + ew * kAnyWarpBytes));
+                else
+                    store_linear<is_gelu_linear<EPI>(), kResVector>(p, row0, col0, acc, g8, nullptr);
             } else {
                 float* band = (EPI == kEpiDgeluBgrad) ? p.workspace + (static_cast<int64_t>(m0 / kBM) * 4 + q) * p.N
                                                       : nullptr;
@@ -374,12 +379,12 @@ int launch_mx_impl(const TensorMaps& maps, const GemmParams& p, cudaStream_t str
         cudaFuncAttributes attr;
         if (cudaFuncGetAttributes(&attr, kern) != cudaSuccess || attr.numRegs != kLaunchRegs) return -3;
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(kMxSmemBytes)) != cudaSuccess)
+                                 static_cast<int>(kMxSmemBytes<EPI>)) != cudaSuccess)
             return -3;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(2, 1, 1);
         cfg.blockDim = dim3(kThreads, 1, 1);
-        cfg.dynamicSmemBytes = kMxSmemBytes;
+        cfg.dynamicSmemBytes = kMxSmemBytes<EPI>;
         int n = 0;
         if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
             cudaGetLastError();
@@ -392,7 +397,7 @@ int launch_mx_impl(const TensorMaps& maps, const GemmParams& p, cudaStream_t str
     }
     const int pairs = pairs_on[dev];
     const int grid = 2 * (p.total_tiles < pairs ? p.total_tiles : pairs);
-    kern<<<grid, kThreads, kMxSmemBytes, stream>>>(maps, p);
+    kern<<<grid, kThreads, kMxSmemBytes<EPI>, stream>>>(maps, p);
     return cudaGetLastError() == cudaSuccess ? 0 : -3;
 }
 

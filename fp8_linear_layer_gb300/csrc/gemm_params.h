@@ -21,7 +21,7 @@ enum EpiKind : int {
     // Z = C + bias; Y = act(Z) + residual, act none or gelu; bias and aux = Z optional
     kEpiLinear = 7,       // the residual's and the output's rows 16-byte aligned
     kEpiLinearGelu = 8,
-    kEpiLinearAny = 9,    // any sizes and alignment
+    kEpiLinearAny = 9,    // any sizes and alignment, residual optional
     kEpiLinearGeluAny = 10,
 };
 
@@ -60,7 +60,7 @@ struct GemmParams {
     uint8_t* qout;        // kEpiDgeluQuant: e5m2 codes of the bf16 dZ, [M][N]
     float* qscale;        // kEpiDgeluQuant: their scales, [N/128][qsld]
     int64_t qsld;
-    const void* res;      // kEpiLinear*: bf16 residual [M][ldr]
+    const void* res;      // kEpiLinear*: bf16 residual [M][ldr] (null allowed with kEpiLinear*Any)
     int64_t ldr;
     GroupEntry groups[kMaxGroups];
 };

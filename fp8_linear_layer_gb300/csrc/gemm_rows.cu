@@ -19,6 +19,7 @@
 //               of B per thread, all tokens; otherwise read the accumulator
 //               once at the end.
 //   all warps   epilogue: a thread takes two neighbouring features.
+#include <atomic>
 #include <cuda_runtime.h>
 
 #include "common.cuh"
@@ -37,7 +38,7 @@ constexpr int rows_stages() {
     return NT == 64 ? 4 : 5;
 }
 template <int NT>
-constexpr int rows_ctas_per_sm() {  // as rows_cluster counts them
+constexpr int rows_ctas_per_sm() {
     return NT == 128 ? 1 : 2;
 }
 
@@ -434,8 +435,51 @@ int launch_rows_recipe(const RowsMaps& maps, const RowsParams& p, cudaStream_t s
 
 }  // namespace
 
-int launch_gemm_rows(const RowsMaps& maps, RowsParams p, int recipe, cudaStream_t stream, int num_sms) {
-    p.cluster = rows_cluster(p.M, p.N, p.nkb, num_sms);
+// CTAs of clusters of c that run at once: the GPCs' sizes leave SMs over (of 152,
+// 120 take part in clusters of 8 CTAs that fill an SM each)
+template <int NT>
+static int rows_slots(int c) {
+    static std::atomic<int> known[64][4];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    std::atomic<int>& slot = known[dev][c == 1 ? 0 : c == 2 ? 1 : c == 4 ? 2 : 3];
+    int n = slot.load(std::memory_order_relaxed);
+    if (n == 0) {
+        auto kern = gemm_rows_kernel<kRecipeBlock, NT>;
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(rows_smem_bytes<NT>())) != cudaSuccess)
+            return 0;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(c));
+        cfg.blockDim = dim3(kRowsThreads);
+        cfg.dynamicSmemBytes = rows_smem_bytes<NT>();
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = static_cast<unsigned>(c);
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
+            cudaGetLastError();
+            return 0;
+        }
+        n *= c;
+        slot.store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
+int rows_cluster(int64_t M, int64_t N, int64_t nkb) {
+    const int nt = rows_tokens(M);
+    const int64_t tiles = (N + kRowsFeatures - 1) / kRowsFeatures * ((M + nt - 1) / nt);
+    int c = 1;
+    while (c < 8 && nkb >= 4 * c && tiles * 2 * c <= (nt == 128 ? rows_slots<128>(2 * c) : rows_slots<64>(2 * c))) c *= 2;
+    return c;
+}
+
+int launch_gemm_rows(const RowsMaps& maps, RowsParams p, int recipe, cudaStream_t stream) {
+    p.cluster = rows_cluster(p.M, p.N, p.nkb);
     switch (recipe) {
         case kRecipeBlock: return launch_rows_recipe<kRecipeBlock>(maps, p, stream);
         case kRecipeMx: return launch_rows_recipe<kRecipeMx>(maps, p, stream);

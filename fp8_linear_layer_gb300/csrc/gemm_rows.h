@@ -11,16 +11,9 @@ constexpr int kRowsFeatures = 128;  // rows of B per output tile: the MMA's M
 // tokens (rows of A) per output tile: the MMA's N
 inline int rows_tokens(int64_t M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128; }
 
-// CTAs that share the K blocks of an output tile: as many as run at once (two
-// per SM, one at 128 tokens) with two blocks each, at most 8
-inline int rows_cluster(int64_t M, int64_t N, int64_t nkb, int num_sms) {
-    const int nt = rows_tokens(M);
-    const int64_t tiles = (N + kRowsFeatures - 1) / kRowsFeatures * ((M + nt - 1) / nt);
-    const int64_t slots = static_cast<int64_t>(num_sms) * (nt == 128 ? 1 : 2);
-    int c = 1;
-    while (c < 8 && tiles * 2 * c <= slots && nkb >= 4 * c) c *= 2;
-    return c;
-}
+// CTAs that share the K blocks of an output tile: as many as run at once with
+// two blocks each, at most 8
+int rows_cluster(int64_t M, int64_t N, int64_t nkb);
 
 // Whether this kernel is taken.  Up to 64 tokens always (1x128 / MXFP8 at 64
 // tokens: 17.6 / 16.5 us against the tile kernels' 24.2 / 18.5 at 14336 features
@@ -29,9 +22,9 @@ inline int rows_cluster(int64_t M, int64_t N, int64_t nkb, int num_sms) {
 // few SMs: 256 x 2112 over 7168 takes 15.3 / 12.4 us against 37.3 / 25.0, 256 x
 // 4096 over 14336 40.1 / 30.4 against 70.5 / 44.7; a split in two of a short K
 // does not pay (256 x 4096 over 1024: 11.4 / 10.2 against 9.4 / 8.5).
-inline bool rows_kernel_taken(int64_t M, int64_t N, int64_t K, int num_sms) {
+inline bool rows_kernel_taken(int64_t M, int64_t N, int64_t K) {
     if (M <= 64) return true;
-    const int c = rows_cluster(M, N, K / 128, num_sms);
+    const int c = rows_cluster(M, N, K / 128);
     return c >= 4 || (c == 2 && K / 128 >= 32);
 }
 
@@ -58,6 +51,6 @@ struct RowsParams {
     uint16_t* aux;          // bf16 [M][N] or null
 };
 
-int launch_gemm_rows(const RowsMaps& maps, RowsParams p, int recipe, cudaStream_t stream, int num_sms);
+int launch_gemm_rows(const RowsMaps& maps, RowsParams p, int recipe, cudaStream_t stream);
 
 }  // namespace fp8ll

@@ -42,8 +42,9 @@ struct __align__(1024) TpSmem {
     uint64_t drain;
     uint32_t tmem_base;
 };
-constexpr size_t kTpSmemBytes = sizeof(TpSmem) + 1024;
-static_assert(kTpSmemBytes <= 232448, "shared memory budget");
+template <int EPI>
+constexpr size_t kTpSmemBytes = sizeof(TpSmem) + any_stage_bytes<EPI>() + 1024;
+static_assert(kTpSmemBytes<kEpiLinearAny> <= 232448 && sizeof(TpSmem) % 16 == 0, "shared memory budget");
 
 // pair-tile index -> (pair-row tile, n tile): bands of kTpRaster pair rows
 // walked column by column, as decode_tile does for 128-row tiles
@@ -257,8 +258,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             } else if (EPI == kEpiNone || EPI == kEpiBias || EPI == kEpiBiasGelu) {
                 store_fprop<EPI>(p, row0, col0, acc);
             } else if (is_linear<EPI>()) {
-                store_linear<is_gelu_linear<EPI>(), is_any_linear<EPI>() ? kResAny : kResVector>(p, row0, col0, acc, g8,
-                                                                                                  nullptr);
+                if (is_any_linear<EPI>())
+                    store_linear_any<is_gelu_linear<EPI>()>(
+                        p, row0, col0, acc, lane,
+                        reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(&sm) + sizeof(TpSmem) + ew * kAnyWarpBytes));
+                else
+                    store_linear<is_gelu_linear<EPI>(), kResVector>(p, row0, col0, acc, g8, nullptr);
             } else {
                 float* band = (EPI == kEpiDgeluBgrad) ? p.workspace + (static_cast<int64_t>(m0 / kBM) * 4 + q) * p.N
                                                       : nullptr;
@@ -293,12 +298,12 @@ int launch_tensor_impl(const TensorMaps& maps, const GemmParams& p, cudaStream_t
         cudaFuncAttributes attr;
         if (cudaFuncGetAttributes(&attr, kern) != cudaSuccess || attr.numRegs != kLaunchRegs) return -3;
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(kTpSmemBytes)) != cudaSuccess)
+                                 static_cast<int>(kTpSmemBytes<EPI>)) != cudaSuccess)
             return -3;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(2, 1, 1);
         cfg.blockDim = dim3(kThreads, 1, 1);
-        cfg.dynamicSmemBytes = kTpSmemBytes;
+        cfg.dynamicSmemBytes = kTpSmemBytes<EPI>;
         int n = 0;
         if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
             cudaGetLastError();
@@ -311,7 +316,7 @@ int launch_tensor_impl(const TensorMaps& maps, const GemmParams& p, cudaStream_t
     }
     const int pairs = pairs_on[dev];
     const int grid = 2 * (p.total_tiles < pairs ? p.total_tiles : pairs);
-    kern<<<grid, kThreads, kTpSmemBytes, stream>>>(maps, p);
+    kern<<<grid, kThreads, kTpSmemBytes<EPI>, stream>>>(maps, p);
     return cudaGetLastError() == cudaSuccess ? 0 : -3;
 }
 

@@ -59,7 +59,8 @@ def check(y, z, acc, S, bias, act, residual):
 
 
 SHAPES = [(1, 1, 128), (1, 256, 4096), (2, 40, 256), (3, 1000, 896), (8, 129, 1280), (9, 72, 2048), (16, 512, 7168),
-          (17, 264, 384), (33, 2110, 512), (64, 96, 1024), (100, 301, 640), (129, 264, 256), (300, 520, 384), (150, 200, 4096), (257, 129, 2048), (128, 1030, 4096)]
+          (17, 264, 384), (33, 2110, 512), (64, 96, 1024), (100, 301, 640), (129, 264, 256), (300, 520, 384), (150, 200, 4096), (257, 129, 2048), (128, 1030, 4096),
+          (800, 2051, 256), (1000, 1918, 128)]
 
 
 @pytest.mark.parametrize("recipe", RECIPES)
