@@ -1035,8 +1035,15 @@ int fp8_mx_gemm_linear(int64_t M, int64_t N, int64_t K, const fp8ll_mx_operand_t
     }
     rc = mx_setup(M, N, K, A, B, maps, p, &dev);
     if (rc != FP8LL_OK) return rc;
-    const int epi = fill_linear(args, p);
-    return launch_gemm_mx(maps, p, epi, reinterpret_cast<cudaStream_t>(stream)) == 0 ? FP8LL_OK : FP8LL_ERR_LAUNCH;
+    int epi = fill_linear(args, p);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (launch_gemm_mx_splits(p)) {
+        if (epi < kEpiLinear) epi = args.act == FP8LL_ACT_GELU ? kEpiLinearGeluAny : kEpiLinearAny;
+        rc = launch_gemm_mx_split(maps, p, epi, s);
+    } else {
+        rc = launch_gemm_mx(maps, p, epi, s);
+    }
+    return rc == 0 ? FP8LL_OK : FP8LL_ERR_LAUNCH;
 }
 
 int fp8_tensor_gemm_linear(int64_t M, int64_t N, int64_t K, const fp8ll_tensor_operand_t* A,
@@ -1065,9 +1072,15 @@ int fp8_tensor_gemm_linear(int64_t M, int64_t N, int64_t K, const fp8ll_tensor_o
     }
     rc = tensor_setup(M, N, K, A, B, maps, p, &dev);
     if (rc != FP8LL_OK) return rc;
-    const int epi = fill_linear(args, p);
-    return launch_gemm_tensor(maps, p, epi, reinterpret_cast<cudaStream_t>(stream)) == 0 ? FP8LL_OK
-                                                                                         : FP8LL_ERR_LAUNCH;
+    int epi = fill_linear(args, p);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (launch_gemm_tensor_splits(p)) {
+        if (epi < kEpiLinear) epi = args.act == FP8LL_ACT_GELU ? kEpiLinearGeluAny : kEpiLinearAny;
+        rc = launch_gemm_tensor_split(maps, p, epi, s);
+    } else {
+        rc = launch_gemm_tensor(maps, p, epi, s);
+    }
+    return rc == 0 ? FP8LL_OK : FP8LL_ERR_LAUNCH;
 }
 
 }  // extern "C"

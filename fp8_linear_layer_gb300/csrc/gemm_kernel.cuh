@@ -555,7 +555,7 @@ __device__ __forceinline__ void store_rows(T* g, int64_t ld, int rows, int n, in
 
 // The epilogue of one warp for any sizes; stage: its kAnyWarpBytes of shared
 // memory.  The bias is added to the accumulators in place.
-template <bool GELU>
+template <bool GELU, int ROWS = 4>
 __device__ __forceinline__ void store_linear_any(const GemmParams& p, int row0, int col0,
                                                  uint64_t (&acc)[4 * kChunks], int lane, uint32_t* stage) {
     const uint16_t* bias = static_cast<const uint16_t*>(p.bias);
@@ -573,7 +573,7 @@ __device__ __forceinline__ void store_linear_any(const GemmParams& p, int row0, 
             const float b0 = col < p.N ? __uint_as_float(static_cast<uint32_t>(bias[col]) << 16) : 0.0f;
             const float b1 = col + 1 < p.N ? __uint_as_float(static_cast<uint32_t>(bias[col + 1]) << 16) : 0.0f;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
+            for (int r = 0; r < ROWS; ++r) {
                 const float2 a = unpack_f32x2(acc[4 * c + r]);
                 acc[4 * c + r] = pack_f32x2(a.x + b0, a.y + b1);
             }
@@ -589,7 +589,7 @@ __device__ __forceinline__ void store_linear_any(const GemmParams& p, int row0, 
     };
     uint32_t* mine = stage + g8 * kAnyRowWords + cq;  // the thread's word of chunk c: mine[4 c]
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
+    for (int r = 0; r < ROWS; ++r) {
         const int row = rbase + 8 * r, rows = p.M - row;  // of the eight that exist
         if (rows <= 0) break;
         if (res) {
@@ -620,7 +620,8 @@ __device__ __forceinline__ void store_linear_any(const GemmParams& p, int row0, 
     }
 }
 
-template <bool GELU, int RES>
+// ROWS: of the thread's four rows row0 + 8 r, the first ROWS are there.
+template <bool GELU, int RES, int ROWS = 4>
 __device__ __forceinline__ void store_linear(const GemmParams& p, int row0, int col0,
                                              const uint64_t (&acc)[4 * kChunks], int g8, const uint8_t* rrow) {
     uint16_t* out = static_cast<uint16_t*>(p.out);
@@ -648,14 +649,14 @@ __device__ __forceinline__ void store_linear(const GemmParams& p, int row0, int 
         uint32_t yw[4][4], zw[4][4];  // [row][chunk]; yw holds the residual's pair until the sum replaces it
         if (RES == kResVector) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
+            for (int r = 0; r < ROWS; ++r) {
                 uint4 v = make_uint4(0, 0, 0, 0);
                 if (row0 + 8 * r < p.M && vcol < p.N)
                     v = *reinterpret_cast<const uint4*>(res + (row0 + 8 * r) * p.ldr + vcol);
                 yw[r][0] = v.x; yw[r][1] = v.y; yw[r][2] = v.z; yw[r][3] = v.w;
             }
 #pragma unroll
-            for (int r = 0; r < 4; ++r) quad_transpose(yw[r], cq);
+            for (int r = 0; r < ROWS; ++r) quad_transpose(yw[r], cq);
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -663,7 +664,7 @@ __device__ __forceinline__ void store_linear(const GemmParams& p, int row0, int 
             uint32_t rw[4];
             if (RES == kResStaged) load_z_smem(rrow, g8, c, rw);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
+            for (int r = 0; r < ROWS; ++r) {
                 if (RES == kResVector) rw[r] = yw[r][j];
                 const float2 a = unpack_f32x2(acc[4 * c + r]);
                 const uint32_t b = bw[c % kAhead];
@@ -674,7 +675,7 @@ __device__ __forceinline__ void store_linear(const GemmParams& p, int row0, int 
             }
         }
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
+        for (int r = 0; r < ROWS; ++r) {
             const int row = row0 + 8 * r;
             quad_transpose(yw[r], cq);
             if (aux) quad_transpose(zw[r], cq);

@@ -39,6 +39,7 @@
 // The per-tensor scaled GEMM (one scale per operand, no scale atoms) runs on
 // CTA pairs in gemm_tensor.cu.
 #include "gemm_kernel.cuh"
+#include "split_pair.cuh"
 
 namespace fp8ll {
 
@@ -66,7 +67,9 @@ struct __align__(1024) MxSmem {
     uint64_t sf_full[kMxStages];   // leader: stage s's scales are in both CTAs' tensor memory
     uint64_t sf_drain;             // leader: the copier's last copies completed
     uint32_t tmem_base;
+    int32_t failed;  // SPLIT 2: an epilogue wait of this CTA ran out
 };
+static_assert(sizeof(MxSmem::b) >= kSplitBytes, "a split tile's sums take the place of B's stages");
 template <int EPI>
 constexpr size_t kMxSmemBytes = sizeof(MxSmem) + any_stage_bytes<EPI>() + 1024;
 static_assert(kMxSmemBytes<kEpiLinearAny> <= 232448 && sizeof(MxSmem) % 16 == 0, "shared memory budget");
@@ -104,8 +107,10 @@ __device__ __forceinline__ void decode_mx_tile(const GemmParams& p, int t, int& 
     nt = r / bm;
 }
 
-template <int EPI>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+// SPLIT: pairs of a cluster that share a tile's K blocks (1, or 2 for the linear
+// epilogues: see split_pair.cuh)
+template <int EPI, int SPLIT>
+__global__ void __cluster_dims__(2 * SPLIT, 1, 1) __launch_bounds__(kThreads, 1)
     gemm_mx_kernel(const __grid_constant__ TensorMaps maps, const __grid_constant__ GemmParams p) {
     extern __shared__ uint8_t smem_raw[];
     MxSmem& sm = *reinterpret_cast<MxSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -113,11 +118,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const uint64_t budget = p.budget_ns;
-    const int nkb = p.groups[0].nkb;
-    const uint32_t rank = cluster_ctarank();
+    const uint32_t crank = cluster_ctarank();
+    const uint32_t rank = SPLIT == 1 ? crank : crank & 1u;          // within the pair
+    const uint32_t lead = SPLIT == 1 ? 0u : crank & ~1u;            // cluster rank of the pair's leader
+    const uint16_t pair_mask = static_cast<uint16_t>(0x3u << lead);
     const bool leader = rank == 0;
-    const int pair = blockIdx.x >> 1;
-    const int num_pairs = gridDim.x >> 1;
+    const int part = SPLIT == 1 ? 0 : static_cast<int>(crank >> 1);  // which share of the K blocks
+    const int kb_first = SPLIT == 1 ? 0 : p.groups[0].nkb * part / SPLIT;
+    const int nkb = SPLIT == 1 ? p.groups[0].nkb : p.groups[0].nkb * (part + 1) / SPLIT - kb_first;
+    const int pair = blockIdx.x / (2 * SPLIT);
+    const int num_pairs = gridDim.x / (2 * SPLIT);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kMxStages; ++s) {
@@ -127,6 +137,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         mbar_init(smem_addr(&sm.acc_full[0]), 1);
         mbar_init(smem_addr(&sm.acc_empty[0]), 2 * kEpiWarps);
         mbar_init(smem_addr(&sm.drain), 1);
+        if (SPLIT == 2) sm.failed = 0;
         for (int s = 0; s < kMxStages; ++s) mbar_init(smem_addr(&sm.sf_full[s]), 1);
         mbar_init(smem_addr(&sm.sf_drain), 1);
         fence_mbar_init();
@@ -140,6 +151,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     cluster_sync();
     tc_fence_after();
     const uint32_t tmem_base = sm.tmem_base;
+    bool exchanged = false;  // SPLIT 2: this warp has passed the cluster's exchange barrier
 
     if (warp < kFirstEpiWarp) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtrl));
     if (warp == 0) {
@@ -166,15 +178,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         }
                         const uint32_t fb = smem_addr(&sm.full[s]);
                         if (leader) mbar_arrive_expect_tx(fb, 2 * kMxStageBytes);
-                        const uint32_t fbl = mapa_shared(fb, 0);
-                        tma_load_2d_pair(smem_addr(sm.a[s]), &maps.a, fbl, kb * kBK, m0);
-                        tma_load_2d_pair(smem_addr(sm.b[s]), &maps.b, fbl, kb * kBK, nb0);
+                        const uint32_t fbl = mapa_shared(fb, lead);
+                        tma_load_2d_pair(smem_addr(sm.a[s]), &maps.a, fbl, (kb_first + kb) * kBK, m0);
+                        tma_load_2d_pair(smem_addr(sm.b[s]), &maps.b, fbl, (kb_first + kb) * kBK, nb0);
                         // scale atoms: rows of 128 words; A's atom of this CTA's 128-row group,
                         // both atoms of the tile's 256 rows of B
                         tma_load_2d_pair(smem_addr(sm.sfa[s]), &maps.sa, fbl, 0,
-                                         static_cast<int32_t>(kb * p.sfa_groups + 2 * mt + static_cast<int>(rank)));
+                                         static_cast<int32_t>((kb_first + kb) * p.sfa_groups + 2 * mt + static_cast<int>(rank)));
                         tma_load_2d_pair(smem_addr(sm.sfb[s]), &maps.sb, fbl, 0,
-                                         static_cast<int32_t>(kb * p.sfb_groups + 2 * nt));
+                                         static_cast<int32_t>((kb_first + kb) * p.sfb_groups + 2 * nt));
                         ++n_issued;
                         ring_advance<kMxStages>(s, ph);
                     }
@@ -231,8 +243,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             mma_mx_pair(tmem_base, adesc + 2u * k, bdesc + 2u * k, idesc, tsf, tsf + 4,
                                         (kb > 0 || k > 0) ? 1u : 0u);
                         }
-                        mma_commit_pair(smem_addr(&sm.empty[s]), 0x3);
-                        if (kb == nkb - 1) mma_commit_pair(smem_addr(&sm.acc_full[0]), 0x3);
+                        mma_commit_pair(smem_addr(&sm.empty[s]), pair_mask);
+                        if (kb == nkb - 1) mma_commit_pair(smem_addr(&sm.acc_full[0]), pair_mask);
                     }
                     __syncwarp();
                     ring_advance<kMxStages>(s, ph);
@@ -241,7 +253,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             if (!ok && lane == 0) record_status(p.status, kStatusTimeout);
             // every MMA of the pair completes before either CTA frees its memory
-            if (lane == 0) mma_commit_pair(smem_addr(&sm.drain), 0x3);
+            if (lane == 0) mma_commit_pair(smem_addr(&sm.drain), pair_mask);
             __syncwarp();
             mbar_wait(smem_addr(&sm.drain), 0, budget);
             __syncwarp();
@@ -265,7 +277,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         sf_copy_pair(tsf, smem_addr(sm.sfa[s]));
                         sf_copy_pair(tsf + 4, smem_addr(sm.sfb[s]));
                         sf_copy_pair(tsf + 8, smem_addr(sm.sfb[s] + 512));
-                        mma_commit_pair(smem_addr(&sm.sf_full[s]), 0x1);
+                        mma_commit_pair(smem_addr(&sm.sf_full[s]), static_cast<uint16_t>(1u << lead));
                     }
                     __syncwarp();
                     ring_advance<kMxStages>(s, ph);
@@ -273,7 +285,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             if (!ok && lane == 0) record_status(p.status, kStatusTimeout);
             // the copies complete before either CTA frees its tensor memory
-            if (lane == 0) mma_commit_pair(smem_addr(&sm.sf_drain), 0x1);
+            if (lane == 0) mma_commit_pair(smem_addr(&sm.sf_drain), static_cast<uint16_t>(1u << lead));
             __syncwarp();
             mbar_wait(smem_addr(&sm.sf_drain), 0, budget);
             __syncwarp();
@@ -286,10 +298,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int half = ew >> 2;
         const int g8 = lane >> 2;
         const int cq = lane & 3;
-        const uint32_t acc_empty_leader = mapa_shared(smem_addr(&sm.acc_empty[0]), 0);
+        const uint32_t acc_empty_leader = mapa_shared(smem_addr(&sm.acc_empty[0]), lead);
         uint32_t aph = 0;
         bool ok = true;
-        for (int t = pair; t < p.total_tiles && ok; t += num_pairs) {
+        for (int t = pair; t < p.total_tiles && ok; t += num_pairs) {  // SPLIT 2: one tile per cluster
             int mt, nt;
             decode_mx_tile(p, t, mt, nt);
             const int m0 = mt * kMxRows + static_cast<int>(rank) * kBM, n0 = nt * kBN;
@@ -329,10 +341,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             __syncwarp();
             mbar_arrive_remote_lane0(acc_empty_leader, lane);
             aph ^= 1u;
+            if (SPLIT == 2) {
+                split_send(acc, sm.b, ew * 32 + lane, part);
+                cluster_sync();
+                exchanged = true;
+                if (split_failed(&sm.failed, crank)) break;
+                split_add(acc, sm.b, ew * 32 + lane, part, crank);
+            }
             // the peer of a pair whose tile ends inside the leader's rows holds
             // only rows outside the matrix and stores nothing
             if (m0 >= p.M) continue;
-            const int row0 = m0 + q * 32 + g8;
+            const int row0 = m0 + q * 32 + g8 + 16 * part;
             const int col0 = n0 + half * kHalfN + 2 * cq;
             if (EPI == kEpiWgrad) {
                 store_wgrad(p, 0, row0, col0, acc);
@@ -340,11 +359,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 store_fprop<EPI>(p, row0, col0, acc);
             } else if (is_linear<EPI>()) {
                 if (is_any_linear<EPI>())
-                    store_linear_any<is_gelu_linear<EPI>()>(
+                    store_linear_any<is_gelu_linear<EPI>(), 4 / SPLIT>(
                         p, row0, col0, acc, lane,
                         reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(&sm) + sizeof(MxSmem) + ew * kAnyWarpBytes));
                 else
-                    store_linear<is_gelu_linear<EPI>(), kResVector>(p, row0, col0, acc, g8, nullptr);
+                    store_linear<is_gelu_linear<EPI>(), kResVector, 4 / SPLIT>(p, row0, col0, acc, g8, nullptr);
             } else {
                 float* band = (EPI == kEpiDgeluBgrad) ? p.workspace + (static_cast<int64_t>(m0 / kBM) * 4 + q) * p.N
                                                       : nullptr;
@@ -352,6 +371,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
         }
         if (!ok && lane == 0) record_status(p.status, kStatusTimeout);
+        if (SPLIT == 2 && !ok) sm.failed = 1;
+    }
+    if (SPLIT == 2 && !exchanged) {  // the other roles, and epilogue warps whose wait ran out, meet the exchange here
+        __syncwarp();
+        cluster_sync();
     }
 
     // neither CTA leaves (or frees its tensor memory) while the other may still
@@ -368,11 +392,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
 }
 
-template <int EPI>
-int launch_mx_impl(const TensorMaps& maps, const GemmParams& p, cudaStream_t stream) {
-    auto kern = gemm_mx_kernel<EPI>;
+// clusters of the kernel that run at once on the current device, configured on
+// first use; negative on failure
+template <int EPI, int SPLIT>
+int launch_mx_impl_slots() {
+    auto kern = gemm_mx_kernel<EPI, SPLIT>;
     static unsigned long long configured = 0;
-    static int pairs_on[64] = {0};  // resident CTA pairs per device
+    static int clusters_on[64] = {0};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return -3;
     if (!(configured & (1ull << dev))) {
@@ -382,7 +408,7 @@ int launch_mx_impl(const TensorMaps& maps, const GemmParams& p, cudaStream_t str
                                  static_cast<int>(kMxSmemBytes<EPI>)) != cudaSuccess)
             return -3;
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(2, 1, 1);
+        cfg.gridDim = dim3(2 * SPLIT, 1, 1);
         cfg.blockDim = dim3(kThreads, 1, 1);
         cfg.dynamicSmemBytes = kMxSmemBytes<EPI>;
         int n = 0;
@@ -390,15 +416,36 @@ int launch_mx_impl(const TensorMaps& maps, const GemmParams& p, cudaStream_t str
             cudaGetLastError();
             int sms = 0;
             if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return -3;
-            n = sms / 2;
+            n = sms / (2 * SPLIT);
         }
-        pairs_on[dev] = n;
+        clusters_on[dev] = n;
         configured |= 1ull << dev;
     }
-    const int pairs = pairs_on[dev];
-    const int grid = 2 * (p.total_tiles < pairs ? p.total_tiles : pairs);
-    kern<<<grid, kThreads, kMxSmemBytes<EPI>, stream>>>(maps, p);
+    return clusters_on[dev];
+}
+
+template <int EPI, int SPLIT = 1>
+int launch_mx_impl(const TensorMaps& maps, const GemmParams& p, cudaStream_t stream) {
+    const int slots = launch_mx_impl_slots<EPI, SPLIT>();
+    if (slots < 0) return -3;
+    // one tile per cluster where its K blocks are split
+    const int64_t clusters = SPLIT == 2 || p.total_tiles < slots ? p.total_tiles : slots;
+    gemm_mx_kernel<EPI, SPLIT><<<static_cast<unsigned>(2 * SPLIT * clusters), kThreads, kMxSmemBytes<EPI>, stream>>>(maps, p);
     return cudaGetLastError() == cudaSuccess ? 0 : -3;
+}
+
+bool launch_gemm_mx_splits(const GemmParams& p) {
+    return split_pays(p, launch_mx_impl_slots<kEpiLinear, 2>());
+}
+
+int launch_gemm_mx_split(const TensorMaps& maps, const GemmParams& p, int epi, cudaStream_t stream) {
+    switch (epi) {
+        case kEpiLinear: return launch_mx_impl<kEpiLinear, 2>(maps, p, stream);
+        case kEpiLinearGelu: return launch_mx_impl<kEpiLinearGelu, 2>(maps, p, stream);
+        case kEpiLinearAny: return launch_mx_impl<kEpiLinearAny, 2>(maps, p, stream);
+        case kEpiLinearGeluAny: return launch_mx_impl<kEpiLinearGeluAny, 2>(maps, p, stream);
+        default: return -3;
+    }
 }
 
 int launch_gemm_mx(const TensorMaps& maps, const GemmParams& p, int epi, cudaStream_t stream) {

@@ -46,6 +46,12 @@ int launch_gemm_linear(const TensorMaps& maps, const GemmParams& p, int epi, cud
 // (p.num_m_pairs, p.tiles_per_group in pair tiles) and size their own grids.
 int launch_gemm_mx(const TensorMaps& maps, const GemmParams& p, int epi, cudaStream_t stream);
 int launch_gemm_tensor(const TensorMaps& maps, const GemmParams& p, int epi, cudaStream_t stream);
+// The same with the K blocks of each tile split over two pairs, for the linear
+// epilogues: whether that pays for these sizes, and the launch.
+bool launch_gemm_mx_splits(const GemmParams& p);
+bool launch_gemm_tensor_splits(const GemmParams& p);
+int launch_gemm_mx_split(const TensorMaps& maps, const GemmParams& p, int epi, cudaStream_t stream);
+int launch_gemm_tensor_split(const TensorMaps& maps, const GemmParams& p, int epi, cudaStream_t stream);
 int launch_bgrad_finalize(const float* ws, int64_t num_bands, int64_t N, float* bgrad, cudaStream_t stream,
                           int num_sms);
 

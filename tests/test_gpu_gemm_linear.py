@@ -60,7 +60,8 @@ def check(y, z, acc, S, bias, act, residual):
 
 SHAPES = [(1, 1, 128), (1, 256, 4096), (2, 40, 256), (3, 1000, 896), (8, 129, 1280), (9, 72, 2048), (16, 512, 7168),
           (17, 264, 384), (33, 2110, 512), (64, 96, 1024), (100, 301, 640), (129, 264, 256), (300, 520, 384), (150, 200, 4096), (257, 129, 2048), (128, 1030, 4096),
-          (800, 2051, 256), (1000, 1918, 128)]
+          (800, 2051, 256), (1000, 1918, 128), (1000, 1000, 2048), (900, 1203, 4096),
+          (650, 1408, 2304)]
 
 
 @pytest.mark.parametrize("recipe", RECIPES)
@@ -186,9 +187,8 @@ def test_refusals(fp8):
 
 
 @pytest.mark.parametrize("recipe", RECIPES)
-@pytest.mark.parametrize("M", [5, 100, 3000])
-def test_a_starved_pipeline_times_out_and_writes_nothing(fp8, recipe, M):
-    N, K = 264, 1024
+@pytest.mark.parametrize("M,N,K", [(5, 264, 1024), (100, 264, 1024), (3000, 264, 1024), (1000, 1000, 2048)])
+def test_a_starved_pipeline_times_out_and_writes_nothing(fp8, recipe, M, N, K):
     a, b = workloads.normal_bf16((M, K), 6, "a"), workloads.normal_bf16((N, K), 6, "b")
     A, B, _, _ = operands(fp8, recipe, a, b, E4M3, E4M3)
     res = torch.ones((M, N), dtype=torch.bfloat16, device="cuda")
