@@ -4,9 +4,13 @@ Y = X W^T + b: the forward GEMM with bias / tanh-GELU epilogues, the data-
 gradient GEMM with the GELU-derivative and bias-gradient epilogue, and the
 accumulating fp32 weight-gradient GEMM plus its k-grouped MoE variant (and the
 same GEMMs on MXFP8 operands, scaled by the tensor core), all in
-hand-written CUDA behind the C ABI of include/fp8ll.h.  This package is the
-Python binding (ctypes) over that library (``binding``) and the training
-step of one layer built from those calls (``linear``).
+hand-written CUDA behind the C ABI of include/fp8ll.h.  Around the layer, the
+operators of a pre-norm residual block: RMS norm with the residual's addition
+and an fp8 output, its backward pass, the GEMM with bias, activation and residual
+(also for a few tokens), and gradient clipping.  This package is the Python
+binding (ctypes) over that library (``binding``, ``block``), the training step
+of one layer (``linear``) and a feed-forward block (``feedforward``) built from
+those calls.
 """
 from .binding import (ACC_FAST, ACC_FULL, ACT_GELU, ACT_NONE, E4M3, E5M2, EPI_BIAS, EPI_BIAS_GELU, EPI_DGELU, EPI_DGELU_BGRAD,
                       EPI_NONE, EXPORTS, Fp8Error, Fp8Tensor, cast_f32, debug_starve_next_gemm, device_status,

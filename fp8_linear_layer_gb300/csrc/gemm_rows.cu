@@ -24,6 +24,7 @@
 
 #include "common.cuh"
 #include "gemm_rows.h"
+#include "launch.cuh"
 #include "ptx.cuh"
 #include "rmsnorm.h"
 
@@ -172,6 +173,8 @@ __global__ void __launch_bounds__(kRowsThreads, rows_ctas_per_sm<NT>())
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sm.tmem_base;
+    await_dependency();
+    release_dependents();
     constexpr uint32_t kSfCol = NT;  // MXFP8: scale columns behind the accumulator
 
     bool ok = true;
@@ -407,20 +410,12 @@ int launch_rows_impl(const RowsMaps& maps, const RowsParams& p, cudaStream_t str
             return -3;
         configured |= 1ull << dev;
     }
-    cudaLaunchConfig_t cfg = {};
     const int64_t tiles = (static_cast<int64_t>(p.N) + kRowsFeatures - 1) / kRowsFeatures;
-    cfg.gridDim = dim3(static_cast<unsigned>(tiles * p.cluster), static_cast<unsigned>((p.M + NT - 1) / NT));
-    cfg.blockDim = dim3(kRowsThreads);
-    cfg.dynamicSmemBytes = rows_smem_bytes<NT>();
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(p.cluster);
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, maps, p) == cudaSuccess ? 0 : -3;
+    const dim3 grid(static_cast<unsigned>(tiles * p.cluster), static_cast<unsigned>((p.M + NT - 1) / NT));
+    return launch_dependent_clusters(kern, grid, static_cast<unsigned>(p.cluster), kRowsThreads, rows_smem_bytes<NT>(),
+                                     stream, maps, p) == cudaSuccess
+               ? 0
+               : -3;
 }
 
 template <int RECIPE>

@@ -100,6 +100,7 @@ __device__ __forceinline__ int head_of(const void* p, int bf16, int n) {
 template <int CAP>
 __global__ void __launch_bounds__(kThreadsClip) grad_norm_kernel(const __grid_constant__ Table<CAP> t,
                                                                  float* __restrict__ partials) {
+    await_dependency();
     release_dependents();
     __shared__ float part[kThreadsClip / 32];
     float s = 0.0f;
@@ -256,34 +257,25 @@ int run(int64_t count, const fp8ll_grad_t* grads, int scale, float max_norm, flo
         if (t.count == 0) break;
         ++launches;
         const int g = grid_of(t.chunks, num_sms);
-        grad_norm_kernel<CAP><<<g, kThreadsClip, 0, stream>>>(t, partials + used);
+        if (launch_dependent(grad_norm_kernel<CAP>, static_cast<unsigned>(g), kThreadsClip, 0, stream, t,
+                             partials + used) != cudaSuccess)
+            return -3;
         used += g;
     }
     if (!scale || used == 0) {
-        if (cudaGetLastError() != cudaSuccess) return -3;
         return launch_dependent(grad_norm_finalize_kernel, 1, kThreadsClip, 0, stream, partials, used, norm) ==
                        cudaSuccess
                    ? 0
                    : -3;
     }
-    if (cudaGetLastError() != cudaSuccess) return -3;
     // the launches of pass 1 in reverse order: the last tensors are the ones in L2
-    bool first = true;
     for (int k = launches - 1; k >= 0; --k) {
         if (launches > 1) fill(t, count, grads, starts[k]);
-        const unsigned g = static_cast<unsigned>(grid_of(t.chunks, num_sms));
-        float* out = first ? norm : nullptr;
-        // only the launch right behind pass 1 overlaps it
-        if (first) {
-            if (launch_dependent(grad_scale_kernel<CAP>, g, kThreadsClip, 0, stream, t, partials, used, max_norm, out) !=
-                cudaSuccess)
-                return -3;
-        } else {
-            grad_scale_kernel<CAP><<<g, kThreadsClip, 0, stream>>>(t, partials, used, max_norm, out);
-        }
-        first = false;
+        if (launch_dependent(grad_scale_kernel<CAP>, static_cast<unsigned>(grid_of(t.chunks, num_sms)), kThreadsClip, 0,
+                             stream, t, partials, used, max_norm, k == launches - 1 ? norm : nullptr) != cudaSuccess)
+            return -3;
     }
-    return cudaGetLastError() == cudaSuccess ? 0 : -3;
+    return 0;
 }
 
 }  // namespace

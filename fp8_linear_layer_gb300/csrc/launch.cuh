@@ -1,12 +1,14 @@
-// launch.cuh -- a kernel whose launch overlaps the end of the kernel before it on
-// the stream (programmatic dependent launch).
+// launch.cuh -- kernels whose launch overlaps the end of the kernel before them
+// on the stream (programmatic dependent launch).
 //
-// The first kernel calls release_dependents() as it starts: the second one's
-// blocks may then take the places of blocks that finish, with their set-up done
-// by the time the last one does.  The second kernel calls await_dependency()
-// before its first access to memory: it returns when the first kernel has
-// completed and its writes are visible, so the pair behaves as two launches in
-// stream order.
+// Every kernel launched this way calls await_dependency() before its first
+// access to global memory: it returns when the kernel before has completed and its
+// writes are visible, so the order of the stream holds.  One that then calls
+// release_dependents() lets the next kernel's blocks take the places of blocks
+// that finish, with their set-up done by the time the last one does: a product of
+// one token behind another takes 6.8 us instead of 8.0 at 7168 x 2048, 14.9
+// instead of 15.6 at 14336 x 4096.  (Released before the wait, blocks of the next
+// kernel gather on the SMs that finish first: 16.4.)
 #pragma once
 #include <cuda_runtime.h>
 
@@ -16,19 +18,29 @@ __device__ __forceinline__ void release_dependents() { asm volatile("griddepcont
 __device__ __forceinline__ void await_dependency() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 template <typename... Params, typename... Args>
-cudaError_t launch_dependent(void (*kern)(Params...), unsigned grid, unsigned block, size_t smem, cudaStream_t stream,
-                             Args&&... args) {
+cudaError_t launch_dependent_clusters(void (*kern)(Params...), dim3 grid, unsigned cluster, unsigned block, size_t smem,
+                                      cudaStream_t stream, Args&&... args) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(block);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 0 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, static_cast<Params>(args)...);
+}
+
+template <typename... Params, typename... Args>
+cudaError_t launch_dependent(void (*kern)(Params...), unsigned grid, unsigned block, size_t smem, cudaStream_t stream,
+                             Args&&... args) {
+    return launch_dependent_clusters(kern, dim3(grid), 0, block, smem, stream, static_cast<Args&&>(args)...);
 }
 
 }  // namespace fp8ll
