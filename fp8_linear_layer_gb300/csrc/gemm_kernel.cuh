@@ -51,6 +51,7 @@
 #include "cast_rule.cuh"
 #include "common.cuh"
 #include "internal.h"
+#include "launch.cuh"
 #include "ptx.cuh"
 
 namespace fp8ll {
@@ -512,26 +513,21 @@ static_assert(any_stage_bytes<kEpiLinearAny>() == kEpiWarps * kAnyWarpBytes, "st
 
 // Eight rows (those below `rows`) of n elements of type T -- pairs of bf16 where
 // every row is 4-byte aligned, else single ones -- between global memory and the
-// stage, by a whole warp along the rows.  All loads of four rows are in flight
-// before the first is stored.
+// stage, by a whole warp along the rows.  All loads are in flight before the
+// first is stored.
 template <typename T>
 __device__ __forceinline__ void load_rows(const T* g, int64_t ld, int rows, int n, int lane, uint32_t* stage) {
     constexpr int kPer = 8 / sizeof(T);  // 2 words or 4 halves per lane and row
     T* st = reinterpret_cast<T*>(stage);
+    T v[8][kPer];
 #pragma unroll
-    for (int i0 = 0; i0 < 8; i0 += 4) {
-        T v[4][kPer];
+    for (int i = 0; i < 8; ++i)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int j = 0; j < kPer; ++j) v[i][j] = i < rows && lane + 32 * j < n ? g[i * ld + lane + 32 * j] : T(0);
 #pragma unroll
-            for (int j = 0; j < kPer; ++j)
-                v[i][j] = i0 + i < rows && lane + 32 * j < n ? g[(i0 + i) * ld + lane + 32 * j] : T(0);
+    for (int i = 0; i < 8; ++i)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < kPer; ++j)
-                st[(i0 + i) * (kAnyRowWords * 4 / sizeof(T)) + lane + 32 * j] = v[i][j];
-    }
+        for (int j = 0; j < kPer; ++j) st[i * (kAnyRowWords * 4 / sizeof(T)) + lane + 32 * j] = v[i][j];
 }
 
 template <typename T>
@@ -820,6 +816,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem_base = sm.tmem_base;
     uint8_t* const zs = reinterpret_cast<uint8_t*>(&sm) + sizeof(SmemLayout);  // Z, residual or output staging
     const bool z_staged = uses_z<EPI>() && p.z_tma != 0;
+    if (is_linear<EPI>()) {
+        await_dependency();
+        release_dependents();
+    }
 
     if (warp < kFirstEpiWarp) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtrl));
     if (warp == 0) {
@@ -1113,6 +1113,11 @@ int launch_gemm_impl(const TensorMaps& maps, const GemmParams& p, cudaStream_t s
             return -3;
         configured |= 1ull << dev;
     }
+    if (is_linear<EPI>())
+        return launch_dependent(kern, static_cast<unsigned>(grid), kThreads, smem_bytes<EPI>(), stream, maps, p) ==
+                       cudaSuccess
+                   ? 0
+                   : -3;
     kern<<<grid, kThreads, smem_bytes<EPI>(), stream>>>(maps, p);
     return cudaGetLastError() == cudaSuccess ? 0 : -3;
 }

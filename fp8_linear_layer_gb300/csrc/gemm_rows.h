@@ -21,11 +21,13 @@ int rows_cluster(int64_t M, int64_t N, int64_t nkb);
 // where a K split shortens the chain of blocks that few tiles would leave to
 // few SMs: 256 x 2112 over 7168 takes 15.3 / 12.4 us against 37.3 / 25.0, 256 x
 // 4096 over 14336 40.1 / 30.4 against 70.5 / 44.7; a split in two of a short K
-// does not pay (256 x 4096 over 1024: 11.4 / 10.2 against 9.4 / 8.5).
+// does not pay (256 x 4096 over 1024: 11.4 / 10.2 against 9.4 / 8.5), unless the
+// rows are not 16-byte aligned, which costs this kernel's epilogue less (256 x
+// 2001 over 512 with GELU, residual and Z: 13.8 / 12.9 against 19.4 / 23.8).
 inline bool rows_kernel_taken(int64_t M, int64_t N, int64_t K) {
     if (M <= 64) return true;
     const int c = rows_cluster(M, N, K / 128);
-    return c >= 4 || (c == 2 && K / 128 >= 32);
+    return c >= 4 || (c == 2 && (K / 128 >= 32 || N % 8 != 0));
 }
 
 struct RowsMaps {

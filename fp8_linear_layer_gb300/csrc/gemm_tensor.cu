@@ -106,6 +106,10 @@ __global__ void __cluster_dims__(2 * SPLIT, 1, 1) __launch_bounds__(kThreads, 1)
     cluster_sync();
     tc_fence_after();
     const uint32_t tmem_base = sm.tmem_base;
+    if (is_linear<EPI>()) {
+        await_dependency();
+        release_dependents();
+    }
     bool exchanged = false;  // SPLIT 2: this warp has passed the cluster's exchange barrier
 
     if (warp < kFirstEpiWarp) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtrl));
@@ -349,7 +353,10 @@ int launch_tensor_impl(const TensorMaps& maps, const GemmParams& p, cudaStream_t
     if (slots < 0) return -3;
     // one tile per cluster where its K blocks are split
     const int64_t clusters = SPLIT == 2 || p.total_tiles < slots ? p.total_tiles : slots;
-    gemm_tensor_kernel<EPI, SPLIT><<<static_cast<unsigned>(2 * SPLIT * clusters), kThreads, kTpSmemBytes<EPI>, stream>>>(maps, p);
+    const unsigned grid = static_cast<unsigned>(2 * SPLIT * clusters);
+    if (is_linear<EPI>())
+        return launch_dependent(gemm_tensor_kernel<EPI, SPLIT>, grid, kThreads, kTpSmemBytes<EPI>, stream, maps, p) == cudaSuccess ? 0 : -3;
+    gemm_tensor_kernel<EPI, SPLIT><<<grid, kThreads, kTpSmemBytes<EPI>, stream>>>(maps, p);
     return cudaGetLastError() == cudaSuccess ? 0 : -3;
 }
 
