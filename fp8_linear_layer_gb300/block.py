@@ -293,7 +293,7 @@ class GradList:
                                      dtype=torch.float32, device=device)
         # the memory that the table points to stays allocated as long as the list,
         # whatever becomes of the tensors
-        self._storages = [t.untyped_storage() for t in self.grads + self.out]
+        self._storages = [t.untyped_storage() for t in self.grads + self.out + [self.norm, self.workspace]]
         self._tail = (self.norm.data_ptr(), self.workspace.data_ptr(), self.workspace.numel() * 4)
 
 

@@ -634,7 +634,7 @@ __device__ __forceinline__ void store_linear(const GemmParams& p, int row0, int 
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
             const int col = col0 + 8 * (c0 + i);
-            bw[i] = bias && col < p.N ? __ldg(reinterpret_cast<const unsigned int*>(bias + col)) : 0u;
+            bw[i] = bias && col < p.N ? *reinterpret_cast<const uint32_t*>(bias + col) : 0u;
         }
     };
     if (kAhead == kChunks) load_bias(0);

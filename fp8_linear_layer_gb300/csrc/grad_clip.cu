@@ -101,7 +101,7 @@ __device__ __forceinline__ int head_of(const void* p, int bf16, int n) {
 
 template <int CAP>
 __global__ void __launch_bounds__(kThreadsClip) grad_norm_kernel(const __grid_constant__ Table<CAP> t,
-                                                                 float* __restrict__ partials) {
+                                                                 float* partials) {
     await_dependency();
     release_dependents();
     __shared__ float part[kThreadsClip / 32];
@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(kThreadsClip) grad_norm_kernel(const __grid_co
         const int vecs = (n - head) / per;
         const uint4* v = reinterpret_cast<const uint4*>(g + head * (bf16 ? 2 : 4));
         const bool keep = c >= t.keep_from;
-        auto load = [&](int j) { return keep ? __ldg(v + j) : __ldcs(v + j); };
+        auto load = [&](int j) { return keep ? v[j] : __ldcs(v + j); };
         int i = threadIdx.x;
         for (; i + 3 * kThreadsClip < vecs; i += 4 * kThreadsClip) {
             const uint4 a = load(i), b = load(i + kThreadsClip), d = load(i + 2 * kThreadsClip),
@@ -152,10 +152,10 @@ __global__ void __launch_bounds__(kThreadsClip) grad_norm_kernel(const __grid_co
 // In fp32: the sum is a tree of a few additions per thread and thirteen levels.
 // (In fp64 every CTA paid for it at this part's fp64 rate: clipping 67 MB took
 // 36.5 us instead of 29.0.)
-__device__ __forceinline__ float total_norm(const float* __restrict__ partials, int count) {
+__device__ __forceinline__ float total_norm(const float* partials, int count) {
     __shared__ float part[kThreadsClip / 32];
     float s = 0.0f;
-    for (int i = threadIdx.x; i < count; i += kThreadsClip) s += partials[i];
+    for (int i = threadIdx.x; i < count; i += kThreadsClip) s += __ldcg(partials + i);
 #pragma unroll
     for (int off = 16; off >= 1; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = s;
@@ -166,8 +166,8 @@ __device__ __forceinline__ float total_norm(const float* __restrict__ partials, 
     return sqrtf(total);
 }
 
-__global__ void __launch_bounds__(kThreadsClip) grad_norm_finalize_kernel(const float* __restrict__ partials,
-                                                                          int count, float* __restrict__ norm) {
+__global__ void __launch_bounds__(kThreadsClip) grad_norm_finalize_kernel(const float* partials,
+                                                                          int count, float* norm) {
     await_dependency();
     const float v = total_norm(partials, count);
     if (threadIdx.x == 0) *norm = v;
@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(kThreadsClip) grad_norm_finalize_kernel(const 
 
 template <int CAP>
 __global__ void __launch_bounds__(kThreadsClip) grad_scale_kernel(const __grid_constant__ Table<CAP> t,
-                                                                  const float* __restrict__ partials, int count,
+                                                                  const float* partials, int count,
                                                                   float max_norm, float* norm) {
     await_dependency();
     const float v = total_norm(partials, count);

@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(MAXT) rmsnorm_rows_kernel(const __grid_constan
     };
     auto load_gamma = [&](int v) {
         const int i = threadIdx.x + v * T;
-        return i < nv ? __ldg(reinterpret_cast<const uint4*>(p.gamma + 8 * i)) : zero;
+        return i < nv ? *reinterpret_cast<const uint4*>(p.gamma + 8 * i) : zero;
     };
     int64_t r = blockIdx.x;
     fetch(r);
@@ -271,6 +271,10 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
 template <int FMT, int RECIPE>
 __global__ void __launch_bounds__(256, kColsCtas) rmsnorm_cols_kernel(const __grid_constant__ RmsNormParams p) {
     extern __shared__ __align__(16) uint8_t stage_raw[];
@@ -279,20 +283,18 @@ __global__ void __launch_bounds__(256, kColsCtas) rmsnorm_cols_kernel(const __gr
     const uint16_t* h = p.h ? p.h : p.x;
     const int64_t ldh = p.h ? p.cols : p.ldx;
     const int64_t ncb = p.cols / 128, ntiles = (p.rows / 128) * ncb;
-    // the last rows first: the rows kernel left them in L2
     float inv_t = 1.0f, s_t = 1.0f;
     if (RECIPE == kRecipeTensor) block_scale<FMT>(*p.amax_in, inv_t, s_t);
     auto fetch = [&](int64_t t, int buf) {
-        const int64_t q = ntiles - 1 - t, rb = q / ncb, r0 = rb * 128, c0 = (q - rb * ncb) * 128;
+        const int64_t rb = t / ncb, r0 = rb * 128, c0 = (t - rb * ncb) * 128;
 #pragma unroll
         for (int it = 0; it < 8; ++it) {
             const int i = threadIdx.x + it * 256;
             const int rr = i >> 4, ch = i & 15;
             cp_async16(smem_addr(&stage[buf].tile[rr][(ch * 4 + 8 * (rr >> 5)) & 63]), h + (r0 + rr) * ldh + c0 + ch * 8);
         }
-        if (threadIdx.x < 32)
-            cp_async16(smem_addr(&stage[buf].rstd[threadIdx.x >> 3][4 * (threadIdx.x & 7)]),
-                       p.rstd + r0 + 4 * threadIdx.x);
+        if (threadIdx.x < 128)
+            cp_async4(smem_addr(&stage[buf].rstd[threadIdx.x >> 5][threadIdx.x & 31]), p.rstd + r0 + threadIdx.x);
     };
     const int cp = threadIdx.x >> 2, part = threadIdx.x & 3;
     const int wcol = (cp + 8 * part) & 63;
@@ -306,9 +308,9 @@ __global__ void __launch_bounds__(256, kColsCtas) rmsnorm_cols_kernel(const __gr
         asm volatile("cp.async.commit_group;" ::: "memory");
         asm volatile("cp.async.wait_group 1;" ::: "memory");
         __syncthreads();
-        const int64_t q = ntiles - 1 - t, rb = q / ncb, r0 = rb * 128, c0 = (q - rb * ncb) * 128;
+        const int64_t rb = t / ncb, r0 = rb * 128, c0 = (t - rb * ncb) * 128;
         const int64_t c = c0 + 2 * cp;
-        const uint32_t gw = __ldg(reinterpret_cast<const unsigned int*>(p.gamma + c));
+        const uint32_t gw = *reinterpret_cast<const uint32_t*>(p.gamma + c);
         const float g_lo = bf16_lo(gw), g_hi = bf16_hi(gw);
         float inv_lo = inv_t, inv_hi = inv_t, s_lo, s_hi;
         if (RECIPE != kRecipeTensor) {
@@ -484,7 +486,7 @@ __global__ void __launch_bounds__(MAXT, 1) rmsnorm_grad_kernel(const __grid_cons
     };
     auto gamma = [&](int v) {
         const int i = tid + v * T;
-        return i < nv ? __ldg(reinterpret_cast<const uint4*>(p.gamma + 8 * i)) : zero;
+        return i < nv ? *reinterpret_cast<const uint4*>(p.gamma + 8 * i) : zero;
     };
     const int64_t step = static_cast<int64_t>(gridDim.x) * kRowsPerCta;
     const int own = WARP ? static_cast<int>(threadIdx.x) / (WARP ? LANES : 1) : 0;  // the row within the CTA
@@ -583,8 +585,8 @@ __global__ void __launch_bounds__(MAXT, 1) rmsnorm_grad_kernel(const __grid_cons
 
 // dgamma[c] (+)= sum over the bands: 32 columns per CTA, 32 threads per column
 // take every 32nd band, their sums are added in order
-__global__ void __launch_bounds__(1024) rmsnorm_grad_finalize_kernel(const float* __restrict__ ws, int bands,
-                                                                     int64_t cols, float* __restrict__ out,
+__global__ void __launch_bounds__(1024) rmsnorm_grad_finalize_kernel(const float* ws, int bands,
+                                                                     int64_t cols, float* out,
                                                                      int accumulate) {
     await_dependency();
     __shared__ float part[32][33];
@@ -593,7 +595,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_grad_finalize_kernel(const float
     float s = 0.0f;
     if (c < cols) {
 #pragma unroll 8
-        for (int b = sl; b < bands; b += 32) s += ws[b * cols + c];
+        for (int b = sl; b < bands; b += 32) s += __ldcg(ws + b * cols + c);
     }
     part[sl][cl] = s;
     __syncthreads();

@@ -99,6 +99,22 @@ def test_codes_are_the_cast_of_the_same_values(fp8):
     assert torch.equal(got.rows.scale[:, :4], cast.scale[:, :4])
 
 
+@pytest.mark.parametrize("recipe", ["block", "mx", "tensor"])
+def test_rstd_at_any_element(fp8, recipe):
+    # rstd needs no more than its own alignment
+    x, gamma, amax = stream(256, 384, 3), scales(384, 4), torch.tensor([6.0], device="cuda")
+    want = call(fp8, recipe, x, gamma, 0, None, amax, cols=True)
+    make = {"block": fp8.empty_rmsnorm, "mx": fp8.empty_mx_rmsnorm, "tensor": fp8.empty_tensor_rmsnorm}[recipe]
+    out = make(256, 384, 0, cols_too=True)
+    out.rstd = torch.zeros(259, device="cuda")[3:]
+    got = call(fp8, recipe, x, gamma, 0, None, amax, out=out)
+    dx, _ = fp8.rmsnorm_backward(x, x, gamma, out.rstd)
+    want_dx, _ = fp8.rmsnorm_backward(x, x, gamma, want.rstd)
+    torch.cuda.synchronize()
+    assert torch.equal(got.rstd, want.rstd) and torch.equal(got.rows.q, want.rows.q)
+    assert torch.equal(got.cols.q, want.cols.q) and torch.equal(dx, want_dx)
+
+
 @pytest.mark.parametrize("onto", ["x", "residual"])
 def test_stream_in_place(fp8, onto):
     x, r, gamma = stream(37, 1024, 3), stream(37, 1024, 4), scales(1024, 5)
