@@ -294,7 +294,27 @@ class GradList:
         # the memory that the table points to stays allocated as long as the list,
         # whatever becomes of the tensors
         self._storages = [t.untyped_storage() for t in self.grads + self.out + [self.norm, self.workspace]]
+        self._apart = self._outputs_apart()
         self._tail = (self.norm.data_ptr(), self.workspace.data_ptr(), self.workspace.numel() * 4)
+
+
+    def _outputs_apart(self) -> bool:
+        # every place that clipping writes is apart from every other tensor of the
+        # list (one listed twice would be scaled twice, in no certain order)
+        spans = []
+        for g, o in zip(self.grads, self.out):
+            size = g.numel() * g.element_size()
+            if size == 0:
+                continue
+            spans.append((o.data_ptr(), o.data_ptr() + size, True))
+            if o.data_ptr() != g.data_ptr():
+                spans.append((g.data_ptr(), g.data_ptr() + size, False))
+        end, written = 0, 0  # of all spans so far, of those written to
+        for lo, hi, writes in sorted(spans):
+            if lo < (end if writes else written):
+                return False
+            end, written = max(end, hi), max(written, hi) if writes else written
+        return True
 
 
 def grad_norm(grads) -> torch.Tensor:
@@ -307,7 +327,9 @@ def grad_norm(grads) -> torch.Tensor:
 
 def clip_grads(grads, max_norm: float) -> torch.Tensor:
     """Scales every tensor by min(1, max_norm / (norm + 1e-6)), norm the L2 norm
-    over all of them, and returns the norm (device, 1 element)."""
+    over all of them, and returns the norm (device, 1 element).  No tensor may
+    overlap another that is written to: a shared one is listed once."""
     g = grads if isinstance(grads, GradList) else GradList(grads)
+    assert g._apart, "clip_grads: a tensor of the list overlaps another"
     _check(lib().fp8_clip_grads(len(g.grads), g.table, float(max_norm), *g._tail, _stream()), "fp8_clip_grads")
     return g.norm

@@ -320,6 +320,7 @@ static bool valid_linear(int64_t M, int64_t N, const LinearArgs& a) {
     if (a.aux && (!aligned16(a.aux) || overlaps(a.aux, M * N * 2, a.out, M * N * 2))) return false;
     if (a.residual) {
         if ((reinterpret_cast<uintptr_t>(a.residual) & 1u) != 0 || a.ldr < N || a.ldr >= (1LL << 36)) return false;
+        if (M > 1 && a.ldr > (1LL << 60) / M) return false;  // its extent in bytes stays within 64 bits
         const int64_t rbytes = ((M - 1) * a.ldr + N) * 2;
         // the output may take the residual's place, element by element
         const bool in_place = a.residual == a.out && a.ldr == N;

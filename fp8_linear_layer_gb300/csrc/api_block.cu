@@ -26,12 +26,15 @@ bool share(const Range& a, const Range& b) {
     return x < y + static_cast<uintptr_t>(b.bytes) && y < x + static_cast<uintptr_t>(a.bytes);
 }
 
+// rows of ld elements whose extent, in bytes of up to 4 an element, stays within 64 bits
+bool spans(int64_t rows, int64_t ld) { return ld < (1LL << 36) && (rows < 2 || ld <= (1LL << 60) / rows); }
+
 bool valid_norm(const RmsNormParams& p, int fmt) {
     if (fmt != FP8LL_E4M3 && fmt != FP8LL_E5M2) return false;
     if (p.cols % 128 != 0 || p.cols > kNormMaxCols || p.rows > (1LL << 31) - 1) return false;
     if (!(p.eps >= 0.0f) || std::isinf(p.eps)) return false;
-    if (!p.x || !aligned(p.x, 16) || p.ldx < p.cols || p.ldx % 8 != 0 || p.ldx >= (1LL << 36)) return false;
-    if (p.residual && (!aligned(p.residual, 16) || p.ldr < p.cols || p.ldr % 8 != 0 || p.ldr >= (1LL << 36)))
+    if (!p.x || !aligned(p.x, 16) || p.ldx < p.cols || p.ldx % 8 != 0 || !spans(p.rows, p.ldx)) return false;
+    if (p.residual && (!aligned(p.residual, 16) || p.ldr < p.cols || p.ldr % 8 != 0 || !spans(p.rows, p.ldr)))
         return false;
     if (p.residual && !p.h) return false;
     if (!p.gamma || !aligned(p.gamma, 16) || !p.rstd || !aligned(p.rstd, 4)) return false;
@@ -188,9 +191,9 @@ int fp8_rmsnorm_backward(const void* dy_bf16, const void* h_bf16, const void* ga
     if (!aligned(dy_bf16, 16) || !aligned(h_bf16, 16) || !aligned(gamma_bf16, 16) || !aligned(rstd, 4) ||
         !aligned(residual_grad_bf16, 16) || !aligned(dx_bf16, 16))
         return FP8LL_ERR_INVALID_ARG;
-    if (lddy < cols || lddy % 8 != 0 || lddy >= (1LL << 36) || ldh < cols || ldh % 8 != 0 || ldh >= (1LL << 36))
+    if (lddy < cols || lddy % 8 != 0 || !spans(rows, lddy) || ldh < cols || ldh % 8 != 0 || !spans(rows, ldh))
         return FP8LL_ERR_INVALID_ARG;
-    if (residual_grad_bf16 && (ldres < cols || ldres % 8 != 0 || ldres >= (1LL << 36))) return FP8LL_ERR_INVALID_ARG;
+    if (residual_grad_bf16 && (ldres < cols || ldres % 8 != 0 || !spans(rows, ldres))) return FP8LL_ERR_INVALID_ARG;
     const int64_t need = static_cast<int64_t>(fp8_rmsnorm_workspace_size(rows, cols));
     if (!workspace || !aligned(workspace, 16) || static_cast<int64_t>(workspace_bytes) < need)
         return FP8LL_ERR_WORKSPACE;

@@ -499,8 +499,10 @@ int fp8_rmsnorm_backward(const void* dy_bf16, const void* h_bf16, const void* ga
                          size_t workspace_bytes, fp8ll_stream_t stream);
 
 /* One gradient tensor: n elements of fp32 or bf16, contiguous, aligned to the
- * element.  out: where the clipped gradient goes, of the same type (grad itself
- * for in place; otherwise it must overlap no tensor of the list). */
+ * element.  out: where the clipped gradient goes, of the same type: grad itself
+ * (in place), or memory of its own.  An out that overlaps its own gradient
+ * without being it is refused; that it overlaps no other entry's grad or out is
+ * the caller's to see to (a tensor that two layers share is listed once). */
 typedef struct {
     const void* grad;
     void* out;

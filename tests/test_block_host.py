@@ -120,3 +120,42 @@ def test_gradient_list_refusals(f):
     assert call([ok], ws=None) == WS and call([ok], ws=vp(0x20008)) == WS
     assert L.fp8_grad_norm_workspace_size(-1) == 0
     assert L.fp8_grad_norm_workspace_size(5000) > L.fp8_grad_norm_workspace_size(500) > 0
+
+
+def test_extents_beyond_64_bits_are_refused(f):
+    E = f.binding.ERR_INVALID_ARG
+    far = (1 << 36) - 8
+    many = dict(rows=(1 << 31) - 1, qc=None, sc=None, sldr=1 << 31)
+    assert block_norm(f, **dict(many, ldx=far)) == E
+    assert block_norm(f, **dict(many, ldr=far)) == E
+    for ld in ("lddy", "ldh", "ldres"):
+        assert f.lib().fp8_rmsnorm_backward(*dict(BACK, **{"rows": (1 << 31) - 1, ld: far}).values(), None) == E
+
+
+@pytest.mark.parametrize("views,apart", [
+    ([(0, 100), (100, 200)], True),
+    ([(0, 100), (0, 100)], False),             # a shared weight listed twice
+    ([(0, 100), (99, 120)], False),
+    ([(0, 300), (20, 40)], False),             # one inside another
+    ([(0, 10), (50, 50), (10, 20)], True),     # an empty one
+])
+def test_overlapping_gradients(f, views, apart):
+    torch = pytest.importorskip("torch")
+    t = torch.zeros(300)
+    g = f.GradList([t[a:b] for a, b in views])
+    assert g._apart is apart
+    # with outputs elsewhere the gradients may overlap, the outputs may not
+    o = [torch.zeros(b - a) for a, b in views]
+    assert f.GradList([t[a:b] for a, b in views], o)._apart is True
+    assert f.GradList(o, [t[a:b] for a, b in views])._apart is apart
+    if not apart:
+        with pytest.raises(AssertionError, match="overlaps"):
+            f.clip_grads(g, 1.0)
+
+
+def test_output_over_another_gradient(f):
+    torch = pytest.importorskip("torch")
+    a, b = torch.zeros(64), torch.zeros(64)
+    assert f.GradList([a, b], [torch.zeros(64), a])._apart is False
+    assert f.GradList([a, b], [a, b])._apart is True
+    assert f.GradList([a, b], [b, a])._apart is False
