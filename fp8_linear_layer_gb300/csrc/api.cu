@@ -979,7 +979,7 @@ int fp8_gemm_linear(int64_t M, int64_t N, int64_t K, const fp8ll_operand_t* A, c
     int rc = current_device(&dev);
     if (rc != FP8LL_OK) return rc;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (rows_kernel_taken(M, N, K)) {
+    if (rows_kernel_taken(M, N, K, kRecipeBlock)) {
         RowsParams r = rows_params(M, N, K, A->fmt, B->fmt, args, dev);
         r.idesc |= 1u << 4;  // fp32 accumulators
         RowsMaps rm;
@@ -996,9 +996,14 @@ int fp8_gemm_linear(int64_t M, int64_t N, int64_t K, const fp8ll_operand_t* A, c
     p.num_groups = 1;
     p.groups[0] = GroupEntry{0, static_cast<int32_t>(K / 128), 0, 0};
     p.total_tiles = p.tiles_per_group;
-    const int epi = fill_linear(args, p);
-    // an aligned residual goes through shared memory by TMA
+    int epi = fill_linear(args, p);
     std::memset(&maps.z, 0, sizeof(maps.z));
+    const int parts = gemm_linear_parts(p);
+    if (parts > 1) {
+        if (epi < kEpiLinear) epi = act == FP8LL_ACT_GELU ? kEpiLinearGelu : kEpiLinear;
+        return launch_gemm_linear_parts(maps, p, epi, parts, s) == 0 ? FP8LL_OK : FP8LL_ERR_LAUNCH;
+    }
+    // an aligned residual goes through shared memory by TMA
     if (epi == kEpiLinear || epi == kEpiLinearGelu) {
         if (!encode_z(residual_bf16, M, N, ldr, &maps.z)) return FP8LL_ERR_LAUNCH;
         p.z_tma = 1;
@@ -1019,7 +1024,7 @@ int fp8_mx_gemm_linear(int64_t M, int64_t N, int64_t K, const fp8ll_mx_operand_t
     if (!valid_k(K) || !valid_mx_operand(A, M, K) || !valid_mx_operand(B, N, K)) return FP8LL_ERR_INVALID_ARG;
     int rc = current_device(&dev);
     if (rc != FP8LL_OK) return rc;
-    if (rows_kernel_taken(M, N, K)) {
+    if (rows_kernel_taken(M, N, K, kRecipeMx)) {
         RowsParams r = rows_params(M, N, K, A->fmt, B->fmt, args, dev);
         r.idesc |= 1u << 23;  // UE8M0 scales
         r.groups_w = mx_sf_groups(N);
@@ -1039,7 +1044,7 @@ int fp8_mx_gemm_linear(int64_t M, int64_t N, int64_t K, const fp8ll_mx_operand_t
     int epi = fill_linear(args, p);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (launch_gemm_mx_splits(p)) {
-        if (epi < kEpiLinear) epi = args.act == FP8LL_ACT_GELU ? kEpiLinearGeluAny : kEpiLinearAny;
+        if (epi < kEpiLinear) epi = args.act == FP8LL_ACT_GELU ? kEpiLinearGelu : kEpiLinear;
         rc = launch_gemm_mx_split(maps, p, epi, s);
     } else {
         rc = launch_gemm_mx(maps, p, epi, s);
@@ -1058,7 +1063,7 @@ int fp8_tensor_gemm_linear(int64_t M, int64_t N, int64_t K, const fp8ll_tensor_o
     if (!valid_k(K) || !valid_tensor_operand(A, M, K) || !valid_tensor_operand(B, N, K)) return FP8LL_ERR_INVALID_ARG;
     int rc = current_device(&dev);
     if (rc != FP8LL_OK) return rc;
-    if (rows_kernel_taken(M, N, K)) {
+    if (rows_kernel_taken(M, N, K, kRecipeTensor)) {
         RowsParams r = rows_params(M, N, K, A->fmt, B->fmt, args, dev);
         r.idesc |= 1u << 4;  // fp32 accumulators
         r.tsw = B->scale;
@@ -1076,7 +1081,7 @@ int fp8_tensor_gemm_linear(int64_t M, int64_t N, int64_t K, const fp8ll_tensor_o
     int epi = fill_linear(args, p);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (launch_gemm_tensor_splits(p)) {
-        if (epi < kEpiLinear) epi = args.act == FP8LL_ACT_GELU ? kEpiLinearGeluAny : kEpiLinearAny;
+        if (epi < kEpiLinear) epi = args.act == FP8LL_ACT_GELU ? kEpiLinearGelu : kEpiLinear;
         rc = launch_gemm_tensor_split(maps, p, epi, s);
     } else {
         rc = launch_gemm_tensor(maps, p, epi, s);

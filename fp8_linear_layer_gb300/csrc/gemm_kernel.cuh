@@ -53,6 +53,7 @@
 #include "internal.h"
 #include "launch.cuh"
 #include "ptx.cuh"
+#include "split_k.cuh"
 
 namespace fp8ll {
 
@@ -91,6 +92,7 @@ struct __align__(1024) SmemLayout {
     uint64_t zfull, zempty;
     uint64_t drain;
     uint32_t tmem_base;
+    int32_t failed;  // SPLIT > 1: an epilogue wait of this CTA ran out
 };
 // The dgrad kernels add the Z tile buffer right after the layout (1024-byte
 // aligned, as 128-byte swizzling needs): four boxes of 128 rows x 64 columns.
@@ -122,10 +124,12 @@ template <int EPI>
 constexpr size_t any_stage_bytes() {
     return is_any_linear<EPI>() ? static_cast<size_t>(kEpiWarps) * 8 * 68 * 4 : 0;
 }
-template <int EPI>
+template <int EPI, int SPLIT = 1>
 constexpr size_t smem_bytes() {
-    return sizeof(SmemLayout) + (uses_z<EPI>() ? kZBytes : any_stage_bytes<EPI>()) + 1024;
+    return sizeof(SmemLayout) + (uses_z<EPI>() && SPLIT == 1 ? kZBytes : any_stage_bytes<EPI>()) + 1024;
 }
+static_assert(sizeof(SmemLayout::b) >= kSplitBytes<2> && sizeof(SmemLayout::b) >= kSplitBytes<4>,
+              "a split tile's sums take the place of B's stages");
 static_assert(smem_bytes<kEpiDgelu>() <= 232448, "shared memory budget");
 
 template <int N>
@@ -160,6 +164,7 @@ __device__ __forceinline__ void decode_tile(const GemmParams& p, int t, int& g, 
 // row0 = m0 + 32 * quadrant + lane / 4 and col0 = n0 + 128 * half + 2 * (lane % 4).
 
 constexpr int kChunks = kHalfN / 8;  // 8-column chunks per thread (16)
+static_assert(kChunks == kSplitChunks && 32 * kEpiWarps == kSplitThreads, "the split exchanges these fragments");
 
 __device__ __forceinline__ void red_add_v2(float* addr, float a, float b) {
     asm volatile("red.global.add.v2.f32 [%0], {%1, %2};" ::"l"(addr), "f"(a), "f"(b) : "memory");
@@ -647,7 +652,7 @@ __device__ __forceinline__ void store_linear(const GemmParams& p, int row0, int 
 #pragma unroll
             for (int r = 0; r < ROWS; ++r) {
                 uint4 v = make_uint4(0, 0, 0, 0);
-                if (row0 + 8 * r < p.M && vcol < p.N)
+                if (res && row0 + 8 * r < p.M && vcol < p.N)
                     v = *reinterpret_cast<const uint4*>(res + (row0 + 8 * r) * p.ldr + vcol);
                 yw[r][0] = v.x; yw[r][1] = v.y; yw[r][2] = v.z; yw[r][3] = v.w;
             }
@@ -778,7 +783,9 @@ __device__ __forceinline__ void store_dgrad_quant(const GemmParams& p, int row0,
 
 // -------------------------------------------------------------------- kernel
 
-template <int EPI>
+// SPLIT: CTAs of a cluster that share a tile's K blocks (1, or 2 or 4 for the
+// linear epilogues: see split_k.cuh); one tile per cluster where they do.
+template <int EPI, int SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_fp8_kernel(const __grid_constant__ TensorMaps maps, const __grid_constant__ GemmParams p) {
     extern __shared__ uint8_t smem_raw[];
@@ -787,6 +794,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const uint64_t budget = p.budget_ns;
+    // this CTA's share of a tile's K blocks: the first one (i = 0), the one behind the last (i = 1)
+    auto share = [](int nkb, int i) {
+        return SPLIT == 1 ? i * nkb : nkb * (static_cast<int>(cluster_ctarank()) + i) / SPLIT;
+    };
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
@@ -804,6 +815,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(smem_addr(&sm.zfull), 1);
         mbar_init(smem_addr(&sm.zempty), kEpiWarps);
         mbar_init(smem_addr(&sm.drain), 1);
+        if (SPLIT > 1) sm.failed = 0;
         fence_mbar_init();
     }
     if (warp == 1) {
@@ -815,7 +827,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem_base = sm.tmem_base;
     uint8_t* const zs = reinterpret_cast<uint8_t*>(&sm) + sizeof(SmemLayout);  // Z, residual or output staging
-    const bool z_staged = uses_z<EPI>() && p.z_tma != 0;
+    const bool z_staged = SPLIT == 1 && uses_z<EPI>() && p.z_tma != 0;
+    bool exchanged = false;  // SPLIT > 1: this warp has passed the cluster's exchange barrier
     if (is_linear<EPI>()) {
         await_dependency();
         release_dependents();
@@ -834,12 +847,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             int n_issued = 0, ns_issued = 0;
             bool ok = true;
             if (!p.debug_starve) {
-                for (int t = blockIdx.x; t < p.total_tiles && ok; t += gridDim.x) {
+                for (int t = blockIdx.x / SPLIT; t < p.total_tiles && ok; t += gridDim.x / SPLIT) {
                     int g, mt, nt;
                     decode_tile(p, t, g, mt, nt);
                     const GroupEntry ge = p.groups[g];
                     const int m0 = mt * kBM, n0 = nt * kBN;
-                    for (int kb = 0; kb < ge.nkb; ++kb) {
+                    const int kb_end = share(ge.nkb, 1);
+                    for (int kb = share(ge.nkb, 0); kb < kb_end; ++kb) {
                         const int kbg = ge.kb_start + kb;
                         if (!mbar_wait(smem_addr(&sm.empty[s]), ph ^ 1u, budget)) {
                             ok = false;
@@ -933,10 +947,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         int s = 0, ab = 0;
         uint32_t ph = 0, aph = 0;
         bool ok = true;
-        for (int t = blockIdx.x; t < p.total_tiles && ok; t += gridDim.x) {
+        for (int t = blockIdx.x / SPLIT; t < p.total_tiles && ok; t += gridDim.x / SPLIT) {
             int g, mt, nt;
             decode_tile(p, t, g, mt, nt);
-            const int nkb = p.groups[g].nkb;
+            const int nkb = share(p.groups[g].nkb, 1) - share(p.groups[g].nkb, 0);
             for (int kb = 0; kb < nkb; ++kb) {
                 ok = mbar_wait_warp(smem_addr(&sm.acc_empty[ab]), aph ^ 1u, budget);
                 if (ok) ok = mbar_wait_warp(smem_addr(&sm.full[s]), ph, budget);
@@ -974,7 +988,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int ab = 0, ss = 0;
         uint32_t aph = 0, sph = 0, zph = 0;
         bool ok = true;
-        for (int t = blockIdx.x; t < p.total_tiles && ok; t += gridDim.x) {
+        for (int t = blockIdx.x / SPLIT; t < p.total_tiles && ok; t += gridDim.x / SPLIT) {
             int g, mt, nt;
             decode_tile(p, t, g, mt, nt);
             const GroupEntry ge = p.groups[g];
@@ -985,7 +999,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t tq = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                                 static_cast<uint32_t>(half * kHalfN);
             if (is_linear<EPI>()) {
-                if (is_any_linear<EPI>()) prefetch_residual(p, m0 + q * 32 + g8 + 8 * cq, n0 + half * kHalfN);
+                if (is_any_linear<EPI>() || SPLIT > 1) prefetch_residual(p, m0 + q * 32 + g8 + 8 * cq, n0 + half * kHalfN);
             } else if (uses_z<EPI>() && !z_staged) {
                 // the stored pre-activations of this tile are read once the K loop
                 // is done: ask for them in L2 now (each lane of a quad one of the
@@ -1000,7 +1014,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     prefetch_l2(zrow + pc1);
                 }
             }
-            for (int kb = 0; kb < ge.nkb; ++kb) {
+            // counted up to zero where the share takes registers of its own
+            for (int kb = SPLIT == 1 ? 0 : share(ge.nkb, 0) - share(ge.nkb, 1); kb < (SPLIT == 1 ? ge.nkb : 0); ++kb) {
                 ok = mbar_wait2_warp(smem_addr(&sm.acc_full[ab]), aph, smem_addr(&sm.sfull[ss]), sph, budget);
                 if (!ok) break;
                 tc_fence_after();
@@ -1043,6 +1058,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ring_advance<kSStages>(ss, sph);
             }
             if (!ok) break;
+            if (SPLIT > 1) {
+                // what only the end needs is found again here, so that the K loop's
+                // registers hold none of it
+                int tid = threadIdx.x - 32 * kFirstEpiWarp;
+                asm volatile("" : "+r"(tid));
+                const int part = static_cast<int>(cluster_ctarank());
+                split_send<SPLIT == 1 ? 2 : SPLIT>(acc, sm.b, tid, part);
+                cluster_sync();
+                exchanged = true;
+                if (split_failed<SPLIT>(&sm.failed, 0, 1)) break;
+                split_add<SPLIT == 1 ? 2 : SPLIT>(acc, sm.b, tid, part, 0, 1);
+                int t_again = blockIdx.x / SPLIT;
+                asm volatile("" : "+r"(t_again));
+                decode_tile(p, t_again, g, mt, nt);
+                const int row = mt * kBM + ((tid >> 5) & 3) * 32 + ((tid & 31) >> 2) + 8 * (4 / SPLIT) * part;
+                const int col = nt * kBN + (tid >> 7) * kHalfN + 2 * (tid & 3);
+                if (is_any_linear<EPI>())
+                    store_linear_any<is_gelu_linear<EPI>(), 4 / SPLIT>(
+                        p, row, col, acc, tid & 31, reinterpret_cast<uint32_t*>(zs + (tid >> 5) * kAnyWarpBytes));
+                else
+                    store_linear<is_gelu_linear<EPI>(), kResVector, 4 / SPLIT>(p, row, col, acc, (tid & 31) >> 2,
+                                                                                nullptr);
+                break;
+            }
             const int row0 = m0 + q * 32 + g8;
             const int col0 = n0 + half * kHalfN + 2 * cq;
             if (EPI == kEpiWgrad) {
@@ -1090,17 +1129,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         if (!ok && lane == 0) record_status(p.status, kStatusTimeout);
+        if (SPLIT > 1 && !ok) sm.failed = 1;
+    }
+    if (SPLIT > 1 && !exchanged) {  // the other roles, and epilogue warps whose wait ran out, meet the exchange here
+        __syncwarp();
+        cluster_sync();
     }
 
+    if (SPLIT > 1) __syncwarp();
     tc_fence_before();
-    __syncthreads();
+    if (SPLIT == 1)
+        __syncthreads();
+    else
+        cluster_sync();  // no CTA leaves while another may still read its sums
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tmem_base, kTmemCols);
 }
 
-template <int EPI>
-int launch_gemm_impl(const TensorMaps& maps, const GemmParams& p, cudaStream_t stream, int grid) {
-    auto kern = gemm_fp8_kernel<EPI>;
+// prepares the kernel on the current device, on first use; 0 or a negative error
+template <int EPI, int SPLIT>
+int configure_gemm(int* device) {
+    auto kern = gemm_fp8_kernel<EPI, SPLIT>;
     static unsigned long long configured = 0;  // one bit per device ordinal
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return -3;
@@ -1109,10 +1158,19 @@ int launch_gemm_impl(const TensorMaps& maps, const GemmParams& p, cudaStream_t s
         cudaFuncAttributes attr;
         if (cudaFuncGetAttributes(&attr, kern) != cudaSuccess || attr.numRegs != kLaunchRegs) return -3;
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(smem_bytes<EPI>())) != cudaSuccess)
+                                 static_cast<int>(smem_bytes<EPI, SPLIT>())) != cudaSuccess)
             return -3;
         configured |= 1ull << dev;
     }
+    *device = dev;
+    return 0;
+}
+
+template <int EPI>
+int launch_gemm_impl(const TensorMaps& maps, const GemmParams& p, cudaStream_t stream, int grid) {
+    int dev = 0;
+    if (configure_gemm<EPI, 1>(&dev) != 0) return -3;
+    auto kern = gemm_fp8_kernel<EPI, 1>;
     if (is_linear<EPI>())
         return launch_dependent(kern, static_cast<unsigned>(grid), kThreads, smem_bytes<EPI>(), stream, maps, p) ==
                        cudaSuccess
@@ -1120,6 +1178,48 @@ int launch_gemm_impl(const TensorMaps& maps, const GemmParams& p, cudaStream_t s
                    : -3;
     kern<<<grid, kThreads, smem_bytes<EPI>(), stream>>>(maps, p);
     return cudaGetLastError() == cudaSuccess ? 0 : -3;
+}
+
+// one tile per cluster of SPLIT CTAs
+template <int EPI, int SPLIT>
+int launch_gemm_split(const TensorMaps& maps, const GemmParams& p, cudaStream_t stream) {
+    int dev = 0;
+    if (configure_gemm<EPI, SPLIT>(&dev) != 0) return -3;
+    return launch_dependent_clusters(gemm_fp8_kernel<EPI, SPLIT>, dim3(SPLIT * p.total_tiles), SPLIT, kThreads,
+                                     smem_bytes<EPI, SPLIT>(), stream, maps, p) == cudaSuccess
+               ? 0
+               : -3;
+}
+
+// clusters of SPLIT CTAs that run at once on the current device (GPCs' sizes
+// leave SMs over), asked once; 0 where that is not known
+template <int SPLIT>
+int gemm_split_slots() {
+    static int slots_on[64] = {0};
+    static unsigned long long known = 0;
+    int dev = 0;
+    if (configure_gemm<kEpiLinearAny, SPLIT>(&dev) != 0) return 0;
+    if (!(known & (1ull << dev))) {
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = SPLIT;
+        attr.val.clusterDim.y = 1;
+        attr.val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(SPLIT, 1, 1);
+        cfg.blockDim = dim3(kThreads, 1, 1);
+        cfg.dynamicSmemBytes = smem_bytes<kEpiLinearAny, SPLIT>();
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, gemm_fp8_kernel<kEpiLinearAny, SPLIT>, &cfg) != cudaSuccess || n < 1) {
+            cudaGetLastError();
+            n = 0;
+        }
+        slots_on[dev] = n;
+        known |= 1ull << dev;
+    }
+    return slots_on[dev];
 }
 
 }  // namespace fp8ll

@@ -39,7 +39,7 @@
 // The per-tensor scaled GEMM (one scale per operand, no scale atoms) runs on
 // CTA pairs in gemm_tensor.cu.
 #include "gemm_kernel.cuh"
-#include "split_pair.cuh"
+#include "split_k.cuh"
 
 namespace fp8ll {
 
@@ -69,7 +69,7 @@ struct __align__(1024) MxSmem {
     uint32_t tmem_base;
     int32_t failed;  // SPLIT 2: an epilogue wait of this CTA ran out
 };
-static_assert(sizeof(MxSmem::b) >= kSplitBytes, "a split tile's sums take the place of B's stages");
+static_assert(sizeof(MxSmem::b) >= kSplitBytes<2>, "a split tile's sums take the place of B's stages");
 template <int EPI>
 constexpr size_t kMxSmemBytes = sizeof(MxSmem) + any_stage_bytes<EPI>() + 1024;
 static_assert(kMxSmemBytes<kEpiLinearAny> <= 232448 && sizeof(MxSmem) % 16 == 0, "shared memory budget");
@@ -108,7 +108,7 @@ __device__ __forceinline__ void decode_mx_tile(const GemmParams& p, int t, int& 
 }
 
 // SPLIT: pairs of a cluster that share a tile's K blocks (1, or 2 for the linear
-// epilogues: see split_pair.cuh)
+// epilogues: see split_k.cuh)
 template <int EPI, int SPLIT>
 __global__ void __cluster_dims__(2 * SPLIT, 1, 1) __launch_bounds__(kThreads, 1)
     gemm_mx_kernel(const __grid_constant__ TensorMaps maps, const __grid_constant__ GemmParams p) {
@@ -346,11 +346,11 @@ __global__ void __cluster_dims__(2 * SPLIT, 1, 1) __launch_bounds__(kThreads, 1)
             mbar_arrive_remote_lane0(acc_empty_leader, lane);
             aph ^= 1u;
             if (SPLIT == 2) {
-                split_send(acc, sm.b, ew * 32 + lane, part);
+                split_send<2>(acc, sm.b, ew * 32 + lane, part);
                 cluster_sync();
                 exchanged = true;
-                if (split_failed(&sm.failed, crank)) break;
-                split_add(acc, sm.b, ew * 32 + lane, part, crank);
+                if (split_failed<2>(&sm.failed, rank, 2)) break;
+                split_add<2>(acc, sm.b, ew * 32 + lane, part, rank, 2);
             }
             // the peer of a pair whose tile ends inside the leader's rows holds
             // only rows outside the matrix and stores nothing

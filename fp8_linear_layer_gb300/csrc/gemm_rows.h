@@ -4,6 +4,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include "rmsnorm.h"
+
 namespace fp8ll {
 
 constexpr int kRowsFeatures = 128;  // rows of B per output tile: the MMA's M
@@ -18,16 +20,20 @@ int rows_cluster(int64_t M, int64_t N, int64_t nkb);
 // Whether this kernel is taken.  Up to 64 tokens always (1x128 / MXFP8 at 64
 // tokens: 17.6 / 16.5 us against the tile kernels' 24.2 / 18.5 at 14336 features
 // over 4096, 17.6 / 16.7 against 69.7 / 44.2 at 4096 over 14336).  Beyond that
-// where a K split shortens the chain of blocks that few tiles would leave to
-// few SMs: 256 x 2112 over 7168 takes 15.3 / 12.4 us against 37.3 / 25.0, 256 x
-// 4096 over 14336 40.1 / 30.4 against 70.5 / 44.7; a split in two of a short K
-// does not pay (256 x 4096 over 1024: 11.4 / 10.2 against 9.4 / 8.5), unless the
-// rows are not 16-byte aligned, which costs this kernel's epilogue less (256 x
-// 2001 over 512 with GELU, residual and Z: 13.8 / 12.9 against 19.4 / 23.8).
-inline bool rows_kernel_taken(int64_t M, int64_t N, int64_t K) {
+// where K is split four or eight ways: 256 x 2112 over 7168 takes 14.2 us on 1x128
+// operands, 18.6 in the tile kernel's four parts; 512 x 1024 over 4096 takes 9.0 us
+// on MXFP8 operands, 13.8 in the pair kernel's two.  A split in two is left to the
+// tile kernels where they split K themselves (1x128, 256 x 4096 over 14336: 39.1 us,
+// 29.6 in four parts) or K is short (256 x 4096 over 1024: 11.4 / 10.2 against 9.4 /
+// 8.5).  It is taken for MXFP8 and per-tensor operands from K = 4096 (128 x 8192 over
+// 4096: 14.2 against 15.1; within 5% either way elsewhere), and for rows that are
+// not 16-byte aligned, which cost this kernel's epilogue less (256 x 2001 over 512
+// with GELU, residual and Z: 13.8 / 12.9 against 19.4 / 23.8).
+inline bool rows_kernel_taken(int64_t M, int64_t N, int64_t K, int recipe) {
     if (M <= 64) return true;
     const int c = rows_cluster(M, N, K / 128);
-    return c >= 4 || (c == 2 && (K / 128 >= 32 || N % 8 != 0));
+    if (c != 2) return c >= 4;
+    return recipe == kRecipeBlock ? N % 8 != 0 && K < 1024 : N % 8 != 0 || K >= 4096;
 }
 
 struct RowsMaps {

@@ -23,7 +23,7 @@
 //               accumulator (16x256b fragments), hands the buffer back to the
 //               leader and stores through the epilogues of the 1x128 kernel.
 #include "gemm_kernel.cuh"
-#include "split_pair.cuh"
+#include "split_k.cuh"
 
 namespace fp8ll {
 
@@ -44,7 +44,7 @@ struct __align__(1024) TpSmem {
     uint32_t tmem_base;
     int32_t failed;  // SPLIT 2: an epilogue wait of this CTA ran out
 };
-static_assert(sizeof(TpSmem::b) >= kSplitBytes, "a split tile's sums take the place of B's stages");
+static_assert(sizeof(TpSmem::b) >= kSplitBytes<2>, "a split tile's sums take the place of B's stages");
 template <int EPI>
 constexpr size_t kTpSmemBytes = sizeof(TpSmem) + any_stage_bytes<EPI>() + 1024;
 static_assert(kTpSmemBytes<kEpiLinearAny> <= 232448 && sizeof(TpSmem) % 16 == 0, "shared memory budget");
@@ -63,7 +63,7 @@ __device__ __forceinline__ void decode_pair_tile(const GemmParams& p, int t, int
 }
 
 // SPLIT: pairs of a cluster that share a tile's K blocks (1, or 2 for the linear
-// epilogues: see split_pair.cuh)
+// epilogues: see split_k.cuh)
 template <int EPI, int SPLIT>
 __global__ void __cluster_dims__(2 * SPLIT, 1, 1) __launch_bounds__(kThreads, 1)
     gemm_tensor_kernel(const __grid_constant__ TensorMaps maps, const __grid_constant__ GemmParams p) {
@@ -261,11 +261,11 @@ __global__ void __cluster_dims__(2 * SPLIT, 1, 1) __launch_bounds__(kThreads, 1)
             mbar_arrive_remote_lane0(acc_empty0 + static_cast<uint32_t>(ab) * acc_empty_step, lane);
             ring_advance<2>(ab, aph);
             if (SPLIT == 2) {
-                split_send(acc, sm.b, ew * 32 + lane, part);
+                split_send<2>(acc, sm.b, ew * 32 + lane, part);
                 cluster_sync();
                 exchanged = true;
-                if (split_failed(&sm.failed, crank)) break;
-                split_add(acc, sm.b, ew * 32 + lane, part, crank);
+                if (split_failed<2>(&sm.failed, rank, 2)) break;
+                split_add<2>(acc, sm.b, ew * 32 + lane, part, rank, 2);
             }
             const float st = __fmul_rn(*p.tsa, *p.tsb);
             const uint64_t st2 = pack_f32x2(st, st);

@@ -46,6 +46,10 @@ int launch_gemm_linear(const TensorMaps& maps, const GemmParams& p, int epi, cud
 // (p.num_m_pairs, p.tiles_per_group in pair tiles) and size their own grids.
 int launch_gemm_mx(const TensorMaps& maps, const GemmParams& p, int epi, cudaStream_t stream);
 int launch_gemm_tensor(const TensorMaps& maps, const GemmParams& p, int epi, cudaStream_t stream);
+// 1x128: over how many CTAs of a cluster the K blocks of each tile are split
+// (1: not), and the kernel that does it (linear epilogues alone)
+int gemm_linear_parts(const GemmParams& p);
+int launch_gemm_linear_parts(const TensorMaps& maps, const GemmParams& p, int epi, int parts, cudaStream_t stream);
 // The same with the K blocks of each tile split over two pairs, for the linear
 // epilogues: whether that pays for these sizes, and the launch.
 bool launch_gemm_mx_splits(const GemmParams& p);

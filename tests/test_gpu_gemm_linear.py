@@ -221,3 +221,41 @@ def test_few_rows_split_over_k_the_same_way_every_time(fp8, recipe, N, K):
     alone, _ = product(fp8, recipe)(one, B)
     torch.cuda.synchronize()
     assert torch.equal(alone, first[3:4]) and fp8.device_status() == 0
+
+
+# tiles of 128 x 256 too few for the SMs, their K blocks in two (1000 x 2110, 513
+# rows of 2050) or four parts of equal or unequal lengths, or whole (1000 x 2110 over 1024)
+@pytest.mark.parametrize("recipe", RECIPES)
+@pytest.mark.parametrize("M,N,K", [(1000, 2110, 1664), (1000, 2112, 1024), (1000, 2112, 1536), (513, 2050, 4480),
+                                   (600, 1023, 1024), (600, 1032, 2176), (385, 1300, 2432), (700, 520, 3968)])
+def test_few_tiles(fp8, recipe, M, N, K):
+    a, b = workloads.normal_bf16((M, K), 11, "a"), workloads.normal_bf16((N, K), 11, "b", std=0.05)
+    bias = workloads.normal_bf16((N,), 11, "bias").cuda()
+    res = workloads.normal_bf16((M, N), 11, "res", std=3.0).cuda()
+    A, B, acc, S = operands(fp8, recipe, a, b, E4M3, E5M2)
+    call = product(fp8, recipe)
+    for bi, act, r in ((None, 0, None), (bias, 0, res), (bias, 1, None), (None, 1, res)):
+        out, aux = call(A, B, bi, act, r, want_aux=bool(act))
+        torch.cuda.synchronize()
+        check(out, aux, acc, S, bi, act, r)
+        place = res.clone() if r is not None else torch.empty_like(out)
+        again, aux2 = call(A, B, bi, act, place if r is not None else None, out=place, want_aux=bool(act))
+        torch.cuda.synchronize()
+        assert torch.equal(out, again) and (aux is None or torch.equal(aux, aux2))
+    assert fp8.device_status() == 0
+
+
+@pytest.mark.parametrize("recipe", RECIPES)
+@pytest.mark.parametrize("M,N,K", [(1000, 2112, 2048), (600, 1023, 2048)])
+def test_a_starved_split_times_out_and_writes_nothing(fp8, recipe, M, N, K):
+    a, b = workloads.normal_bf16((M, K), 6, "a"), workloads.normal_bf16((N, K), 6, "b")
+    A, B, _, _ = operands(fp8, recipe, a, b, E4M3, E4M3)
+    out = torch.full((M, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    fp8.debug_starve_next_gemm(20)
+    product(fp8, recipe)(A, B, out=out)
+    torch.cuda.synchronize()
+    assert fp8.device_status() == fp8.binding.ERR_TIMEOUT and bool((out == 7.0).all())
+    got, _ = product(fp8, recipe)(A, B)
+    again, _ = product(fp8, recipe)(A, B)
+    torch.cuda.synchronize()
+    assert fp8.device_status() == 0 and torch.equal(got, again)
