@@ -1180,46 +1180,4 @@ int launch_gemm_impl(const TensorMaps& maps, const GemmParams& p, cudaStream_t s
     return cudaGetLastError() == cudaSuccess ? 0 : -3;
 }
 
-// one tile per cluster of SPLIT CTAs
-template <int EPI, int SPLIT>
-int launch_gemm_split(const TensorMaps& maps, const GemmParams& p, cudaStream_t stream) {
-    int dev = 0;
-    if (configure_gemm<EPI, SPLIT>(&dev) != 0) return -3;
-    return launch_dependent_clusters(gemm_fp8_kernel<EPI, SPLIT>, dim3(SPLIT * p.total_tiles), SPLIT, kThreads,
-                                     smem_bytes<EPI, SPLIT>(), stream, maps, p) == cudaSuccess
-               ? 0
-               : -3;
-}
-
-// clusters of SPLIT CTAs that run at once on the current device (GPCs' sizes
-// leave SMs over), asked once; 0 where that is not known
-template <int SPLIT>
-int gemm_split_slots() {
-    static int slots_on[64] = {0};
-    static unsigned long long known = 0;
-    int dev = 0;
-    if (configure_gemm<kEpiLinearAny, SPLIT>(&dev) != 0) return 0;
-    if (!(known & (1ull << dev))) {
-        cudaLaunchAttribute attr;
-        attr.id = cudaLaunchAttributeClusterDimension;
-        attr.val.clusterDim.x = SPLIT;
-        attr.val.clusterDim.y = 1;
-        attr.val.clusterDim.z = 1;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(SPLIT, 1, 1);
-        cfg.blockDim = dim3(kThreads, 1, 1);
-        cfg.dynamicSmemBytes = smem_bytes<kEpiLinearAny, SPLIT>();
-        cfg.attrs = &attr;
-        cfg.numAttrs = 1;
-        int n = 0;
-        if (cudaOccupancyMaxActiveClusters(&n, gemm_fp8_kernel<kEpiLinearAny, SPLIT>, &cfg) != cudaSuccess || n < 1) {
-            cudaGetLastError();
-            n = 0;
-        }
-        slots_on[dev] = n;
-        known |= 1ull << dev;
-    }
-    return slots_on[dev];
-}
-
 }  // namespace fp8ll

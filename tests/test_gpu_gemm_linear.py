@@ -259,3 +259,23 @@ def test_a_starved_split_times_out_and_writes_nothing(fp8, recipe, M, N, K):
     again, _ = product(fp8, recipe)(A, B)
     torch.cuda.synchronize()
     assert fp8.device_status() == 0 and torch.equal(got, again)
+
+
+@pytest.mark.parametrize("recipe", ["block", "mx"])
+@pytest.mark.parametrize("M,N,first_row,first_column", [(70000, 32776, 69700, 0), (66000, 32771, 65700, 0),
+                                                        (64, 2 ** 25 + 1005, 0, 2 ** 25)])
+def test_more_than_two_to_the_31_outputs(fp8, recipe, M, N, first_row, first_column):
+    # K of one block: the last rows or features alone give the same bits, whatever kernel computes them
+    K = 128
+    make = {"block": fp8.quantize, "mx": fp8.mx_quantize}[recipe]
+    g = torch.Generator(device="cuda").manual_seed(1)
+    a = torch.randn(M, K, generator=g, device="cuda").bfloat16()
+    b = torch.randn(N, K, generator=g, device="cuda").bfloat16()
+    res = torch.zeros(M, N, dtype=torch.bfloat16, device="cuda")
+    part = torch.randn(M - first_row, N - first_column, generator=g, device="cuda").bfloat16()
+    res[first_row:, first_column:] = part
+    out, _ = product(fp8, recipe)(make(a, E4M3), make(b, E4M3), None, 0, res, out=res)
+    want, _ = product(fp8, recipe)(make(a[first_row:].contiguous(), E4M3), make(b[first_column:].contiguous(), E4M3),
+                                   None, 0, part)
+    torch.cuda.synchronize()
+    assert torch.equal(out[first_row:, first_column:], want) and fp8.device_status() == 0
