@@ -9,9 +9,9 @@
 // not exist, and K is split over a cluster of up to eight CTAs, which add their
 // fp32 sums through distributed shared memory in rank order (deterministic).
 // Two CTAs per SM keep 128 KB or more of B in flight there.  One token, 14336
-// features over 4096: 14.9 us one behind another on 1x128 operands, 0.60 of the
+// features over 4096: 13.1 us one behind another on 1x128 operands, 0.68 of the
 // copy rate; what is left is the launch, the first loads' latency and the join
-// (4.6 us at 7168 x 2048 for 2.2 us of loads).  On the tile kernel 25.5 us, with
+// (4.2 us at 7168 x 2048 for 2.2 us of loads).  On the tile kernel 22.1 us, with
 // fp8 mma.sync fragments straight from global memory 17.1 (43 at 13 tokens on
 // MXFP8: those MMAs take 53 cycles each here).
 // Per CTA of 8 warps:
@@ -435,14 +435,14 @@ int launch_rows_recipe(const RowsMaps& maps, const RowsParams& p, cudaStream_t s
 
 }  // namespace
 
-// CTAs of clusters of c that run at once: the GPCs' sizes leave SMs over (of 152,
-// 120 take part in clusters of 8 CTAs that fill an SM each)
-template <int NT>
+// CTAs of clusters of c, one CTA to an SM, that run at once: the GPCs' sizes leave
+// SMs over (of 152, 144 take part in clusters of 4, 120 in clusters of 8)
 static int rows_slots(int c) {
-    static std::atomic<int> known[64][4];
+    constexpr int NT = 128;  // its shared memory: one CTA fills an SM
+    static std::atomic<int> known[64][3];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-    std::atomic<int>& slot = known[dev][c == 1 ? 0 : c == 2 ? 1 : c == 4 ? 2 : 3];
+    std::atomic<int>& slot = known[dev][c == 2 ? 0 : c == 4 ? 1 : 2];
     int n = slot.load(std::memory_order_relaxed);
     if (n == 0) {
         auto kern = gemm_rows_kernel<kRecipeBlock, NT>;
@@ -470,11 +470,30 @@ static int rows_slots(int c) {
     return n;
 }
 
+// A CTA's chain of K blocks halves with every step, as long as its clusters run at
+// once.  With one CTA per SM a step needs two blocks for each.  With two (up to 64
+// tokens; a cluster of 8 then takes 4 SMs: 36 such clusters run at once, 38 do not)
+// the join of the sums, which grows with the tokens, has to be won back.  us, 1x128,
+// 1 / 32 / 64 tokens:
+//   14336 over 4096  in 1 part  14.9 / 16.1 / 18.7   in 2  13.2 / 14.3 / 16.3
+//   14336 over 1024  in 1        6.1 /  7.2 /  8.7   in 2   6.4 /  7.6 /  9.5
+//    8192 over 4096  in 2       10.0 / 11.0 / 12.7   in 4   9.4 / 10.4 / 11.5
+//    8192 over 1024  in 2        4.8 /  5.6 /  6.8   in 4   4.7 /  5.5 /  6.7
+//    4096 over 14336 in 4       14.4 / 15.6 / 17.0   in 8  13.1 / 14.3 / 16.1
+//    2112 over 4096  in 4        6.1 /  6.4 /  7.3   in 8   5.1 /  5.8 /  7.5
+//    4096 over 5120  in 4        7.8 /  8.4 /  9.4   in 8   7.8 /  9.1 / 10.6
 int rows_cluster(int64_t M, int64_t N, int64_t nkb) {
     const int nt = rows_tokens(M);
     const int64_t tiles = (N + kRowsFeatures - 1) / kRowsFeatures * ((M + nt - 1) / nt);
     int c = 1;
-    while (c < 8 && nkb >= 4 * c && tiles * 2 * c <= (nt == 128 ? rows_slots<128>(2 * c) : rows_slots<64>(2 * c))) c *= 2;
+    while (c < 8) {
+        const int next = 2 * c;
+        const bool alone = nkb >= 2 * next && tiles * next <= rows_slots(next);
+        const int64_t enough = next == 2 ? 16 : next == 4 ? 8 : nt == 16 ? 32 : nt + 32;
+        const bool two_per_sm = nt < 128 && nkb >= enough && tiles * next <= 2 * rows_slots(next < 4 ? next : 4);
+        if (!alone && !two_per_sm) break;
+        c = next;
+    }
     return c;
 }
 

@@ -13,13 +13,12 @@ constexpr int kRowsFeatures = 128;  // rows of B per output tile: the MMA's M
 // tokens (rows of A) per output tile: the MMA's N
 inline int rows_tokens(int64_t M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128; }
 
-// CTAs that share the K blocks of an output tile: as many as run at once with
-// two blocks each, at most 8
+// CTAs that share the K blocks of an output tile, at most 8
 int rows_cluster(int64_t M, int64_t N, int64_t nkb);
 
 // Whether this kernel is taken.  Up to 64 tokens always (1x128 / MXFP8 at 64
-// tokens: 17.6 / 16.5 us against the tile kernels' 24.2 / 18.5 at 14336 features
-// over 4096, 17.6 / 16.7 against 69.7 / 44.2 at 4096 over 14336).  Beyond that
+// tokens: 16.3 / 14.9 us against the tile kernels' 18.9 / 18.0 at 14336 features
+// over 4096, 16.0 / 15.1 against 26.4 / 27.1 at 4096 over 14336).  Beyond that
 // where K is split four or eight ways: 256 x 2112 over 7168 takes 14.2 us on 1x128
 // operands, 18.6 in the tile kernel's four parts; 512 x 1024 over 4096 takes 9.0 us
 // on MXFP8 operands, 13.8 in the pair kernel's two.  A split in two is left to the

@@ -8,9 +8,9 @@
 // change while the reading kernel runs.  One that then calls
 // release_dependents() lets the next kernel's blocks take the places of blocks
 // that finish, with their set-up done by the time the last one does: a product of
-// one token behind another takes 6.8 us instead of 8.0 at 7168 x 2048, 14.9
-// instead of 15.6 at 14336 x 4096.  (Released before the wait, blocks of the next
-// kernel gather on the SMs that finish first: 16.4.)
+// one token behind another takes 6.5 us instead of 7.5 at 7168 x 2048, 12.9
+// instead of 14.7 at 4096 x 14336.  (Released before the wait, blocks of the next
+// kernel gather on the SMs that finish first: slower than without.)
 #pragma once
 #include <cuda_runtime.h>
 
