@@ -299,7 +299,7 @@ static bool overlaps(const void* a, int64_t na, const void* b, int64_t nb) {
 
 // The epilogue arguments the three linear GEMMs share: checks them, fills the
 // parameters and picks the epilogue (without a residual, on aligned rows, the
-// forward GEMM's).
+// forward GEMM's; `pairs`: of the CTA-pair kernels').
 struct LinearArgs {
     const void* bias;
     int act;
@@ -352,7 +352,7 @@ static RowsParams rows_params(int64_t M, int64_t N, int64_t K, int fmt_a, int fm
     return p;
 }
 
-static int fill_linear(const LinearArgs& a, GemmParams& p) {
+static int fill_linear(const LinearArgs& a, GemmParams& p, bool pairs) {
     p.out = a.out;
     p.aux = a.act == FP8LL_ACT_GELU ? a.aux : nullptr;
     p.bias = a.bias;
@@ -363,6 +363,7 @@ static int fill_linear(const LinearArgs& a, GemmParams& p) {
         if (!a.residual) return gelu ? kEpiBiasGelu : a.bias ? kEpiBias : kEpiNone;
         if (aligned16(a.residual) && a.ldr % 8 == 0) return gelu ? kEpiLinearGelu : kEpiLinear;
     }
+    if (pairs && p.N % 2 != 0) return gelu ? kEpiLinearGeluOdd : kEpiLinearOdd;
     return gelu ? kEpiLinearGeluAny : kEpiLinearAny;
 }
 
@@ -996,7 +997,7 @@ int fp8_gemm_linear(int64_t M, int64_t N, int64_t K, const fp8ll_operand_t* A, c
     p.num_groups = 1;
     p.groups[0] = GroupEntry{0, static_cast<int32_t>(K / 128), 0, 0};
     p.total_tiles = p.tiles_per_group;
-    int epi = fill_linear(args, p);
+    int epi = fill_linear(args, p, false);
     std::memset(&maps.z, 0, sizeof(maps.z));
     const int parts = gemm_linear_parts(p);
     if (parts > 1) {
@@ -1041,7 +1042,7 @@ int fp8_mx_gemm_linear(int64_t M, int64_t N, int64_t K, const fp8ll_mx_operand_t
     }
     rc = mx_setup(M, N, K, A, B, maps, p, &dev);
     if (rc != FP8LL_OK) return rc;
-    int epi = fill_linear(args, p);
+    int epi = fill_linear(args, p, true);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (launch_gemm_mx_splits(p)) {
         if (epi < kEpiLinear) epi = args.act == FP8LL_ACT_GELU ? kEpiLinearGelu : kEpiLinear;
@@ -1078,7 +1079,7 @@ int fp8_tensor_gemm_linear(int64_t M, int64_t N, int64_t K, const fp8ll_tensor_o
     }
     rc = tensor_setup(M, N, K, A, B, maps, p, &dev);
     if (rc != FP8LL_OK) return rc;
-    int epi = fill_linear(args, p);
+    int epi = fill_linear(args, p, true);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (launch_gemm_tensor_splits(p)) {
         if (epi < kEpiLinear) epi = args.act == FP8LL_ACT_GELU ? kEpiLinearGelu : kEpiLinear;

@@ -108,15 +108,20 @@ constexpr bool uses_z() {
 }
 template <int EPI>
 constexpr bool is_linear() {
-    return EPI == kEpiLinear || EPI == kEpiLinearGelu || EPI == kEpiLinearAny || EPI == kEpiLinearGeluAny;
+    return EPI == kEpiLinear || EPI == kEpiLinearGelu || EPI == kEpiLinearAny || EPI == kEpiLinearGeluAny ||
+           EPI == kEpiLinearOdd || EPI == kEpiLinearGeluOdd;
 }
 template <int EPI>
 constexpr bool is_gelu_linear() {
-    return EPI == kEpiLinearGelu || EPI == kEpiLinearGeluAny;
+    return EPI == kEpiLinearGelu || EPI == kEpiLinearGeluAny || EPI == kEpiLinearGeluOdd;
 }
 template <int EPI>
 constexpr bool is_any_linear() {
-    return EPI == kEpiLinearAny || EPI == kEpiLinearGeluAny;
+    return EPI == kEpiLinearAny || EPI == kEpiLinearGeluAny || EPI == kEpiLinearOdd || EPI == kEpiLinearGeluOdd;
+}
+template <int EPI>
+constexpr bool is_odd_linear() {
+    return EPI == kEpiLinearOdd || EPI == kEpiLinearGeluOdd;
 }
 
 // the linear epilogue of any sizes stages 8 rows x 128 columns per epilogue warp
@@ -512,7 +517,9 @@ __device__ __forceinline__ void store_dgrad(const GemmParams& p, int row0, int c
 // each element before the store of it: out may be the residual's own buffer.
 enum ResMode : int { kResStaged = 0, kResVector = 1, kResAny = 2 };
 
-constexpr int kAnyRowWords = 68;  // 64 words of a row, padded: the fragments' eight rows fall in distinct banks
+// 64 words of a row and four more: the fragments' eight rows fall in distinct banks,
+// and 17 pieces of 16 bytes hold 128 columns that start inside a piece
+constexpr int kAnyRowWords = 68;
 constexpr uint32_t kAnyWarpBytes = 8 * kAnyRowWords * 4;
 static_assert(any_stage_bytes<kEpiLinearAny>() == kEpiWarps * kAnyWarpBytes, "staging of all epilogue warps");
 
@@ -618,6 +625,139 @@ __device__ __forceinline__ void store_linear_any(const GemmParams& p, int row0, 
             __syncwarp();
             put(p.aux, row, rows);
         }
+    }
+}
+
+// elements between the 16-byte boundary below and g
+__device__ __forceinline__ int row_shift(const uint16_t* g) {
+    return static_cast<int>(reinterpret_cast<uintptr_t>(g) >> 1) & 7;
+}
+
+// Eight rows (those below `rows`) of n <= 128 elements between global memory and
+// the stage, by a whole warp: element x of row i stands at 136 i + row_shift + x, so
+// that whole 16-byte pieces of a row move as such, half a warp to a row, and only
+// the up to seven elements before the first and behind the last piece alone.
+template <bool STORE>
+__device__ __forceinline__ void move_rows(uint16_t* g, int64_t ld, int rows, int n, int lane, uint16_t* stage) {
+    constexpr int kPitch = 2 * kAnyRowWords;
+    uint4 v[4];
+    uint16_t e[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int row = 2 * i + (lane >> 4);
+        uint16_t* gr = g + row * ld;
+        const int shift = row_shift(gr), x = 8 * (lane & 15) - shift;
+        uint4* st = reinterpret_cast<uint4*>(stage + row * kPitch + 8 * (lane & 15));
+        const bool in = row < rows && x >= 0 && x + 8 <= n;
+        if (STORE) {
+            v[i] = *st;
+            if (in) *reinterpret_cast<uint4*>(gr + x) = v[i];
+        } else if (in) {
+            v[i] = *reinterpret_cast<const uint4*>(gr + x);
+        }
+    }
+    const int row = lane >> 2;
+    uint16_t* gr = g + row * ld;
+    const int shift = row_shift(gr);
+    const int head = min((8 - shift) & 7, n), tail = head + ((n - head) & ~7);
+    uint16_t* st = stage + row * kPitch + shift;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int x = (i < 2 ? 0 : tail) + (lane & 3) + 4 * (i & 1);
+        const bool in = row < rows && x < (i < 2 ? head : n);
+        if (STORE) {
+            if (in) gr[x] = st[x];
+        } else if (in) {
+            e[i] = gr[x];
+        }
+    }
+    if (STORE) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = 2 * i + (lane >> 4), k = lane & 15;
+        const int x = 8 * k - row_shift(g + r * ld);
+        if (r < rows && x >= 0 && x + 8 <= n) *reinterpret_cast<uint4*>(stage + r * kPitch + 8 * k) = v[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int x = (i < 2 ? 0 : tail) + (lane & 3) + 4 * (i & 1);
+        if (row < rows && x < (i < 2 ? head : n)) st[x] = e[i];
+    }
+}
+
+// store_linear_any for an odd N, whose rows are 2-byte aligned: single elements cost
+// it four accesses a row where this one makes half of one.  The accumulators become
+// the output's values in place.  MXFP8 with GELU, residual and Z, us, this / that:
+// 438 x 1015 over 384 16.7 / 22.5, 8192 x 4099 over 2048 126 / 167.  (Rows of an
+// even N move faster in words, 438 x 1014: 16.2 / 14.2, and one kernel with both
+// ways took 16.7; in the 1x128 kernels, whose
+// registers the K loop needs, it made the loop spill, 8192 x 4099 over 14336: 728 /
+// 603.)
+template <bool GELU, int ROWS = 4>
+__device__ __forceinline__ void store_linear_odd(const GemmParams& p, int row0, int col0,
+                                                 uint64_t (&acc)[4 * kChunks], int lane, uint32_t* stage_words) {
+    uint16_t* stage = reinterpret_cast<uint16_t*>(stage_words);
+    const uint16_t* bias = static_cast<const uint16_t*>(p.bias);
+    uint16_t* res = const_cast<uint16_t*>(static_cast<const uint16_t*>(p.res));  // read only
+    const int g8 = lane >> 2, cq = lane & 3;
+    const int cbase = col0 - 2 * cq, rbase = row0 - g8;  // the warp's first column and row
+    const int n = p.N - cbase < kHalfN ? p.N - cbase : kHalfN;
+    if (n <= 0 || rbase >= p.M) return;
+    // whether a pair of the residual's columns may straddle words of the stage
+    const bool res_halves = (p.ldr & 1) != 0 || (reinterpret_cast<uintptr_t>(res) & 2u) != 0;
+    if (bias) {
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+            const int col = col0 + 8 * c;
+            const float b0 = col < p.N ? __uint_as_float(static_cast<uint32_t>(bias[col]) << 16) : 0.0f;
+            const float b1 = col + 1 < p.N ? __uint_as_float(static_cast<uint32_t>(bias[col + 1]) << 16) : 0.0f;
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r) {
+                const float2 a = unpack_f32x2(acc[4 * c + r]);
+                acc[4 * c + r] = pack_f32x2(a.x + b0, a.y + b1);
+            }
+        }
+    }
+    uint16_t* own = stage + g8 * 2 * kAnyRowWords + 2 * cq;  // the thread's pair of chunk c: own[shift + 8 c]
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+        const int row = rbase + 8 * r, rows = p.M - row;  // of the eight that exist
+        if (rows <= 0) break;
+        const int64_t off = static_cast<int64_t>(row) * p.N + cbase;
+        auto put = [&](void* base) {  // the values of this r, rounded
+            uint16_t* g = static_cast<uint16_t*>(base) + off;
+            uint16_t* mine = own + row_shift(g + static_cast<int64_t>(g8) * p.N);
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) {
+                const float2 y = unpack_f32x2(acc[4 * c + r]);
+                const uint32_t w = pack_bf16x2(y.x, y.y);
+                mine[8 * c] = static_cast<uint16_t>(w);
+                mine[8 * c + 1] = static_cast<uint16_t>(w >> 16);
+            }
+            __syncwarp();
+            move_rows<true>(g, p.N, rows, n, lane, stage);
+            __syncwarp();
+        };
+        if (GELU && p.aux) put(p.aux);
+        const uint16_t* mine = own;
+        if (res) {
+            uint16_t* g = res + row * p.ldr + cbase;
+            move_rows<false>(g, p.ldr, rows, n, lane, stage);
+            mine += row_shift(g + g8 * p.ldr);
+            __syncwarp();
+        }
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+            uint32_t w = 0u;
+            if (res)
+                w = res_halves ? mine[8 * c] | static_cast<uint32_t>(mine[8 * c + 1]) << 16
+                               : *reinterpret_cast<const uint32_t*>(mine + 8 * c);
+            const float2 z = unpack_f32x2(acc[4 * c + r]);
+            const float2 y = GELU ? gelu_tanh2(z.x, z.y) : z;
+            acc[4 * c + r] = pack_f32x2(y.x + bf16_lo(w), y.y + bf16_hi(w));
+        }
+        if (res) __syncwarp();
+        put(p.out);
     }
 }
 

@@ -362,12 +362,15 @@ __global__ void __cluster_dims__(2 * SPLIT, 1, 1) __launch_bounds__(kThreads, 1)
             } else if (EPI == kEpiNone || EPI == kEpiBias || EPI == kEpiBiasGelu) {
                 store_fprop<EPI>(p, row0, col0, acc);
             } else if (is_linear<EPI>()) {
-                if (is_any_linear<EPI>())
-                    store_linear_any<is_gelu_linear<EPI>(), 4 / SPLIT>(
-                        p, row0, col0, acc, lane,
-                        reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(&sm) + sizeof(MxSmem) + ew * kAnyWarpBytes));
-                else
+                if (is_any_linear<EPI>()) {
+                    uint32_t* stage = reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(&sm) + sizeof(MxSmem) + ew * kAnyWarpBytes);
+                    if (is_odd_linear<EPI>())
+                        store_linear_odd<is_gelu_linear<EPI>(), 4 / SPLIT>(p, row0, col0, acc, lane, stage);
+                    else
+                        store_linear_any<is_gelu_linear<EPI>(), 4 / SPLIT>(p, row0, col0, acc, lane, stage);
+                } else {
                     store_linear<is_gelu_linear<EPI>(), kResVector, 4 / SPLIT>(p, row0, col0, acc, g8, nullptr);
+                }
             } else {
                 float* band = (EPI == kEpiDgeluBgrad) ? p.workspace + (static_cast<int64_t>(m0 / kBM) * 4 + q) * p.N
                                                       : nullptr;
@@ -451,6 +454,8 @@ int launch_gemm_mx_split(const TensorMaps& maps, const GemmParams& p, int epi, c
         case kEpiLinearGelu: return launch_mx_impl<kEpiLinearGelu, 2>(maps, p, stream);
         case kEpiLinearAny: return launch_mx_impl<kEpiLinearAny, 2>(maps, p, stream);
         case kEpiLinearGeluAny: return launch_mx_impl<kEpiLinearGeluAny, 2>(maps, p, stream);
+        case kEpiLinearOdd: return launch_mx_impl<kEpiLinearOdd, 2>(maps, p, stream);
+        case kEpiLinearGeluOdd: return launch_mx_impl<kEpiLinearGeluOdd, 2>(maps, p, stream);
         default: return -3;
     }
 }
@@ -467,6 +472,8 @@ int launch_gemm_mx(const TensorMaps& maps, const GemmParams& p, int epi, cudaStr
         case kEpiLinearGelu: return launch_mx_impl<kEpiLinearGelu>(maps, p, stream);
         case kEpiLinearAny: return launch_mx_impl<kEpiLinearAny>(maps, p, stream);
         case kEpiLinearGeluAny: return launch_mx_impl<kEpiLinearGeluAny>(maps, p, stream);
+        case kEpiLinearOdd: return launch_mx_impl<kEpiLinearOdd>(maps, p, stream);
+        case kEpiLinearGeluOdd: return launch_mx_impl<kEpiLinearGeluOdd>(maps, p, stream);
         default: return -3;
     }
 }

@@ -23,6 +23,8 @@ enum EpiKind : int {
     kEpiLinearGelu = 8,
     kEpiLinearAny = 9,    // any sizes and alignment, residual optional
     kEpiLinearGeluAny = 10,
+    kEpiLinearOdd = 11,   // the same for an odd N (CTA pairs)
+    kEpiLinearGeluOdd = 12,
 };
 
 // One schedulable group of output tiles: all tiles of a group share the same
@@ -60,7 +62,7 @@ struct GemmParams {
     uint8_t* qout;        // kEpiDgeluQuant: e5m2 codes of the bf16 dZ, [M][N]
     float* qscale;        // kEpiDgeluQuant: their scales, [N/128][qsld]
     int64_t qsld;
-    const void* res;      // kEpiLinear*: bf16 residual [M][ldr] (null allowed with kEpiLinear*Any)
+    const void* res;      // kEpiLinear*: bf16 residual [M][ldr] (null: none, but in the whole 1x128 kEpiLinear, kEpiLinearGelu)
     int64_t ldr;
     GroupEntry groups[kMaxGroups];
 };

@@ -281,12 +281,15 @@ __global__ void __cluster_dims__(2 * SPLIT, 1, 1) __launch_bounds__(kThreads, 1)
             } else if (EPI == kEpiNone || EPI == kEpiBias || EPI == kEpiBiasGelu) {
                 store_fprop<EPI>(p, row0, col0, acc);
             } else if (is_linear<EPI>()) {
-                if (is_any_linear<EPI>())
-                    store_linear_any<is_gelu_linear<EPI>(), 4 / SPLIT>(
-                        p, row0, col0, acc, lane,
-                        reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(&sm) + sizeof(TpSmem) + ew * kAnyWarpBytes));
-                else
+                if (is_any_linear<EPI>()) {
+                    uint32_t* stage = reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(&sm) + sizeof(TpSmem) + ew * kAnyWarpBytes);
+                    if (is_odd_linear<EPI>())
+                        store_linear_odd<is_gelu_linear<EPI>(), 4 / SPLIT>(p, row0, col0, acc, lane, stage);
+                    else
+                        store_linear_any<is_gelu_linear<EPI>(), 4 / SPLIT>(p, row0, col0, acc, lane, stage);
+                } else {
                     store_linear<is_gelu_linear<EPI>(), kResVector, 4 / SPLIT>(p, row0, col0, acc, g8, nullptr);
+                }
             } else {
                 float* band = (EPI == kEpiDgeluBgrad) ? p.workspace + (static_cast<int64_t>(m0 / kBM) * 4 + q) * p.N
                                                       : nullptr;
@@ -370,6 +373,8 @@ int launch_gemm_tensor_split(const TensorMaps& maps, const GemmParams& p, int ep
         case kEpiLinearGelu: return launch_tensor_impl<kEpiLinearGelu, 2>(maps, p, stream);
         case kEpiLinearAny: return launch_tensor_impl<kEpiLinearAny, 2>(maps, p, stream);
         case kEpiLinearGeluAny: return launch_tensor_impl<kEpiLinearGeluAny, 2>(maps, p, stream);
+        case kEpiLinearOdd: return launch_tensor_impl<kEpiLinearOdd, 2>(maps, p, stream);
+        case kEpiLinearGeluOdd: return launch_tensor_impl<kEpiLinearGeluOdd, 2>(maps, p, stream);
         default: return -3;
     }
 }
@@ -386,6 +391,8 @@ int launch_gemm_tensor(const TensorMaps& maps, const GemmParams& p, int epi, cud
         case kEpiLinearGelu: return launch_tensor_impl<kEpiLinearGelu>(maps, p, stream);
         case kEpiLinearAny: return launch_tensor_impl<kEpiLinearAny>(maps, p, stream);
         case kEpiLinearGeluAny: return launch_tensor_impl<kEpiLinearGeluAny>(maps, p, stream);
+        case kEpiLinearOdd: return launch_tensor_impl<kEpiLinearOdd>(maps, p, stream);
+        case kEpiLinearGeluOdd: return launch_tensor_impl<kEpiLinearGeluOdd>(maps, p, stream);
         default: return -3;
     }
 }
