@@ -14,8 +14,9 @@ block on a few tokens.
     dN = dZ W1
     dh = rmsnorm'(dN) + dY,  dgamma                        (dh: the gradient of x and of r)
 
-No arithmetic here: every step is a library kernel.  Run as a module for the
-time of a step: ``python -m fp8_linear_layer_gb300.feedforward``.
+No arithmetic here but the bias gradients' sum over calls: every step is a
+library kernel.  Run as a module for the time of a step: ``python -m
+fp8_linear_layer_gb300.feedforward``.
 """
 import torch
 
@@ -52,6 +53,7 @@ class FeedForwardBlock:
         self.dN, self.dX = bf16(m, k), bf16(m, k)
         self.dW1, self.dW2 = f32(n, k), f32(k, n)
         self.db1, self.db2, self.dgamma = f32(n), f32(k), f32(k)
+        self.db1_new, self.db2_new = f32(n), f32(k)  # one call's
         self.grads = K.GradList([self.dW1, self.dW2, self.db1, self.db2, self.dgamma])
         self.cast_work = torch.empty((B.workspace_size(m, max(k, n)) // 4,), dtype=torch.float32, device=dev)
         self.norm_work = K.rmsnorm_workspace(m, k, dev)
@@ -77,11 +79,13 @@ class FeedForwardBlock:
 
     def backward(self, dY):
         """The gradient of x (and of the residual) from that of Y; the parameters'
-        gradients are added up, but for the biases', which are this call's."""
-        B.quantize_dbias(dY, B.E5M2, out_t=self.dYTq, out=self.dYq, dbias=self.db2, workspace=self.cast_work)
+        gradients are added up."""
+        B.quantize_dbias(dY, B.E5M2, out_t=self.dYTq, out=self.dYq, dbias=self.db2_new, workspace=self.cast_work)
+        self.db2.add_(self.db2_new)
         B.gemm_wgrad(self.dYTq, self.UTq, self.dW2)
         B.gemm_dgrad(self.dYq, self.W2Tq, self.Z, B.EPI_DGELU, out=self.dZ)
-        B.quantize_dbias(self.dZ, B.E5M2, out_t=self.dZTq, out=self.dZq, dbias=self.db1, workspace=self.cast_work)
+        B.quantize_dbias(self.dZ, B.E5M2, out_t=self.dZTq, out=self.dZq, dbias=self.db1_new, workspace=self.cast_work)
+        self.db1.add_(self.db1_new)
         B.gemm_wgrad(self.dZTq, self.norm.cols, self.dW1)
         K.gemm_linear(self.dZq, self.W1Tq, out=self.dN)
         K.rmsnorm_backward(self.dN, self.norm.h, self.gamma, self.norm.rstd, residual_grad=dY, out=self.dX,

@@ -56,7 +56,7 @@ def test_a_training_step(fp8, made):
     assert off(block.dW2, grads["dW2"]) < 0.1 and off(block.db2, grads["db2"]) < 2e-3
     assert off(block.dW1, grads["dW1"]) < 0.15 and off(block.db1, grads["db1"]) < 0.15
     assert off(dX.float() - dY.float(), dh - dY.float()) < 0.15 and off(block.dgamma, grads["dgamma"]) < 0.15
-    # a second micro-batch adds up (biases: the last one's)
+    # a second micro-batch adds up
     first = block.dW1.clone()
     block.forward(x, r)
     block.backward(dY)
@@ -100,3 +100,18 @@ def test_a_step_in_a_graph(fp8, made):
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(block.grads.grads, want)) and fp8.device_status() == 0
+
+
+def test_bias_gradients_add_up(fp8, made):
+    block, _, (x, r, dY) = made
+    block.zero_grad()
+    block.forward(x, r)
+    block.backward(dY)
+    torch.cuda.synchronize()
+    first = [block.db1.clone(), block.db2.clone()]
+    block.forward(x, r)
+    block.backward(dY)
+    torch.cuda.synchronize()
+    # twice the same sums: doubling is exact
+    assert torch.equal(block.db1, 2 * first[0]) and torch.equal(block.db2, 2 * first[1])
+    assert float(first[0].abs().max()) > 0 and float(first[1].abs().max()) > 0
