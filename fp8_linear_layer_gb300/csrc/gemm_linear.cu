@@ -57,11 +57,13 @@ static int split_slots() {
 // and where rows are not 16-byte aligned, which makes every row that is stored dearer:
 //   600 x 1023 over 1536    16.4 / 22.9   12.7 / 16.3   12.1 / 14.1
 //                   1024    14.0 / 20.5   11.5 / 15.3   11.5 / 13.5
+//   1000 x 2111 over 768    14.3 / 19.5   13.4 / 15.4
+//   1000 x 2110 over 768    11.8 / 15.5   12.2 / 14.0
 int gemm_linear_parts(const GemmParams& p) {
     const int nkb = p.groups[0].nkb;
     const bool odd_rows = p.N % 8 != 0;
-    if (nkb >= (odd_rows ? 8 : 16) && p.total_tiles <= split_slots<4>()) return 4;
-    if (nkb >= (odd_rows ? 8 : 12) && p.total_tiles <= split_slots<2>()) return 2;
+    if (nkb >= (odd_rows ? 6 : 16) && p.total_tiles <= split_slots<4>()) return 4;
+    if (nkb >= (odd_rows ? 6 : 12) && p.total_tiles <= split_slots<2>()) return 2;
     return 1;
 }
 

@@ -32,7 +32,7 @@ inline bool rows_kernel_taken(int64_t M, int64_t N, int64_t K, int recipe) {
     if (M <= 64) return true;
     const int c = rows_cluster(M, N, K / 128);
     if (c != 2) return c >= 4;
-    return recipe == kRecipeBlock ? N % 8 != 0 && K < 1024 : N % 8 != 0 || K >= 4096;
+    return recipe == kRecipeBlock ? N % 8 != 0 && K < 768 : N % 8 != 0 || K >= 4096;
 }
 
 struct RowsMaps {

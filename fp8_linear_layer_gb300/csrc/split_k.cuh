@@ -106,10 +106,18 @@ __device__ __forceinline__ bool split_failed(const int32_t* failed, uint32_t fir
 }
 
 // Whether the split in two of the CTA pairs' tiles is taken: every tile's cluster
-// of four runs at once, and K is long enough to pay for the exchange.  MXFP8, 1000
-// x 2112 with GELU, residual and Z, split / whole: 22.5 / 31.2 us over 7168, 14.9 /
-// 17.0 over 2048; with the residual alone 13.1 / 13.6 over 2048, but 11.5 / 10.7
-// over 1024.
-inline bool split_pays(const GemmParams& p, int slots) { return p.total_tiles <= slots && p.groups[0].nkb >= 16; }
+// of four runs at once, and K is long enough to pay for the exchange, part of which
+// is won back because a part's threads store fewer rows: earlier where rows that are
+// not 16-byte aligned make each dearer.  It does not depend on what is stored, so
+// that a product's sums do not.  MXFP8, us, split / whole, with GELU, residual and Z
+// | the residual | neither:
+//   1000 x 2112 over 7168  21.6 / 31.2
+//                    1536  13.3 / 14.4 | 11.5 / 11.1 | 10.7 / 10.0
+//   1000 x 2111 over  768  14.7 / 18.3 | 12.2 / 12.5 | 10.0 /  9.1
+//   1000 x 2110 over  768  13.1 / 15.5 | 11.1 / 10.8 |  9.3 /  7.9
+//                     512  12.7 / 14.8 | 10.8 / 10.2 |  8.9 /  7.2
+inline bool split_pays(const GemmParams& p, int slots) {
+    return p.total_tiles <= slots && p.groups[0].nkb >= (p.N % 8 != 0 ? 6 : 16);
+}
 
 }  // namespace fp8ll

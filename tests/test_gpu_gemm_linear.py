@@ -279,3 +279,23 @@ def test_more_than_two_to_the_31_outputs(fp8, recipe, M, N, first_row, first_col
                                    None, 0, part)
     torch.cuda.synchronize()
     assert torch.equal(out[first_row:, first_column:], want) and fp8.device_status() == 0
+
+
+@pytest.mark.parametrize("recipe", RECIPES)
+@pytest.mark.parametrize("M,N,K", [(438, 4111, 768), (500, 4110, 896), (900, 2051, 640)])
+def test_few_tiles_of_unaligned_rows(fp8, recipe, M, N, K):
+    a, b = workloads.normal_bf16((M, K), 12, "a"), workloads.normal_bf16((N, K), 12, "b", std=0.05)
+    bias = workloads.normal_bf16((N,), 12, "bias").cuda()
+    wide = workloads.normal_bf16((M, N + 5), 12, "res", std=3.0).cuda()
+    A, B, acc, S = operands(fp8, recipe, a, b, E4M3, E4M3)
+    call = product(fp8, recipe)
+    want = None
+    for act, r in ((0, None), (0, wide[:, 3:N + 3]), (1, wide[:, :N]), (1, None)):
+        out, aux = call(A, B, bias, act, r, want_aux=bool(act))
+        torch.cuda.synchronize()
+        check(out, aux, acc, S, bias, act, r.contiguous() if r is not None else None)
+        # the sums do not depend on what is done with them
+        z = out if want is None else aux if act else None
+        want = out if want is None else want
+        assert z is None or torch.equal(z, want)
+    assert fp8.device_status() == 0
