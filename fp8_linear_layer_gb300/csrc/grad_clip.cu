@@ -252,12 +252,15 @@ int run(int64_t count, const fp8ll_grad_t* grads, int scale, float max_norm, flo
         cudaStream_t stream, int num_sms) {
     Table<CAP> t;
     int used = 0, launches = 0;
+    int held = -1;  // the launch whose tensors t holds
     int64_t starts[kClipMaxTensors / kClipTensorsPerLaunch + 1];
     for (int64_t i = 0; i < count;) {
-        starts[launches] = i;
-        i = fill(t, count, grads, i);
-        if (t.count == 0) break;
-        ++launches;
+        const int64_t first = i;
+        i = fill(t, count, grads, first);
+        held = -1;
+        if (t.count == 0) break;  // only empty tensors were left
+        held = launches;
+        starts[launches++] = first;
         const int g = grid_of(t.chunks, num_sms);
         if (launch_dependent(grad_norm_kernel<CAP>, static_cast<unsigned>(g), kThreadsClip, 0, stream, t,
                              partials + used) != cudaSuccess)
@@ -272,7 +275,7 @@ int run(int64_t count, const fp8ll_grad_t* grads, int scale, float max_norm, flo
     }
     // the launches of pass 1 in reverse order: the last tensors are the ones in L2
     for (int k = launches - 1; k >= 0; --k) {
-        if (launches > 1) fill(t, count, grads, starts[k]);
+        if (k != held) fill(t, count, grads, starts[k]);
         if (launch_dependent(grad_scale_kernel<CAP>, static_cast<unsigned>(grid_of(t.chunks, num_sms)), kThreadsClip, 0,
                              stream, t, partials, used, max_norm, k == launches - 1 ? norm : nullptr) != cudaSuccess)
             return -3;
