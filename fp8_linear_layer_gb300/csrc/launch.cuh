@@ -36,7 +36,9 @@ cudaError_t launch_dependent_clusters(void (*kern)(Params...), dim3 grid, unsign
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = cluster > 0 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kern, static_cast<Params>(args)...);
+    const cudaError_t rc = cudaLaunchKernelEx(&cfg, kern, static_cast<Params>(args)...);
+    if (rc != cudaSuccess) cudaGetLastError();  // the caller reports it: not left for the next check of other code
+    return rc;
 }
 
 template <typename... Params, typename... Args>
