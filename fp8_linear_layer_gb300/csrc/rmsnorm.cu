@@ -2,7 +2,7 @@
 // output, and its backward pass.
 //
 //   h = bf16(x + r)                     (the residual stream; h = x without r)
-//   rstd = 1 / sqrt(mean_c h^2 + eps)
+//   rstd = 1 / sqrt(mean_c h^2 + eps)   (0 where that root is 0)
 //   y = fl32(fl32(h rstd) gamma)        -> fp8 codes and scales, and / or bf16
 //
 // The norm is taken of the rounded h, which is what the stream carries on and
@@ -177,7 +177,9 @@ __global__ void __launch_bounds__(MAXT) rmsnorm_rows_kernel(const __grid_constan
         fetch(r + gridDim.x);
         sq = block_sum(sq, part[k & 1]);
         // correctly rounded: an ulp here moves every code of the row that lies near a tie
-        const float rstd = __frsqrt_rn(__fdiv_rn(sq, static_cast<float>(p.cols)) + p.eps);
+        const float ms = __fdiv_rn(sq, static_cast<float>(p.cols)) + p.eps;
+        // a row of zeros without eps stays zeros, here and in the backward pass (a NaN is none)
+        const float rstd = ms == 0.0f ? 0.0f : __frsqrt_rn(ms);
         if (threadIdx.x == 0) p.rstd[r] = rstd;
         const uint64_t rstd2 = pack_f32x2(rstd, rstd);
         uint64_t y[V][4];

@@ -448,6 +448,7 @@ int fp8_tensor_gemm_linear(int64_t M, int64_t N, int64_t K, const fp8ll_tensor_o
 /* Root-mean-square norm of a residual stream, cast to fp8 for the GEMMs:
  *   h = bf16(x + residual)               (h = x without a residual)
  *   rstd = 1 / sqrt(mean(h^2) + eps)     per row, of the rounded h
+ *                                        (0 where mean(h^2) + eps is 0)
  *   y = fl32(fl32(h * rstd) * gamma)     -> codes and scales by the cast rules,
  *                                           from fp32 (no bf16 rounding first)
  *   x, residual: bf16 [rows][ldx / ldr], 16-byte aligned, leading dimensions
@@ -466,7 +467,10 @@ int fp8_tensor_gemm_linear(int64_t M, int64_t N, int64_t K, const fp8ll_tensor_o
  * The per-tensor form casts with *amax_in, writes *scale and, if amax_out is
  * not NULL, max|y| (for the history of the next step).
  * No output may overlap another or an input, but for h as above.
- * rows == 0 or cols == 0 is a no-op.  A row of zeros gives zeros with scale 1. */
+ * rows == 0 or cols == 0 is a no-op.  A row of zeros gives zeros with scale 1,
+ * also with eps = 0.  Squares are taken in fp32: a row whose sum of squares
+ * overflows (an element of 1.8e19 or more) has rstd 0, and with eps = 0 rows of
+ * |h| below 1e-19 lose digits, and count as zeros where the mean square is 0 there. */
 int fp8_rmsnorm_quantize(const void* x_bf16, const void* residual_bf16, const void* gamma_bf16, int64_t rows,
                          int64_t cols, int64_t ldx, int64_t ldr, float eps, int fmt, void* h_bf16, float* rstd,
                          void* y_bf16, uint8_t* q_rows, float* scale_rows, int64_t scale_ld_rows, uint8_t* q_cols,
