@@ -325,8 +325,9 @@ __global__ void __launch_bounds__(256, kColsCtas) rmsnorm_cols_kernel(const __gr
                 a_lo = fmaxf(a_lo, fabsf(v.x));
                 a_hi = fmaxf(a_hi, fabsf(v.y));
             }
-            a_lo = __fmul_rn(a_lo, fabsf(g_lo));
-            a_hi = __fmul_rn(a_hi, fabsf(g_hi));
+            // a maximum over NaN (gamma NaN, or infinite over zeros) is 0, as of the values one by one
+            a_lo = fmaxf(__fmul_rn(a_lo, fabsf(g_lo)), 0.0f);
+            a_hi = fmaxf(__fmul_rn(a_hi, fabsf(g_hi)), 0.0f);
             if (RECIPE == kRecipeBlock) {
 #pragma unroll
                 for (int off = 1; off <= 2; off <<= 1) {
