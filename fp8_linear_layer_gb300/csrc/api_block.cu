@@ -2,6 +2,7 @@
 // host-side validation and launches.  No allocation, no synchronization.
 #include <cmath>
 #include <cstdint>
+#include <initializer_list>
 
 #include "fp8ll.h"
 #include "grad_clip.h"
@@ -160,8 +161,11 @@ int fp8_tensor_rmsnorm_quantize(const void* x_bf16, const void* residual_bf16, c
     p.amax_in = amax_in;
     p.scale = scale;
     p.amax_out = amax_out;
-    const Range scales[2] = {{scale, 4}, {amax_out, 4}};
+    const Range scales[2] = {{scale, 4}, {amax_out, 4}}, in{amax_in, 4};
     if (!apart(p, scales, 2)) return FP8LL_ERR_INVALID_ARG;
+    const int64_t n = rows * cols;
+    for (const Range& out : {Range{h_bf16, 2 * n}, {rstd, 4 * rows}, {y_bf16, 2 * n}, {q_rows, n}, {q_cols, n}})
+        if (share(out, in)) return FP8LL_ERR_INVALID_ARG;
     return launch(p, kRecipeTensor, fmt, stream);
 }
 
