@@ -26,7 +26,11 @@ def _stream() -> int:
 
 
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
-    return None if t is None else t.data_ptr()
+    """Address of a tensor on the GPU (or none): the kernels take no host memory."""
+    if t is None:
+        return None
+    assert t.is_cuda
+    return t.data_ptr()
 
 
 # -------------------------------------------------------------------- norm ----
@@ -79,17 +83,17 @@ def empty_tensor_rmsnorm(rows: int, cols: int, fmt: int, rows_too: bool = True, 
 
 
 def _rows(t, shape):
-    """Leading dimension of a bf16 matrix of this shape with packed rows."""
+    """Leading dimension of a bf16 matrix of this shape with packed rows, on the GPU."""
     ld, one = t.stride()
-    assert t.dtype is _bf16 and t.shape == shape and (one == 1 or shape[1] == 1)
+    assert t.dtype is _bf16 and t.shape == shape and (one == 1 or shape[1] == 1) and t.is_cuda
     return ld if shape[0] > 1 else shape[1]
 
 
 def _packed(t, dtype, shape):
-    """Address of a contiguous tensor of this type and shape (or none)."""
+    """Address of a contiguous tensor of this type and shape, on the GPU (or none)."""
     if t is None:
         return None
-    assert t.dtype is dtype and t.shape == shape and t.is_contiguous()
+    assert t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.is_cuda
     return t.data_ptr()
 
 
@@ -100,7 +104,8 @@ def _norm_args(x, gamma, eps, fmt, residual, out):
     if residual is not None:
         ldr = _rows(residual, shape)
         assert out.h is not None, "the sum x + residual needs its place (h)"
-    return (x.data_ptr(), _ptr(residual), _packed(gamma, _bf16, (cols,)), rows, cols, ldx, ldr, eps, fmt)
+    return (x.data_ptr(), None if residual is None else residual.data_ptr(), _packed(gamma, _bf16, (cols,)), rows, cols,
+            ldx, ldr, eps, fmt)
 
 
 def _norm_outs(shape, out):
@@ -126,9 +131,9 @@ def rmsnorm_quantize(x: torch.Tensor, gamma: torch.Tensor, eps: float, fmt: int,
     qr = sr = qc = sc = None
     ldr = ldc = 0
     if out.rows is not None:
-        qr, sr, ldr = _codes(out.rows, fmt, m, k), out.rows.scale.data_ptr(), out.rows.scale.stride(0)
+        qr, sr, ldr = _codes(out.rows, fmt, m, k), _ptr(out.rows.scale), out.rows.scale.stride(0)
     if out.cols is not None:
-        qc, sc, ldc = _codes(out.cols, fmt, k, m), out.cols.scale.data_ptr(), out.cols.scale.stride(0)
+        qc, sc, ldc = _codes(out.cols, fmt, k, m), _ptr(out.cols.scale), out.cols.scale.stride(0)
     _check(lib().fp8_rmsnorm_quantize(*args, *_norm_outs(x.shape, out), qr, sr, ldr, qc, sc, ldc, _stream()),
            "fp8_rmsnorm_quantize")
     return out
@@ -144,9 +149,9 @@ def mx_rmsnorm_quantize(x: torch.Tensor, gamma: torch.Tensor, eps: float, fmt: i
     m, k = x.shape
     qr = sr = qc = sc = None
     if out.rows is not None:
-        qr, sr = _codes(out.rows, fmt, m, k), out.rows.sf.data_ptr()
+        qr, sr = _codes(out.rows, fmt, m, k), _ptr(out.rows.sf)
     if out.cols is not None:
-        qc, sc = _codes(out.cols, fmt, k, m), out.cols.sf.data_ptr()
+        qc, sc = _codes(out.cols, fmt, k, m), _ptr(out.cols.sf)
     _check(lib().fp8_mx_rmsnorm_quantize(*args, *_norm_outs(x.shape, out), qr, sr, qc, sc, _stream()),
            "fp8_mx_rmsnorm_quantize")
     return out
@@ -161,15 +166,15 @@ def tensor_rmsnorm_quantize(x: torch.Tensor, gamma: torch.Tensor, eps: float, fm
     if out is None:
         out = empty_tensor_rmsnorm(x.shape[0], x.shape[1], fmt, rows, cols, residual is not None, y, x.device)
     args = _norm_args(x, gamma, eps, fmt, residual, out)
-    assert amax_in.dtype is _f32 and amax_in.numel() == 1
+    assert amax_in.dtype is _f32 and amax_in.numel() == 1 and amax_in.is_cuda
     m, k = x.shape
     qr = qc = scale = spare = None
     if out.rows is not None:
-        qr, scale = _codes(out.rows, fmt, m, k), out.rows.scale.data_ptr()
+        qr, scale = _codes(out.rows, fmt, m, k), _ptr(out.rows.scale)
     if out.cols is not None:
         qc = _codes(out.cols, fmt, k, m)
         assert scale in (None, out.cols.scale.data_ptr()), "both orientations share one scale"
-        scale = out.cols.scale.data_ptr()
+        scale = _ptr(out.cols.scale)
     if scale is None:  # only the bf16 form was asked for
         spare = torch.empty((1,), dtype=_f32, device=x.device)
         scale = spare.data_ptr()
@@ -202,7 +207,7 @@ def rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, gamma: torch.Tensor, rst
         dgamma = torch.empty((cols,), dtype=_f32, device=h.device)
     if workspace is None:
         workspace = rmsnorm_workspace(rows, cols, h.device)
-    assert workspace.is_contiguous()
+    assert workspace.is_contiguous() and workspace.is_cuda
     _check(lib().fp8_rmsnorm_backward(dy.data_ptr(), h.data_ptr(), _packed(gamma, _bf16, (cols,)),
                                       _packed(rstd, _f32, (rows,)), _ptr(r), rows, cols, ldd, ldh, ldr,
                                       _packed(out, _bf16, shape), _packed(dgamma, _f32, (cols,)), int(accumulate),
@@ -213,7 +218,10 @@ def rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, gamma: torch.Tensor, rst
 
 # ----------------------------------------------------------------- product ----
 
-def _linear_args(M, N, bias, act, residual, out, aux, want_aux, device):
+def _linear_args(A, W, scales, bias, act, residual, out, aux, want_aux):
+    M, N, device = A.rows, W.rows, A.q.device
+    assert A.k == W.k
+    assert A.q.is_cuda and W.q.is_cuda and scales[0].is_cuda and scales[1].is_cuda
     if out is None:
         out = torch.empty((M, N), dtype=_bf16, device=device)
     if aux is None and want_aux:
@@ -232,8 +240,7 @@ def gemm_linear(A: Fp8Tensor, W: Fp8Tensor, bias: Optional[torch.Tensor] = None,
     Z-or-None), Z = A W^T + bias with ``want_aux`` or ``aux`` (GELU only).
     ``out`` may be the residual itself.  Few rows run a kernel of their own."""
     M, N = A.rows, W.rows
-    out, aux, args, dst = _linear_args(M, N, bias, act, residual, out, aux, want_aux, A.q.device)
-    assert A.k == W.k
+    out, aux, args, dst = _linear_args(A, W, (A.scale, W.scale), bias, act, residual, out, aux, want_aux)
     oa, ob = A.operand(), W.operand()
     _check(lib().fp8_gemm_linear(M, N, A.k, ctypes.byref(oa), ctypes.byref(ob), *args, int(acc), *dst, _stream()),
            "fp8_gemm_linear")
@@ -245,8 +252,7 @@ def mx_gemm_linear(A: Fp8MxTensor, W: Fp8MxTensor, bias: Optional[torch.Tensor] 
                    aux: Optional[torch.Tensor] = None, want_aux: bool = False):
     """``gemm_linear`` on MXFP8 operands."""
     M, N = A.rows, W.rows
-    out, aux, args, dst = _linear_args(M, N, bias, act, residual, out, aux, want_aux, A.q.device)
-    assert A.k == W.k
+    out, aux, args, dst = _linear_args(A, W, (A.sf, W.sf), bias, act, residual, out, aux, want_aux)
     oa, ob = A.operand(), W.operand()
     _check(lib().fp8_mx_gemm_linear(M, N, A.k, ctypes.byref(oa), ctypes.byref(ob), *args, *dst, _stream()),
            "fp8_mx_gemm_linear")
@@ -259,8 +265,7 @@ def tensor_gemm_linear(A: Fp8TensorScaled, W: Fp8TensorScaled, bias: Optional[to
                        want_aux: bool = False):
     """``gemm_linear`` on per-tensor scaled operands."""
     M, N = A.rows, W.rows
-    out, aux, args, dst = _linear_args(M, N, bias, act, residual, out, aux, want_aux, A.q.device)
-    assert A.k == W.k
+    out, aux, args, dst = _linear_args(A, W, (A.scale, W.scale), bias, act, residual, out, aux, want_aux)
     oa, ob = A.operand(), W.operand()
     _check(lib().fp8_tensor_gemm_linear(M, N, A.k, ctypes.byref(oa), ctypes.byref(ob), *args, *dst, _stream()),
            "fp8_tensor_gemm_linear")
@@ -295,8 +300,8 @@ class GradList:
         # whatever becomes of the tensors
         self._storages = [t.untyped_storage() for t in self.grads + self.out + [self.norm, self.workspace]]
         self._apart = self._outputs_apart()
+        self._on_gpu = device.type == "cuda"  # all are on the device of the first
         self._tail = (self.norm.data_ptr(), self.workspace.data_ptr(), self.workspace.numel() * 4)
-
 
     def _outputs_apart(self) -> bool:
         # every place that clipping writes is apart from every other tensor of the
@@ -321,6 +326,7 @@ def grad_norm(grads) -> torch.Tensor:
     """The L2 norm over all elements of all tensors (a ``GradList`` or a
     sequence of tensors), as a 1-element fp32 device tensor."""
     g = grads if isinstance(grads, GradList) else GradList(grads)
+    assert g._on_gpu, "grad_norm: the tensors are not on the GPU"
     _check(lib().fp8_grad_norm(len(g.grads), g.table, *g._tail, _stream()), "fp8_grad_norm")
     return g.norm
 
@@ -331,5 +337,6 @@ def clip_grads(grads, max_norm: float) -> torch.Tensor:
     overlap another that is written to: a shared one is listed once."""
     g = grads if isinstance(grads, GradList) else GradList(grads)
     assert g._apart, "clip_grads: a tensor of the list overlaps another"
+    assert g._on_gpu, "clip_grads: the tensors are not on the GPU"
     _check(lib().fp8_clip_grads(len(g.grads), g.table, float(max_norm), *g._tail, _stream()), "fp8_clip_grads")
     return g.norm
