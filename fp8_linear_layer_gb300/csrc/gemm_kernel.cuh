@@ -52,6 +52,7 @@
 #include "common.cuh"
 #include "internal.h"
 #include "launch.cuh"
+#include "per_device.h"
 #include "ptx.cuh"
 #include "split_k.cuh"
 
@@ -1289,21 +1290,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 // prepares the kernel on the current device, on first use; 0 or a negative error
 template <int EPI, int SPLIT>
 int configure_gemm(int* device) {
-    auto kern = gemm_fp8_kernel<EPI, SPLIT>;
-    static unsigned long long configured = 0;  // one bit per device ordinal
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return -3;
-    if (!(configured & (1ull << dev))) {
+    static PerDevice configured;
+    if (cudaGetDevice(device) != cudaSuccess) return -3;
+    return configured.get(*device, [] {
+        auto kern = gemm_fp8_kernel<EPI, SPLIT>;
         // the register split above assumes exactly kLaunchRegs per thread at launch
         cudaFuncAttributes attr;
         if (cudaFuncGetAttributes(&attr, kern) != cudaSuccess || attr.numRegs != kLaunchRegs) return -3;
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(smem_bytes<EPI, SPLIT>())) != cudaSuccess)
-            return -3;
-        configured |= 1ull << dev;
-    }
-    *device = dev;
-    return 0;
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    static_cast<int>(smem_bytes<EPI, SPLIT>())) == cudaSuccess
+                   ? 0
+                   : -3;
+    });
 }
 
 template <int EPI>

@@ -406,15 +406,8 @@ __global__ void __launch_bounds__(kRowsThreads, rows_ctas_per_sm<NT>())
 template <int RECIPE, int NT>
 int launch_rows_impl(const RowsMaps& maps, const RowsParams& p, cudaStream_t stream) {
     auto kern = gemm_rows_kernel<RECIPE, NT>;
-    static unsigned long long configured = 0;  // one bit per device ordinal
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return -3;
-    if (!(configured & (1ull << dev))) {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(rows_smem_bytes<NT>())) != cudaSuccess)
-            return -3;
-        configured |= 1ull << dev;
-    }
+    static PerDevice allowed;
+    if (allow_shared_memory(allowed, kern, rows_smem_bytes<NT>()) != 0) return -3;
     const int64_t tiles = (static_cast<int64_t>(p.N) + kRowsFeatures - 1) / kRowsFeatures;
     const dim3 grid(static_cast<unsigned>(tiles * p.cluster), static_cast<unsigned>((p.M + NT - 1) / NT));
     return launch_dependent_clusters(kern, grid, static_cast<unsigned>(p.cluster), kRowsThreads, rows_smem_bytes<NT>(),

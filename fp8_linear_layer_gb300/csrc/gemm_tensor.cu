@@ -23,6 +23,7 @@
 //               accumulator (16x256b fragments), hands the buffer back to the
 //               leader and stores through the epilogues of the 1x128 kernel.
 #include "gemm_kernel.cuh"
+#include "per_device.h"
 #include "split_k.cuh"
 
 namespace fp8ll {
@@ -322,12 +323,11 @@ __global__ void __cluster_dims__(2 * SPLIT, 1, 1) __launch_bounds__(kThreads, 1)
 // first use; negative on failure
 template <int EPI, int SPLIT>
 int launch_tensor_impl_slots() {
-    auto kern = gemm_tensor_kernel<EPI, SPLIT>;
-    static unsigned long long configured = 0;
-    static int clusters_on[64] = {0};
+    static PerDevice clusters;
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return -3;
-    if (!(configured & (1ull << dev))) {
+    if (cudaGetDevice(&dev) != cudaSuccess) return -3;
+    return clusters.get(dev, [dev] {
+        auto kern = gemm_tensor_kernel<EPI, SPLIT>;
         cudaFuncAttributes attr;
         if (cudaFuncGetAttributes(&attr, kern) != cudaSuccess || attr.numRegs != kLaunchRegs) return -3;
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -338,16 +338,13 @@ int launch_tensor_impl_slots() {
         cfg.blockDim = dim3(kThreads, 1, 1);
         cfg.dynamicSmemBytes = kTpSmemBytes<EPI>;
         int n = 0;
-        if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
-            cudaGetLastError();
-            int sms = 0;
-            if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return -3;
-            n = sms / (2 * SPLIT);
-        }
-        clusters_on[dev] = n;
-        configured |= 1ull << dev;
-    }
-    return clusters_on[dev];
+        if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) == cudaSuccess && n >= 1) return n;
+        cudaGetLastError();
+        if (SPLIT > 1) return 0;  // not known to run at once: K is not split
+        int sms = 0;
+        if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return -3;
+        return sms / 2;
+    });
 }
 
 template <int EPI, int SPLIT = 1>

@@ -14,7 +14,23 @@
 #pragma once
 #include <cuda_runtime.h>
 
+#include "per_device.h"
+
 namespace fp8ll {
+
+// lets the kernel have `bytes` of dynamic shared memory on the current device, on
+// first use (`allowed`: the kernel's own); 0 or a negative error
+template <typename Kernel>
+int allow_shared_memory(PerDevice& allowed, Kernel* kern, size_t bytes) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return -3;
+    return allowed.get(dev, [kern, bytes] {
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) ==
+                       cudaSuccess
+                   ? 0
+                   : -3;
+    });
+}
 
 __device__ __forceinline__ void release_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void await_dependency() { asm volatile("griddepcontrol.wait;" ::: "memory"); }

@@ -19,6 +19,7 @@
 #include "cast_rule.cuh"
 #include "common.cuh"
 #include "internal.h"
+#include "launch.cuh"
 #include "mx_rule.cuh"
 #include "ptx.cuh"
 
@@ -417,15 +418,8 @@ int launch_cols(const uint16_t* x, int64_t rows, int64_t cols, int64_t ldx, uint
         return cudaGetLastError() == cudaSuccess ? 0 : -3;
     } else {
         auto kern = quantize_cols_pipe_kernel<FMT, DBIAS>;
-        static unsigned long long configured = 0;  // one bit per device ordinal
-        int dev = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return -3;
-        if (!(configured & (1ull << dev))) {
-            if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kPipeSmem)) !=
-                cudaSuccess)
-                return -3;
-            configured |= 1ull << dev;
-        }
+        static PerDevice allowed;
+        if (allow_shared_memory(allowed, kern, kPipeSmem) != 0) return -3;
         const int64_t ntiles = (rows / 128) * ((cols + 127) / 128);
         if (ntiles == 0) return 0;
         const int64_t cap = static_cast<int64_t>(num_sms) * kPipeCtas;

@@ -381,15 +381,8 @@ __global__ void __launch_bounds__(256, kColsCtas) rmsnorm_cols_kernel(const __gr
 template <int FMT, int RECIPE>
 int launch_cols(const RmsNormParams& p, cudaStream_t stream, int num_sms) {
     auto kern = rmsnorm_cols_kernel<FMT, RECIPE>;
-    static unsigned long long configured = 0;  // one bit per device ordinal
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return -3;
-    if (!(configured & (1ull << dev))) {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * sizeof(ColsStage)) !=
-            cudaSuccess)
-            return -3;
-        configured |= 1ull << dev;
-    }
+    static PerDevice allowed;
+    if (allow_shared_memory(allowed, kern, 2 * sizeof(ColsStage)) != 0) return -3;
     const int64_t tiles = p.rows / 128 * (p.cols / 128), cap = static_cast<int64_t>(num_sms) * kColsCtas;
     return launch_dependent(kern, static_cast<unsigned>(tiles < cap ? tiles : cap), 256, 2 * sizeof(ColsStage), stream,
                             p) == cudaSuccess
@@ -618,15 +611,8 @@ int launch_grad(const RmsNormGradParams& p, int T, int num_sms, int resident, cu
     constexpr int rows_per_cta = LANES ? 256 / (LANES ? LANES : 1) : 1;
     const size_t smem = SMEM || LANES ? static_cast<size_t>(p.cols) * 4 * rows_per_cta : 0;
     if (SMEM) {
-        static unsigned long long configured = 0;  // one bit per device ordinal
-        int dev = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return -3;
-        if (!(configured & (1ull << dev))) {
-            if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     static_cast<int>(kNormMaxCols * 4)) != cudaSuccess)
-                return -3;
-            configured |= 1ull << dev;
-        }
+        static PerDevice allowed;
+        if (allow_shared_memory(allowed, kern, kNormMaxCols * 4) != 0) return -3;
     }
     int64_t cap = static_cast<int64_t>(num_sms) * (resident < 1 ? 1 : resident);
     if (cap > kGradMaxBands) cap = kGradMaxBands;
