@@ -41,7 +41,7 @@ bool valid_norm(const RmsNormParams& p, int fmt) {
     if (!p.gamma || !aligned(p.gamma, 16) || !p.rstd || !aligned(p.rstd, 4)) return false;
     if (!aligned(p.h, 16) || !aligned(p.y, 16) || !aligned(p.qr, 16) || !aligned(p.qc, 16)) return false;
     if (!p.y && !p.qr && !p.qc) return false;
-    if (p.qc && (p.rows % 128 != 0 || p.rows / 128 > 65535)) return false;
+    if (p.qc && p.rows % 128 != 0) return false;
     return true;
 }
 

@@ -463,7 +463,7 @@ int fp8_tensor_gemm_linear(int64_t M, int64_t N, int64_t K, const fp8ll_tensor_o
  *   q_rows: codes [rows][cols], scales as fp8_quantize / fp8_mx_quantize
  *           (transpose = 0) / fp8_tensor_quantize lay them out.
  *   q_cols: the transposed codes [cols][rows], blocked down the rows (transpose
- *           = 1), for the weight gradient; rows % 128 == 0, rows / 128 <= 65535.
+ *           = 1), for the weight gradient; rows % 128 == 0.
  * The per-tensor form casts with *amax_in, writes *scale and, if amax_out is
  * not NULL, max|y| (for the history of the next step).
  * No output may overlap another or an input, but for h as above.
