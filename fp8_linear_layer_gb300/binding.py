@@ -176,8 +176,8 @@ class Fp8Tensor:
         return self.q.shape[1]
 
     def operand(self) -> OperandStruct:
-        return OperandStruct(self.q.data_ptr(), self.scale.data_ptr(), self.q.stride(0),
-                             self.scale.stride(0), int(self.fmt), 0)
+        return OperandStruct(self.q.data_ptr(), self.scale.data_ptr(), self.q.stride()[0],
+                             self.scale.stride()[0], int(self.fmt), 0)
 
 
 def empty_fp8(rows: int, k: int, fmt: int, device="cuda") -> Fp8Tensor:
@@ -377,7 +377,7 @@ class Fp8MxTensor:
         return self.q.shape[1]
 
     def operand(self) -> MxOperandStruct:
-        return MxOperandStruct(self.q.data_ptr(), self.sf.data_ptr(), self.q.stride(0), int(self.fmt), 0)
+        return MxOperandStruct(self.q.data_ptr(), self.sf.data_ptr(), self.q.stride()[0], int(self.fmt), 0)
 
 
 def mx_sf_bytes(rows: int, k: int) -> int:
@@ -488,7 +488,7 @@ class Fp8TensorScaled:
         return self.q.shape[1]
 
     def operand(self) -> TensorOperandStruct:
-        return TensorOperandStruct(self.q.data_ptr(), self.scale.data_ptr(), self.q.stride(0), int(self.fmt), 0)
+        return TensorOperandStruct(self.q.data_ptr(), self.scale.data_ptr(), self.q.stride()[0], int(self.fmt), 0)
 
 
 def empty_tensor_scaled(rows: int, k: int, fmt: int, device="cuda") -> Fp8TensorScaled:

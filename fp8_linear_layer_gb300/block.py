@@ -15,14 +15,15 @@ from . import binding as B
 from .binding import (ACC_FULL, ACT_GELU, ACT_NONE, Fp8MxTensor, Fp8Tensor, Fp8TensorScaled, _check, empty_fp8,
                       empty_mx, lib)
 
-_bf16, _f32 = torch.bfloat16, torch.float32
+_bf16, _f32, _u8 = torch.bfloat16, torch.float32, torch.uint8
+_C = torch._C
 
 
 def _stream() -> int:
     """torch's current stream as the address that the library takes (the same
     stream as ``torch.cuda.current_stream()``, without building its object: a
     call of few tokens is bound by what the host does)."""
-    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return _C._cuda_getCurrentRawStream(_C._cuda_getDevice())
 
 
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
@@ -97,8 +98,7 @@ def _packed(t, dtype, shape):
     return t.data_ptr()
 
 
-def _norm_args(x, gamma, eps, fmt, residual, out):
-    shape = x.shape
+def _norm_args(x, shape, gamma, eps, fmt, residual, out):
     rows, cols = shape
     ldx, ldr = _rows(x, shape), 0
     if residual is not None:
@@ -114,7 +114,7 @@ def _norm_outs(shape, out):
 
 def _codes(t, fmt, rows, cols):
     assert t.fmt == fmt
-    return _packed(t.q, torch.uint8, (rows, cols))
+    return _packed(t.q, _u8, (rows, cols))
 
 
 def rmsnorm_quantize(x: torch.Tensor, gamma: torch.Tensor, eps: float, fmt: int,
@@ -124,17 +124,18 @@ def rmsnorm_quantize(x: torch.Tensor, gamma: torch.Tensor, eps: float, fmt: int,
     fp32 with one scale per 128 elements: row codes for the forward product
     (``rows``), transposed codes for the weight gradient (``cols``), bf16
     (``y``).  With ``out`` its buffers are used, and say which forms are made."""
+    shape = x.shape
+    m, k = shape
     if out is None:
-        out = empty_rmsnorm(x.shape[0], x.shape[1], fmt, rows, cols, residual is not None, y, x.device)
-    args = _norm_args(x, gamma, eps, fmt, residual, out)
-    m, k = x.shape
+        out = empty_rmsnorm(m, k, fmt, rows, cols, residual is not None, y, x.device)
+    args = _norm_args(x, shape, gamma, eps, fmt, residual, out)
     qr = sr = qc = sc = None
     ldr = ldc = 0
     if out.rows is not None:
-        qr, sr, ldr = _codes(out.rows, fmt, m, k), _ptr(out.rows.scale), out.rows.scale.stride(0)
+        qr, sr, ldr = _codes(out.rows, fmt, m, k), _ptr(out.rows.scale), out.rows.scale.stride()[0]
     if out.cols is not None:
-        qc, sc, ldc = _codes(out.cols, fmt, k, m), _ptr(out.cols.scale), out.cols.scale.stride(0)
-    _check(lib().fp8_rmsnorm_quantize(*args, *_norm_outs(x.shape, out), qr, sr, ldr, qc, sc, ldc, _stream()),
+        qc, sc, ldc = _codes(out.cols, fmt, k, m), _ptr(out.cols.scale), out.cols.scale.stride()[0]
+    _check(lib().fp8_rmsnorm_quantize(*args, *_norm_outs(shape, out), qr, sr, ldr, qc, sc, ldc, _stream()),
            "fp8_rmsnorm_quantize")
     return out
 
@@ -143,16 +144,17 @@ def mx_rmsnorm_quantize(x: torch.Tensor, gamma: torch.Tensor, eps: float, fmt: i
                         residual: Optional[torch.Tensor] = None, out: Optional[RmsNorm] = None, rows: bool = True,
                         cols: bool = False, y: bool = False) -> RmsNorm:
     """``rmsnorm_quantize`` with MXFP8 operands (one power-of-two scale per 32 elements)."""
+    shape = x.shape
+    m, k = shape
     if out is None:
-        out = empty_mx_rmsnorm(x.shape[0], x.shape[1], fmt, rows, cols, residual is not None, y, x.device)
-    args = _norm_args(x, gamma, eps, fmt, residual, out)
-    m, k = x.shape
+        out = empty_mx_rmsnorm(m, k, fmt, rows, cols, residual is not None, y, x.device)
+    args = _norm_args(x, shape, gamma, eps, fmt, residual, out)
     qr = sr = qc = sc = None
     if out.rows is not None:
         qr, sr = _codes(out.rows, fmt, m, k), _ptr(out.rows.sf)
     if out.cols is not None:
         qc, sc = _codes(out.cols, fmt, k, m), _ptr(out.cols.sf)
-    _check(lib().fp8_mx_rmsnorm_quantize(*args, *_norm_outs(x.shape, out), qr, sr, qc, sc, _stream()),
+    _check(lib().fp8_mx_rmsnorm_quantize(*args, *_norm_outs(shape, out), qr, sr, qc, sc, _stream()),
            "fp8_mx_rmsnorm_quantize")
     return out
 
@@ -163,11 +165,12 @@ def tensor_rmsnorm_quantize(x: torch.Tensor, gamma: torch.Tensor, eps: float, fm
     """``rmsnorm_quantize`` with one scale for the tensor, made of ``amax_in``
     (a 1-element device tensor: the largest amax of earlier steps); ``amax``
     of the result receives this call's max|y|."""
+    shape = x.shape
+    m, k = shape
     if out is None:
-        out = empty_tensor_rmsnorm(x.shape[0], x.shape[1], fmt, rows, cols, residual is not None, y, x.device)
-    args = _norm_args(x, gamma, eps, fmt, residual, out)
+        out = empty_tensor_rmsnorm(m, k, fmt, rows, cols, residual is not None, y, x.device)
+    args = _norm_args(x, shape, gamma, eps, fmt, residual, out)
     assert amax_in.dtype is _f32 and amax_in.numel() == 1 and amax_in.is_cuda
-    m, k = x.shape
     qr = qc = scale = spare = None
     if out.rows is not None:
         qr, scale = _codes(out.rows, fmt, m, k), _ptr(out.rows.scale)
@@ -178,7 +181,7 @@ def tensor_rmsnorm_quantize(x: torch.Tensor, gamma: torch.Tensor, eps: float, fm
     if scale is None:  # only the bf16 form was asked for
         spare = torch.empty((1,), dtype=_f32, device=x.device)
         scale = spare.data_ptr()
-    _check(lib().fp8_tensor_rmsnorm_quantize(*args, amax_in.data_ptr(), *_norm_outs(x.shape, out), qr, qc, scale,
+    _check(lib().fp8_tensor_rmsnorm_quantize(*args, amax_in.data_ptr(), *_norm_outs(shape, out), qr, qc, scale,
                                              _ptr(out.amax), _stream()), "fp8_tensor_rmsnorm_quantize")
     return out
 
@@ -211,7 +214,7 @@ def rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, gamma: torch.Tensor, rst
     _check(lib().fp8_rmsnorm_backward(dy.data_ptr(), h.data_ptr(), _packed(gamma, _bf16, (cols,)),
                                       _packed(rstd, _f32, (rows,)), _ptr(r), rows, cols, ldd, ldh, ldr,
                                       _packed(out, _bf16, shape), _packed(dgamma, _f32, (cols,)), int(accumulate),
-                                      workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream()),
+                                      workspace.data_ptr(), workspace.nbytes, _stream()),
            "fp8_rmsnorm_backward")
     return out, dgamma
 
@@ -219,16 +222,17 @@ def rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, gamma: torch.Tensor, rst
 # ----------------------------------------------------------------- product ----
 
 def _linear_args(A, W, scales, bias, act, residual, out, aux, want_aux):
-    M, N, device = A.rows, W.rows, A.q.device
-    assert A.k == W.k
+    """(Y, Z, the arguments in front of the operands, behind them, the outputs)"""
+    (M, K), (N, KW) = A.q.shape, W.q.shape
+    assert K == KW
     assert A.q.is_cuda and W.q.is_cuda and scales[0].is_cuda and scales[1].is_cuda
     if out is None:
-        out = torch.empty((M, N), dtype=_bf16, device=device)
+        out = torch.empty((M, N), dtype=_bf16, device=A.q.device)
     if aux is None and want_aux:
         assert act == ACT_GELU, "only an activation has a pre-activation to keep"
-        aux = torch.empty((M, N), dtype=_bf16, device=device)
+        aux = torch.empty((M, N), dtype=_bf16, device=A.q.device)
     shape = (M, N)
-    return (out, aux, (_packed(bias, _bf16, (N,)), act, _ptr(residual),
+    return (out, aux, (M, N, K), (_packed(bias, _bf16, (N,)), act, _ptr(residual),
                        0 if residual is None else _rows(residual, shape)),
             (_packed(out, _bf16, shape), _packed(aux, _bf16, shape)))
 
@@ -239,10 +243,9 @@ def gemm_linear(A: Fp8Tensor, W: Fp8Tensor, bias: Optional[torch.Tensor] = None,
     """Y (bf16 [M][N]) = act(A W^T + bias) + residual, rounded once; returns (Y,
     Z-or-None), Z = A W^T + bias with ``want_aux`` or ``aux`` (GELU only).
     ``out`` may be the residual itself.  Few rows run a kernel of their own."""
-    M, N = A.rows, W.rows
-    out, aux, args, dst = _linear_args(A, W, (A.scale, W.scale), bias, act, residual, out, aux, want_aux)
+    out, aux, sizes, args, dst = _linear_args(A, W, (A.scale, W.scale), bias, act, residual, out, aux, want_aux)
     oa, ob = A.operand(), W.operand()
-    _check(lib().fp8_gemm_linear(M, N, A.k, ctypes.byref(oa), ctypes.byref(ob), *args, int(acc), *dst, _stream()),
+    _check(lib().fp8_gemm_linear(*sizes, ctypes.byref(oa), ctypes.byref(ob), *args, int(acc), *dst, _stream()),
            "fp8_gemm_linear")
     return out, aux
 
@@ -251,10 +254,9 @@ def mx_gemm_linear(A: Fp8MxTensor, W: Fp8MxTensor, bias: Optional[torch.Tensor] 
                    residual: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
                    aux: Optional[torch.Tensor] = None, want_aux: bool = False):
     """``gemm_linear`` on MXFP8 operands."""
-    M, N = A.rows, W.rows
-    out, aux, args, dst = _linear_args(A, W, (A.sf, W.sf), bias, act, residual, out, aux, want_aux)
+    out, aux, sizes, args, dst = _linear_args(A, W, (A.sf, W.sf), bias, act, residual, out, aux, want_aux)
     oa, ob = A.operand(), W.operand()
-    _check(lib().fp8_mx_gemm_linear(M, N, A.k, ctypes.byref(oa), ctypes.byref(ob), *args, *dst, _stream()),
+    _check(lib().fp8_mx_gemm_linear(*sizes, ctypes.byref(oa), ctypes.byref(ob), *args, *dst, _stream()),
            "fp8_mx_gemm_linear")
     return out, aux
 
@@ -264,10 +266,9 @@ def tensor_gemm_linear(A: Fp8TensorScaled, W: Fp8TensorScaled, bias: Optional[to
                        out: Optional[torch.Tensor] = None, aux: Optional[torch.Tensor] = None,
                        want_aux: bool = False):
     """``gemm_linear`` on per-tensor scaled operands."""
-    M, N = A.rows, W.rows
-    out, aux, args, dst = _linear_args(A, W, (A.scale, W.scale), bias, act, residual, out, aux, want_aux)
+    out, aux, sizes, args, dst = _linear_args(A, W, (A.scale, W.scale), bias, act, residual, out, aux, want_aux)
     oa, ob = A.operand(), W.operand()
-    _check(lib().fp8_tensor_gemm_linear(M, N, A.k, ctypes.byref(oa), ctypes.byref(ob), *args, *dst, _stream()),
+    _check(lib().fp8_tensor_gemm_linear(*sizes, ctypes.byref(oa), ctypes.byref(ob), *args, *dst, _stream()),
            "fp8_tensor_gemm_linear")
     return out, aux
 
