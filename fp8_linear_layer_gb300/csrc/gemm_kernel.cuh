@@ -501,8 +501,8 @@ __device__ __forceinline__ void store_dgrad(const GemmParams& p, int row0, int c
 
 // linear: Z = acc + bias, Y = act(Z) + residual, in fp32, rounded once to bf16
 // (+ bf16 aux Z).  Three places for the residual, each a kernel of its own (one
-// kernel with all of them slowed the 1x128 promotion loop by a fifth, 502 ->
-// 589 us at 8192 x 4096 over 14336, through its register allocation):
+// kernel with all of them slowed the 1x128 promotion loop through its register
+// allocation: 589 us at 8192 x 4096 over 14336, 521 to 530 in the staged one):
 //   kResStaged  the tile was staged in shared memory by TMA (rrow as store_dgrad's
 //               zrow) and is read in the accumulator fragment's own order; rows
 //               of the output 16-byte aligned.

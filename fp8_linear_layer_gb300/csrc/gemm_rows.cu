@@ -5,13 +5,15 @@
 // Bound by one read of B.  The tile kernels give 256 features to one SM, which
 // leaves most SMs idle (56 of them work at N = 14336), and walk all of K there.
 // Here the weights are the 128-row side of the MMA and the tokens its N (16, 32
-// or 64 columns), so nothing of the tensor core's work is spent on rows that do
-// not exist, and K is split over a cluster of up to eight CTAs, which add their
-// fp32 sums through distributed shared memory in rank order (deterministic).
-// Two CTAs per SM keep 128 KB or more of B in flight there.  One token, 14336
-// features over 4096: 13.1 us one behind another on 1x128 operands, 0.68 of the
-// copy rate; what is left is the launch, the first loads' latency and the join
-// (4.2 us at 7168 x 2048 for 2.2 us of loads).  On the tile kernel 22.1 us, with
+// or 64 columns; 128 where more rows than 64 come here, a tile of them per grid
+// row), so little of the tensor core's work is spent on rows that do not exist,
+// and K is split over a cluster of up to eight CTAs, which add their fp32 sums
+// through distributed shared memory in rank order (deterministic).  Two CTAs per
+// SM keep 128 KB or more of B in flight there (at 128 tokens one, 80 KB).  One
+// token, 14336 features over 4096: 13.1 us one behind another on 1x128 operands,
+// 0.68 of the copy rate; what is left is the launch, the first loads' latency (they
+// are asked for only when the kernel before has completed) and the join (4.2 us at
+// 7168 x 2048 for 2.2 us of loads).  On the tile kernel 22.1 us, with
 // fp8 mma.sync fragments straight from global memory 17.1 (43 at 13 tokens on
 // MXFP8: those MMAs take 53 cycles each here).
 // Per CTA of 8 warps:

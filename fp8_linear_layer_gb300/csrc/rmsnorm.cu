@@ -17,7 +17,7 @@
 // the measured copy rate (48.9 without the loads ahead and with every lane's own
 // divisions).
 // Columns kernel: reads h again, while half of it is in L2, and casts it down its
-// columns: 18 us more at that size.  (A cluster of CTAs per 128-row band, which
+// columns: 20 us more at that size.  (A cluster of CTAs per 128-row band, which
 // formed h and then cast its tiles from L2, took 98 us for both: each CTA's chain
 // of loads was too long for the CTAs that fit.)
 #include <cuda_runtime.h>
@@ -401,6 +401,9 @@ template <int FMT, int RECIPE>
 int launch_norm(const RmsNormParams& p, cudaStream_t stream, int num_sms) {
     int T, V;
     row_shape(p.cols, T, V);
+    // 768 (1024) threads of rows per SM; from 4224 columns on the kernels' 118 to 121
+    // registers let only 512 run at once (at 7168 columns two CTAs of 224 threads, three
+    // launched): the rest start where the first ones end
     int64_t grid = RECIPE == kRecipeMx ? (p.rows + 255) / 256 * 256 : p.rows;
     const int64_t cap = static_cast<int64_t>(num_sms) * ((V == 1 ? 1024 : 768) / T < 1 ? 1 : (V == 1 ? 1024 : 768) / T);
     if (grid > cap) grid = cap;
@@ -603,10 +606,11 @@ __global__ void __launch_bounds__(1024) rmsnorm_grad_finalize_kernel(const float
     }
 }
 
-// T threads per CTA (a warp per row: 256), `resident` CTAs per SM at once: each
-// CTA leaves one band of partial sums
+// T threads per CTA (a warp per row: 256), up to `per_sm` CTAs per SM: each leaves
+// one band of partial sums.  (They run at once, but for up to 256 columns, where
+// registers let two of the four.)
 template <int V, int MAXT, bool SMEM, bool PRE, int LANES>
-int launch_grad(const RmsNormGradParams& p, int T, int num_sms, int resident, cudaStream_t stream) {
+int launch_grad(const RmsNormGradParams& p, int T, int num_sms, int per_sm, cudaStream_t stream) {
     auto kern = rmsnorm_grad_kernel<V, MAXT, SMEM, PRE, LANES>;
     constexpr int rows_per_cta = LANES ? 256 / (LANES ? LANES : 1) : 1;
     const size_t smem = SMEM || LANES ? static_cast<size_t>(p.cols) * 4 * rows_per_cta : 0;
@@ -614,7 +618,7 @@ int launch_grad(const RmsNormGradParams& p, int T, int num_sms, int resident, cu
         static PerDevice allowed;
         if (allow_shared_memory(allowed, kern, kNormMaxCols * 4) != 0) return -3;
     }
-    int64_t cap = static_cast<int64_t>(num_sms) * (resident < 1 ? 1 : resident);
+    int64_t cap = static_cast<int64_t>(num_sms) * (per_sm < 1 ? 1 : per_sm);
     if (cap > kGradMaxBands) cap = kGradMaxBands;
     const int64_t want = (p.rows + rows_per_cta - 1) / rows_per_cta;
     const int bands = static_cast<int>(want < cap ? want : cap);
