@@ -32,7 +32,9 @@ EXPORTS = ("fp8_scale_ld", "fp8_quantize", "fp8_quantize_dual", "fp8_cast_f32", 
            "fp8_bgrad_from_operand", "fp8_quantize_dbias", "fp8_mx_quantize_dbias", "fp8_gemm_linear",
            "fp8_mx_gemm_linear", "fp8_tensor_gemm_linear", "fp8_rmsnorm_quantize", "fp8_mx_rmsnorm_quantize",
            "fp8_tensor_rmsnorm_quantize", "fp8_rmsnorm_workspace_size", "fp8_rmsnorm_backward",
-           "fp8_grad_norm_workspace_size", "fp8_grad_norm", "fp8_clip_grads")
+           "fp8_grad_norm_workspace_size", "fp8_grad_norm", "fp8_clip_grads", "fp8_layernorm_quantize",
+           "fp8_mx_layernorm_quantize", "fp8_tensor_layernorm_quantize", "fp8_layernorm_workspace_size",
+           "fp8_layernorm_backward", "fp8_dropout")
 
 
 class Fp8Error(RuntimeError):
@@ -119,6 +121,15 @@ def lib():
         L.fp8_rmsnorm_workspace_size.argtypes = [i64, i64]
         L.fp8_rmsnorm_workspace_size.restype = sz
         L.fp8_rmsnorm_backward.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, vp, vp, i32, vp, sz, vp]
+        norm = [vp, vp, vp, vp, i64, i64, i64, i64, f32, i32]
+        L.fp8_layernorm_quantize.argtypes = norm + [vp, vp, vp, vp, vp, vp, i64, vp, vp, i64, vp]
+        L.fp8_mx_layernorm_quantize.argtypes = norm + [vp, vp, vp, vp, vp, vp, vp, vp, vp]
+        L.fp8_tensor_layernorm_quantize.argtypes = norm + [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+        L.fp8_layernorm_workspace_size.argtypes = [i64, i64]
+        L.fp8_layernorm_workspace_size.restype = sz
+        L.fp8_layernorm_backward.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, vp, vp, vp, i32, vp, sz, vp]
+        L.fp8_dropout.argtypes = [vp, vp, i64, i64, i64, i64, ctypes.c_double, ctypes.c_uint64, ctypes.c_uint32, i64, vp,
+                                  vp, vp]
         gp = ctypes.POINTER(GradStruct)
         L.fp8_grad_norm_workspace_size.argtypes = [i64]
         L.fp8_grad_norm_workspace_size.restype = sz
@@ -132,7 +143,8 @@ def lib():
                      "fp8_grouped_wgrad", "fp8_bgrad_from_operand", "fp8_quantize_dbias", "fp8_mx_quantize_dbias",
                      "fp8_gemm_linear", "fp8_mx_gemm_linear", "fp8_tensor_gemm_linear", "fp8_rmsnorm_quantize",
                      "fp8_mx_rmsnorm_quantize", "fp8_tensor_rmsnorm_quantize", "fp8_rmsnorm_backward",
-                     "fp8_grad_norm", "fp8_clip_grads", "fp8_get_device_status",
+                     "fp8_grad_norm", "fp8_clip_grads", "fp8_layernorm_quantize", "fp8_mx_layernorm_quantize",
+                     "fp8_tensor_layernorm_quantize", "fp8_layernorm_backward", "fp8_dropout", "fp8_get_device_status",
                      "fp8_debug_starve_next_gemm"):
             getattr(L, name).restype = i32
         _lib = L

@@ -1,13 +1,14 @@
 """The operators of a pre-norm residual block around the FP8 linear layer:
-RMS norm with the residual's addition and an fp8 output, its backward pass, the
-matrix product with bias, activation and residual, and gradient clipping.
+RMS and layer norm with the residual's addition and an fp8 output, their backward
+passes, dropout on the way into the residual stream, the matrix product with bias,
+activation and residual, and gradient clipping.
 
 Argument marshalling only, as in ``binding``: every computation happens in the
 CUDA library, on torch's current stream.
 """
 import ctypes
 from dataclasses import dataclass
-from typing import Optional, Sequence
+from typing import Optional, Sequence, Union
 
 import torch
 
@@ -32,6 +33,14 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
         return None
     assert t.is_cuda
     return t.data_ptr()
+
+
+def _on_device(*tensors):
+    """The tensors (or none) are on torch's current device, whose stream the call uses."""
+    here = tensors[0].get_device()
+    assert here >= 0 and here == _C._cuda_getDevice(), "the tensors are not on the current GPU"
+    for t in tensors[1:]:
+        assert t is None or t.get_device() == here, "the tensors are on several devices"
 
 
 # -------------------------------------------------------------------- norm ----
@@ -217,6 +226,196 @@ def rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, gamma: torch.Tensor, rst
                                       workspace.data_ptr(), workspace.nbytes, _stream()),
            "fp8_rmsnorm_backward")
     return out, dgamma
+
+
+# -------------------------------------------------------------- layer norm ----
+
+@dataclass
+class LayerNorm(RmsNorm):
+    """What a layer norm leaves: as ``RmsNorm``, and ``mean`` [rows]."""
+    mean: Optional[torch.Tensor] = None
+
+
+def _with_mean(n: RmsNorm) -> LayerNorm:
+    return LayerNorm(n.h, n.rstd, n.rows, n.cols, n.y, n.amax, torch.empty_like(n.rstd))
+
+
+def empty_layernorm(rows: int, cols: int, fmt: int, rows_too: bool = True, cols_too: bool = False,
+                    residual: bool = False, y: bool = False, device="cuda") -> LayerNorm:
+    """Outputs of ``layernorm_quantize``, to be used call after call."""
+    return _with_mean(empty_rmsnorm(rows, cols, fmt, rows_too, cols_too, residual, y, device))
+
+
+def empty_mx_layernorm(rows: int, cols: int, fmt: int, rows_too: bool = True, cols_too: bool = False,
+                       residual: bool = False, y: bool = False, device="cuda") -> LayerNorm:
+    """Outputs of ``mx_layernorm_quantize``."""
+    return _with_mean(empty_mx_rmsnorm(rows, cols, fmt, rows_too, cols_too, residual, y, device))
+
+
+def empty_tensor_layernorm(rows: int, cols: int, fmt: int, rows_too: bool = True, cols_too: bool = False,
+                           residual: bool = False, y: bool = False, device="cuda") -> LayerNorm:
+    """Outputs of ``tensor_layernorm_quantize``: both orientations share one scale."""
+    return _with_mean(empty_tensor_rmsnorm(rows, cols, fmt, rows_too, cols_too, residual, y, device))
+
+
+def _layernorm_args(x, shape, gamma, beta, eps, fmt, residual, out):
+    _on_device(x, gamma, beta, residual, out.h, out.mean, out.rstd, out.y)
+    a = _norm_args(x, shape, gamma, eps, fmt, residual, out)
+    return a[:3] + (_packed(beta, _bf16, (shape[1],)),) + a[3:]
+
+
+def _layernorm_outs(shape, out):
+    h, rstd, y = _norm_outs(shape, out)
+    return h, _packed(out.mean, _f32, (shape[0],)), rstd, y
+
+
+def _block_codes(t, fmt, shape):
+    """(codes, scales, the scales' leading dimension) of an operand that a cast writes, or of none."""
+    if t is None:
+        return None, None, 0
+    _on_device(t.q, t.scale)
+    ld, one = t.scale.stride()
+    assert t.scale.dtype is _f32 and one == 1 and t.scale.shape[0] == shape[1] // 128 and t.scale.shape[1] >= shape[0]
+    return _codes(t, fmt, *shape), t.scale.data_ptr(), ld
+
+
+def _mx_codes(t, fmt, shape):
+    if t is None:
+        return None, None
+    _on_device(t.q, t.sf)
+    assert t.sf.dtype is _u8 and t.sf.is_contiguous() and t.sf.numel() >= B.mx_sf_bytes(*shape)
+    return _codes(t, fmt, *shape), t.sf.data_ptr()
+
+
+def layernorm_quantize(x: torch.Tensor, gamma: torch.Tensor, beta: Optional[torch.Tensor], eps: float, fmt: int,
+                       residual: Optional[torch.Tensor] = None, out: Optional[LayerNorm] = None, rows: bool = True,
+                       cols: bool = False, y: bool = False) -> LayerNorm:
+    """h = x + residual (bf16), then its layer norm y = (h - mean) rstd gamma + beta
+    cast from fp32, as ``rmsnorm_quantize`` casts its output."""
+    shape = x.shape
+    m, k = shape
+    if out is None:
+        out = empty_layernorm(m, k, fmt, rows, cols, residual is not None, y, x.device)
+    _check(lib().fp8_layernorm_quantize(*_layernorm_args(x, shape, gamma, beta, eps, fmt, residual, out),
+                                        *_layernorm_outs(shape, out), *_block_codes(out.rows, fmt, (m, k)),
+                                        *_block_codes(out.cols, fmt, (k, m)), _stream()), "fp8_layernorm_quantize")
+    return out
+
+
+def mx_layernorm_quantize(x: torch.Tensor, gamma: torch.Tensor, beta: Optional[torch.Tensor], eps: float, fmt: int,
+                          residual: Optional[torch.Tensor] = None, out: Optional[LayerNorm] = None, rows: bool = True,
+                          cols: bool = False, y: bool = False) -> LayerNorm:
+    """``layernorm_quantize`` with MXFP8 operands (one power-of-two scale per 32 elements)."""
+    shape = x.shape
+    m, k = shape
+    if out is None:
+        out = empty_mx_layernorm(m, k, fmt, rows, cols, residual is not None, y, x.device)
+    _check(lib().fp8_mx_layernorm_quantize(*_layernorm_args(x, shape, gamma, beta, eps, fmt, residual, out),
+                                           *_layernorm_outs(shape, out), *_mx_codes(out.rows, fmt, (m, k)),
+                                           *_mx_codes(out.cols, fmt, (k, m)), _stream()),
+           "fp8_mx_layernorm_quantize")
+    return out
+
+
+def tensor_layernorm_quantize(x: torch.Tensor, gamma: torch.Tensor, beta: Optional[torch.Tensor], eps: float, fmt: int,
+                              amax_in: torch.Tensor, residual: Optional[torch.Tensor] = None,
+                              out: Optional[LayerNorm] = None, rows: bool = True, cols: bool = False,
+                              y: bool = False) -> LayerNorm:
+    """``layernorm_quantize`` with one scale for the tensor, made of ``amax_in`` (a
+    1-element device tensor: the largest amax of earlier steps); ``amax`` of the
+    result receives this call's max|y|."""
+    shape = x.shape
+    m, k = shape
+    if out is None:
+        out = empty_tensor_layernorm(m, k, fmt, rows, cols, residual is not None, y, x.device)
+    args = _layernorm_args(x, shape, gamma, beta, eps, fmt, residual, out)
+    qr = qc = scale = None
+    for t in (out.rows, out.cols):
+        if t is None:
+            continue
+        assert scale is None or scale.data_ptr() == t.scale.data_ptr(), "both orientations share one scale"
+        scale = t.scale
+        _on_device(t.q, scale)
+    if out.rows is not None:
+        qr = _codes(out.rows, fmt, m, k)
+    if out.cols is not None:
+        qc = _codes(out.cols, fmt, k, m)
+    if scale is None:  # only the bf16 form was asked for
+        scale = torch.empty((1,), dtype=_f32, device=x.device)
+    _on_device(x, amax_in, out.amax)
+    assert amax_in.dtype is _f32 and amax_in.numel() == 1 and scale.dtype is _f32 and scale.numel() == 1
+    _check(lib().fp8_tensor_layernorm_quantize(*args, amax_in.data_ptr(), *_layernorm_outs(shape, out), qr, qc,
+                                               scale.data_ptr(), _packed(out.amax, _f32, (1,)), _stream()),
+           "fp8_tensor_layernorm_quantize")
+    return out
+
+
+def layernorm_workspace(rows: int, cols: int, device="cuda") -> torch.Tensor:
+    """Workspace of ``layernorm_backward``."""
+    return torch.empty((int(lib().fp8_layernorm_workspace_size(int(rows), int(cols))) // 4,), dtype=torch.float32,
+                       device=device)
+
+
+def layernorm_backward(dy: torch.Tensor, h: torch.Tensor, gamma: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
+                       residual_grad: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                       dgamma: Optional[torch.Tensor] = None, dbeta: Optional[torch.Tensor] = None, bias: bool = True,
+                       accumulate: bool = False, workspace: Optional[torch.Tensor] = None):
+    """(dx, dgamma, dbeta) of y = (h - mean) rstd gamma + beta: dx (bf16) is the
+    gradient of h, with the gradient that reaches h around the norm
+    (``residual_grad``) added; dgamma and dbeta (fp32) are written, or added to
+    with ``accumulate``.  Without ``bias`` the norm has no beta, and dbeta is None."""
+    shape = h.shape
+    rows, cols = shape
+    r = residual_grad
+    assert bias or dbeta is None, "a norm without bias has no dbeta"
+    assert not accumulate or (dgamma is not None and (dbeta is not None or not bias)), "accumulate needs dgamma and dbeta"
+    if out is None:
+        out = torch.empty((rows, cols), dtype=_bf16, device=h.device)
+    if dgamma is None:
+        dgamma = torch.empty((cols,), dtype=_f32, device=h.device)
+    if dbeta is None and bias:
+        dbeta = torch.empty((cols,), dtype=_f32, device=h.device)
+    if workspace is None:
+        workspace = layernorm_workspace(rows, cols, h.device)
+    assert workspace.is_contiguous()
+    _on_device(h, dy, gamma, mean, rstd, r, out, dgamma, dbeta, workspace)
+    ldd, ldh, ldr = _rows(dy, shape), _rows(h, shape), 0 if r is None else _rows(r, shape)
+    _check(lib().fp8_layernorm_backward(dy.data_ptr(), h.data_ptr(), _packed(gamma, _bf16, (cols,)),
+                                        _packed(mean, _f32, (rows,)), _packed(rstd, _f32, (rows,)),
+                                        None if r is None else r.data_ptr(), rows, cols, ldd, ldh, ldr,
+                                        _packed(out, _bf16, shape), _packed(dgamma, _f32, (cols,)),
+                                        _packed(dbeta, _f32, (cols,)), int(accumulate), workspace.data_ptr(),
+                                        workspace.nbytes, _stream()), "fp8_layernorm_backward")
+    return out, dgamma, dbeta
+
+
+# ----------------------------------------------------------------- dropout ----
+
+def dropout(x: torch.Tensor, p: float, seed: int, site: int = 0, step: Union[int, torch.Tensor] = 0,
+            residual: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """residual + dropout(x) (bf16 [rows][cols]): an element of x is dropped with
+    probability p, else scaled by 1 / (1 - p).  The mask is a function of the
+    element's place in the matrix, of ``seed`` (of a run, 64 bits), ``site``
+    (which dropout of the model, 32 bits) and ``step`` (64 bits; an int, or a
+    1-element int64 device tensor that a captured step counts up), and is never
+    stored: the gradient of x is this call on the output's gradient, with the same
+    numbers and no residual.  ``out`` may be x or the residual itself."""
+    shape = x.shape
+    ldx, ldr = _rows(x, shape), 0 if residual is None else _rows(residual, shape)
+    assert 0 <= seed < 1 << 64 and 0 <= site < 1 << 32
+    if out is None:
+        out = torch.empty(tuple(shape), dtype=_bf16, device=x.device)
+    counter = None
+    if isinstance(step, torch.Tensor):
+        assert step.dtype is torch.int64 and step.numel() == 1
+        counter, step = step, 0
+    else:
+        assert -(1 << 63) <= step < 1 << 63
+    _on_device(x, residual, out, counter)
+    _check(lib().fp8_dropout(x.data_ptr(), None if residual is None else residual.data_ptr(), shape[0], shape[1], ldx,
+                             ldr, p, seed, site, step, None if counter is None else counter.data_ptr(),
+                             _packed(out, _bf16, shape), _stream()), "fp8_dropout")
+    return out
 
 
 # ----------------------------------------------------------------- product ----

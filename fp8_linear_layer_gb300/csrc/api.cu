@@ -12,7 +12,7 @@
 #include "fp8ll.h"
 #include "gemm_rows.h"
 #include "internal.h"
-#include "rmsnorm.h"
+#include "norm.h"
 
 namespace fp8ll {
 

@@ -1,13 +1,14 @@
-// api_block.cu -- C ABI of the norm, its backward pass and gradient clipping:
-// host-side validation and launches.  No allocation, no synchronization.
+// api_block.cu -- C ABI of the norms, their backward passes, dropout and gradient
+// clipping: host-side validation and launches.  No allocation, no synchronization.
 #include <cmath>
 #include <cstdint>
 #include <initializer_list>
 
+#include "dropout.h"
 #include "fp8ll.h"
 #include "grad_clip.h"
 #include "internal.h"
-#include "rmsnorm.h"
+#include "norm.h"
 
 using namespace fp8ll;
 
@@ -30,9 +31,12 @@ bool share(const Range& a, const Range& b) {
 // rows of ld elements whose extent, in bytes of up to 4 an element, stays within 64 bits
 bool spans(int64_t rows, int64_t ld) { return ld < (1LL << 36) && (rows < 2 || ld <= (1LL << 60) / rows); }
 
-bool valid_norm(const RmsNormParams& p, int fmt) {
+// center: the layer norm's, with mean and beta
+bool valid_norm(const NormParams& p, bool center, int fmt) {
     if (fmt != FP8LL_E4M3 && fmt != FP8LL_E5M2) return false;
-    if (p.cols % 128 != 0 || p.cols > kNormMaxCols || p.rows > (1LL << 31) - 1) return false;
+    if (p.cols % 128 != 0 || p.cols > (center ? kLayerNormMaxCols : kNormMaxCols) || p.rows > (1LL << 31) - 1)
+        return false;
+    if (center && (!p.mean || !aligned(p.mean, 4) || !aligned(p.beta, 16))) return false;
     if (!(p.eps >= 0.0f) || std::isinf(p.eps)) return false;
     if (!p.x || !aligned(p.x, 16) || p.ldx < p.cols || p.ldx % 8 != 0 || !spans(p.rows, p.ldx)) return false;
     if (p.residual && (!aligned(p.residual, 16) || p.ldr < p.cols || p.ldr % 8 != 0 || !spans(p.rows, p.ldr)))
@@ -47,35 +51,38 @@ bool valid_norm(const RmsNormParams& p, int fmt) {
 
 // every output apart from every other and from the inputs; h may take the
 // place of x or of the residual, element by element
-bool apart(const RmsNormParams& p, const Range* scales, int num_scales) {
+bool apart(const NormParams& p, const Range* scales, int num_scales) {
     const int64_t n = p.rows * p.cols;
-    const Range x{p.x, ((p.rows - 1) * p.ldx + p.cols) * 2}, g{p.gamma, p.cols * 2};
+    const Range x{p.x, ((p.rows - 1) * p.ldx + p.cols) * 2}, g{p.gamma, p.cols * 2}, b{p.beta, p.cols * 2};
     const Range r{p.residual, ((p.rows - 1) * p.ldr + p.cols) * 2};
-    Range out[12] = {{p.h, 2 * n}, {p.rstd, 4 * p.rows}, {p.y, 2 * n}, {p.qr, n}, {p.qc, n}};
-    int count = 5;
+    Range out[12] = {{p.h, 2 * n}, {p.rstd, 4 * p.rows}, {p.y, 2 * n}, {p.qr, n}, {p.qc, n}, {p.mean, 4 * p.rows}};
+    int count = 6;
     for (int i = 0; i < num_scales; ++i) out[count++] = scales[i];
     for (int i = 0; i < count; ++i) {
         const bool h_on_x = i == 0 && p.h == p.x && p.ldx == p.cols;
         const bool h_on_r = i == 0 && p.h == p.residual && p.ldr == p.cols;
-        if ((share(out[i], x) && !h_on_x) || (share(out[i], r) && !h_on_r) || share(out[i], g)) return false;
+        if ((share(out[i], x) && !h_on_x) || (share(out[i], r) && !h_on_r) || share(out[i], g) || share(out[i], b))
+            return false;
         for (int j = 0; j < i; ++j)
             if (share(out[i], out[j])) return false;
     }
     return true;
 }
 
-int launch(const RmsNormParams& p, int recipe, int fmt, fp8ll_stream_t stream) {
+int launch(const NormParams& p, bool center, int recipe, int fmt, fp8ll_stream_t stream) {
     int sms = 0;
     const int rc = current_device_sms(&sms);
     if (rc != FP8LL_OK) return rc;
-    return launch_rmsnorm(p, recipe, fmt, reinterpret_cast<cudaStream_t>(stream), sms) == 0 ? FP8LL_OK
-                                                                                           : FP8LL_ERR_LAUNCH;
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return (center ? launch_layernorm(p, recipe, fmt, s, sms) : launch_rmsnorm(p, recipe, fmt, s, sms)) == 0
+               ? FP8LL_OK
+               : FP8LL_ERR_LAUNCH;
 }
 
-RmsNormParams norm_params(const void* x, const void* residual, const void* gamma, int64_t rows, int64_t cols,
+NormParams norm_params(const void* x, const void* residual, const void* gamma, int64_t rows, int64_t cols,
                           int64_t ldx, int64_t ldr, float eps, void* h, float* rstd, void* y, uint8_t* q_rows,
                           uint8_t* q_cols) {
-    RmsNormParams p = {};
+    NormParams p = {};
     p.x = static_cast<const uint16_t*>(x);
     p.residual = static_cast<const uint16_t*>(residual);
     p.gamma = static_cast<const uint16_t*>(gamma);
@@ -92,68 +99,52 @@ RmsNormParams norm_params(const void* x, const void* residual, const void* gamma
     return p;
 }
 
-}  // namespace
-
-extern "C" {
-
-int fp8_rmsnorm_quantize(const void* x_bf16, const void* residual_bf16, const void* gamma_bf16, int64_t rows,
-                         int64_t cols, int64_t ldx, int64_t ldr, float eps, int fmt, void* h_bf16, float* rstd,
-                         void* y_bf16, uint8_t* q_rows, float* scale_rows, int64_t scale_ld_rows, uint8_t* q_cols,
-                         float* scale_cols, int64_t scale_ld_cols, fp8ll_stream_t stream) {
-    if (rows < 0 || cols < 0 || (fmt != FP8LL_E4M3 && fmt != FP8LL_E5M2)) return FP8LL_ERR_INVALID_ARG;
-    if (rows == 0 || cols == 0) return FP8LL_OK;
-    RmsNormParams p = norm_params(x_bf16, residual_bf16, gamma_bf16, rows, cols, ldx, ldr, eps, h_bf16, rstd, y_bf16,
-                                  q_rows, q_cols);
-    if (!valid_norm(p, fmt)) return FP8LL_ERR_INVALID_ARG;
+// The three recipes' calls, of either norm, from parameters without the scales.
+int block_norm(NormParams p, bool center, int fmt, float* scale_rows, int64_t scale_ld_rows, float* scale_cols,
+               int64_t scale_ld_cols, fp8ll_stream_t stream) {
+    if (p.rows < 0 || p.cols < 0 || (fmt != FP8LL_E4M3 && fmt != FP8LL_E5M2)) return FP8LL_ERR_INVALID_ARG;
+    if (p.rows == 0 || p.cols == 0) return FP8LL_OK;
+    if (!valid_norm(p, center, fmt)) return FP8LL_ERR_INVALID_ARG;
     Range scales[2] = {{nullptr, 0}, {nullptr, 0}};
-    if (q_rows) {
-        if (!scale_rows || !aligned(scale_rows, 16) || scale_ld_rows < rows || scale_ld_rows % 4 != 0 ||
+    if (p.qr) {
+        if (!scale_rows || !aligned(scale_rows, 16) || scale_ld_rows < p.rows || scale_ld_rows % 4 != 0 ||
             scale_ld_rows >= (1LL << 36))
             return FP8LL_ERR_INVALID_ARG;
         p.sr = scale_rows;
         p.sldr = scale_ld_rows;
-        scales[0] = Range{scale_rows, ((cols / 128 - 1) * scale_ld_rows + rows) * 4};
+        scales[0] = Range{scale_rows, ((p.cols / 128 - 1) * scale_ld_rows + p.rows) * 4};
     }
-    if (q_cols) {
-        if (!scale_cols || !aligned(scale_cols, 16) || scale_ld_cols < cols || scale_ld_cols % 4 != 0 ||
+    if (p.qc) {
+        if (!scale_cols || !aligned(scale_cols, 16) || scale_ld_cols < p.cols || scale_ld_cols % 4 != 0 ||
             scale_ld_cols >= (1LL << 36))
             return FP8LL_ERR_INVALID_ARG;
         p.sc = scale_cols;
         p.sldc = scale_ld_cols;
-        scales[1] = Range{scale_cols, ((rows / 128 - 1) * scale_ld_cols + cols) * 4};
+        scales[1] = Range{scale_cols, ((p.rows / 128 - 1) * scale_ld_cols + p.cols) * 4};
     }
     if (!apart(p, scales, 2)) return FP8LL_ERR_INVALID_ARG;
-    return launch(p, kRecipeBlock, fmt, stream);
+    return launch(p, center, kRecipeBlock, fmt, stream);
 }
 
-int fp8_mx_rmsnorm_quantize(const void* x_bf16, const void* residual_bf16, const void* gamma_bf16, int64_t rows,
-                            int64_t cols, int64_t ldx, int64_t ldr, float eps, int fmt, void* h_bf16, float* rstd,
-                            void* y_bf16, uint8_t* q_rows, uint8_t* sf_rows, uint8_t* q_cols, uint8_t* sf_cols,
-                            fp8ll_stream_t stream) {
-    if (rows < 0 || cols < 0 || (fmt != FP8LL_E4M3 && fmt != FP8LL_E5M2)) return FP8LL_ERR_INVALID_ARG;
-    if (rows == 0 || cols == 0) return FP8LL_OK;
-    RmsNormParams p = norm_params(x_bf16, residual_bf16, gamma_bf16, rows, cols, ldx, ldr, eps, h_bf16, rstd, y_bf16,
-                                  q_rows, q_cols);
-    if (!valid_norm(p, fmt)) return FP8LL_ERR_INVALID_ARG;
-    if ((q_rows && (!sf_rows || !aligned(sf_rows, 16))) || (q_cols && (!sf_cols || !aligned(sf_cols, 16))))
+int mx_norm(NormParams p, bool center, int fmt, uint8_t* sf_rows, uint8_t* sf_cols, fp8ll_stream_t stream) {
+    if (p.rows < 0 || p.cols < 0 || (fmt != FP8LL_E4M3 && fmt != FP8LL_E5M2)) return FP8LL_ERR_INVALID_ARG;
+    if (p.rows == 0 || p.cols == 0) return FP8LL_OK;
+    if (!valid_norm(p, center, fmt)) return FP8LL_ERR_INVALID_ARG;
+    if ((p.qr && (!sf_rows || !aligned(sf_rows, 16))) || (p.qc && (!sf_cols || !aligned(sf_cols, 16))))
         return FP8LL_ERR_INVALID_ARG;
-    p.sfr = q_rows ? sf_rows : nullptr;
-    p.sfc = q_cols ? sf_cols : nullptr;
-    const Range scales[2] = {{p.sfr, static_cast<int64_t>(fp8_mx_sf_bytes(rows, cols))},
-                             {p.sfc, q_cols ? static_cast<int64_t>(fp8_mx_sf_bytes(cols, rows)) : 0}};
+    p.sfr = p.qr ? sf_rows : nullptr;
+    p.sfc = p.qc ? sf_cols : nullptr;
+    const Range scales[2] = {{p.sfr, static_cast<int64_t>(fp8_mx_sf_bytes(p.rows, p.cols))},
+                             {p.sfc, p.qc ? static_cast<int64_t>(fp8_mx_sf_bytes(p.cols, p.rows)) : 0}};
     if (!apart(p, scales, 2)) return FP8LL_ERR_INVALID_ARG;
-    return launch(p, kRecipeMx, fmt, stream);
+    return launch(p, center, kRecipeMx, fmt, stream);
 }
 
-int fp8_tensor_rmsnorm_quantize(const void* x_bf16, const void* residual_bf16, const void* gamma_bf16, int64_t rows,
-                                int64_t cols, int64_t ldx, int64_t ldr, float eps, int fmt, const float* amax_in,
-                                void* h_bf16, float* rstd, void* y_bf16, uint8_t* q_rows, uint8_t* q_cols,
-                                float* scale, float* amax_out, fp8ll_stream_t stream) {
-    if (rows < 0 || cols < 0 || (fmt != FP8LL_E4M3 && fmt != FP8LL_E5M2)) return FP8LL_ERR_INVALID_ARG;
-    if (rows == 0 || cols == 0) return FP8LL_OK;
-    RmsNormParams p = norm_params(x_bf16, residual_bf16, gamma_bf16, rows, cols, ldx, ldr, eps, h_bf16, rstd, y_bf16,
-                                  q_rows, q_cols);
-    if (!valid_norm(p, fmt)) return FP8LL_ERR_INVALID_ARG;
+int tensor_norm(NormParams p, bool center, int fmt, const float* amax_in, float* scale, float* amax_out,
+                fp8ll_stream_t stream) {
+    if (p.rows < 0 || p.cols < 0 || (fmt != FP8LL_E4M3 && fmt != FP8LL_E5M2)) return FP8LL_ERR_INVALID_ARG;
+    if (p.rows == 0 || p.cols == 0) return FP8LL_OK;
+    if (!valid_norm(p, center, fmt)) return FP8LL_ERR_INVALID_ARG;
     if (!amax_in || !aligned(amax_in, 4) || !scale || !aligned(scale, 4) || !aligned(amax_out, 4))
         return FP8LL_ERR_INVALID_ARG;
     // the kernels read *amax_in while they write the scale and the new amax
@@ -163,55 +154,64 @@ int fp8_tensor_rmsnorm_quantize(const void* x_bf16, const void* residual_bf16, c
     p.amax_out = amax_out;
     const Range scales[2] = {{scale, 4}, {amax_out, 4}}, in{amax_in, 4};
     if (!apart(p, scales, 2)) return FP8LL_ERR_INVALID_ARG;
-    const int64_t n = rows * cols;
-    for (const Range& out : {Range{h_bf16, 2 * n}, {rstd, 4 * rows}, {y_bf16, 2 * n}, {q_rows, n}, {q_cols, n}})
+    const int64_t n = p.rows * p.cols;
+    for (const Range& out :
+         {Range{p.h, 2 * n}, {p.rstd, 4 * p.rows}, {p.y, 2 * n}, {p.qr, n}, {p.qc, n}, {p.mean, 4 * p.rows}})
         if (share(out, in)) return FP8LL_ERR_INVALID_ARG;
-    return launch(p, kRecipeTensor, fmt, stream);
+    return launch(p, center, kRecipeTensor, fmt, stream);
 }
 
-size_t fp8_rmsnorm_workspace_size(int64_t rows, int64_t cols) {
-    if (rows < 1 || cols < 1 || cols > kNormMaxCols) return 0;
-    return static_cast<size_t>(rmsnorm_grad_max_bands(rows)) * static_cast<size_t>(cols) * sizeof(float);
+NormParams layernorm_params(const void* x, const void* residual, const void* gamma, const void* beta, int64_t rows,
+                            int64_t cols, int64_t ldx, int64_t ldr, float eps, void* h, float* mean, float* rstd,
+                            void* y, uint8_t* q_rows, uint8_t* q_cols) {
+    NormParams p = norm_params(x, residual, gamma, rows, cols, ldx, ldr, eps, h, rstd, y, q_rows, q_cols);
+    p.beta = static_cast<const uint16_t*>(beta);
+    p.mean = mean;
+    return p;
 }
 
-int fp8_rmsnorm_backward(const void* dy_bf16, const void* h_bf16, const void* gamma_bf16, const float* rstd,
-                         const void* residual_grad_bf16, int64_t rows, int64_t cols, int64_t lddy, int64_t ldh,
-                         int64_t ldres, void* dx_bf16, float* dgamma, int accumulate, void* workspace,
-                         size_t workspace_bytes, fp8ll_stream_t stream) {
-    if (rows < 0 || cols < 0 || (accumulate != 0 && accumulate != 1)) return FP8LL_ERR_INVALID_ARG;
+// The backward pass of either norm.
+int norm_backward(NormGradParams p, bool center, void* workspace, size_t workspace_bytes, int64_t need,
+                  fp8ll_stream_t stream) {
+    const int64_t rows = p.rows, cols = p.cols;
+    if (rows < 0 || cols < 0 || (p.accumulate != 0 && p.accumulate != 1)) return FP8LL_ERR_INVALID_ARG;
     if (cols == 0) return FP8LL_OK;
-    if (cols % 8 != 0 || cols > kNormMaxCols || !dgamma || !aligned(dgamma, 16)) return FP8LL_ERR_INVALID_ARG;
+    if (cols % 8 != 0 || cols > (center ? kLayerNormMaxCols : kNormMaxCols) || !p.dgamma || !aligned(p.dgamma, 16) ||
+        !aligned(p.dbeta, 16))
+        return FP8LL_ERR_INVALID_ARG;
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     int sms = 0;
     if (rows == 0) {  // a sum over no rows
+        if (share(Range{p.dgamma, cols * 4}, Range{p.dbeta, cols * 4})) return FP8LL_ERR_INVALID_ARG;
         const int rc = current_device_sms(&sms);
-        if (rc != FP8LL_OK || accumulate) return rc;
-        return cudaMemsetAsync(dgamma, 0, static_cast<size_t>(cols) * 4, reinterpret_cast<cudaStream_t>(stream)) ==
-                       cudaSuccess
-                   ? FP8LL_OK
-                   : FP8LL_ERR_LAUNCH;
+        if (rc != FP8LL_OK || p.accumulate) return rc;
+        const size_t bytes = static_cast<size_t>(cols) * 4;
+        if (cudaMemsetAsync(p.dgamma, 0, bytes, s) != cudaSuccess) return FP8LL_ERR_LAUNCH;
+        return !p.dbeta || cudaMemsetAsync(p.dbeta, 0, bytes, s) == cudaSuccess ? FP8LL_OK : FP8LL_ERR_LAUNCH;
     }
     if (rows > (1LL << 31) - 1) return FP8LL_ERR_INVALID_ARG;
-    if (!dy_bf16 || !h_bf16 || !gamma_bf16 || !rstd || !dx_bf16) return FP8LL_ERR_INVALID_ARG;
-    if (!aligned(dy_bf16, 16) || !aligned(h_bf16, 16) || !aligned(gamma_bf16, 16) || !aligned(rstd, 4) ||
-        !aligned(residual_grad_bf16, 16) || !aligned(dx_bf16, 16))
+    if (!p.dy || !p.h || !p.gamma || !p.rstd || !p.dx || (center && !p.mean)) return FP8LL_ERR_INVALID_ARG;
+    if (!aligned(p.dy, 16) || !aligned(p.h, 16) || !aligned(p.gamma, 16) || !aligned(p.rstd, 4) ||
+        !aligned(p.mean, 4) || !aligned(p.dres, 16) || !aligned(p.dx, 16))
         return FP8LL_ERR_INVALID_ARG;
-    if (lddy < cols || lddy % 8 != 0 || !spans(rows, lddy) || ldh < cols || ldh % 8 != 0 || !spans(rows, ldh))
+    if (p.lddy < cols || p.lddy % 8 != 0 || !spans(rows, p.lddy) || p.ldh < cols || p.ldh % 8 != 0 ||
+        !spans(rows, p.ldh))
         return FP8LL_ERR_INVALID_ARG;
-    if (residual_grad_bf16 && (ldres < cols || ldres % 8 != 0 || !spans(rows, ldres))) return FP8LL_ERR_INVALID_ARG;
-    const int64_t need = static_cast<int64_t>(fp8_rmsnorm_workspace_size(rows, cols));
+    if (p.dres && (p.ldres < cols || p.ldres % 8 != 0 || !spans(rows, p.ldres))) return FP8LL_ERR_INVALID_ARG;
     if (!workspace || !aligned(workspace, 16) || static_cast<int64_t>(workspace_bytes) < need)
         return FP8LL_ERR_WORKSPACE;
-    const Range in[5] = {{dy_bf16, ((rows - 1) * lddy + cols) * 2},
-                         {residual_grad_bf16, residual_grad_bf16 ? ((rows - 1) * ldres + cols) * 2 : 0},
-                         {h_bf16, ((rows - 1) * ldh + cols) * 2},
-                         {gamma_bf16, cols * 2},
-                         {rstd, rows * 4}};
-    const Range out[3] = {{dx_bf16, rows * cols * 2}, {dgamma, cols * 4}, {workspace, need}};
-    for (int i = 0; i < 3; ++i) {
-        for (int j = 0; j < 5; ++j) {
+    const Range in[6] = {{p.dy, ((rows - 1) * p.lddy + cols) * 2},
+                         {p.dres, p.dres ? ((rows - 1) * p.ldres + cols) * 2 : 0},
+                         {p.h, ((rows - 1) * p.ldh + cols) * 2},
+                         {p.gamma, cols * 2},
+                         {p.rstd, rows * 4},
+                         {p.mean, rows * 4}};
+    const Range out[4] = {{p.dx, rows * cols * 2}, {p.dgamma, cols * 4}, {workspace, need}, {p.dbeta, cols * 4}};
+    for (int i = 0; i < 4; ++i) {
+        for (int j = 0; j < 6; ++j) {
             // dx may take the place of dy or of the residual's gradient, element by element
-            const bool in_place = i == 0 && ((j == 0 && dx_bf16 == dy_bf16 && lddy == cols) ||
-                                             (j == 1 && dx_bf16 == residual_grad_bf16 && ldres == cols));
+            const bool in_place =
+                i == 0 && ((j == 0 && p.dx == p.dy && p.lddy == cols) || (j == 1 && p.dx == p.dres && p.ldres == cols));
             if (share(out[i], in[j]) && !in_place) return FP8LL_ERR_INVALID_ARG;
         }
         for (int j = 0; j < i; ++j)
@@ -219,22 +219,159 @@ int fp8_rmsnorm_backward(const void* dy_bf16, const void* h_bf16, const void* ga
     }
     const int rc = current_device_sms(&sms);
     if (rc != FP8LL_OK) return rc;
-    RmsNormGradParams p = {};
-    p.dy = static_cast<const uint16_t*>(dy_bf16);
-    p.h = static_cast<const uint16_t*>(h_bf16);
-    p.gamma = static_cast<const uint16_t*>(gamma_bf16);
+    p.partials = static_cast<float*>(workspace);
+    return (center ? launch_layernorm_grad(p, s, sms) : launch_rmsnorm_grad(p, s, sms)) == 0 ? FP8LL_OK
+                                                                                              : FP8LL_ERR_LAUNCH;
+}
+
+NormGradParams grad_params(const void* dy, const void* h, const void* gamma, const float* rstd, const void* dres,
+                           int64_t rows, int64_t cols, int64_t lddy, int64_t ldh, int64_t ldres, void* dx,
+                           float* dgamma, int accumulate) {
+    NormGradParams p = {};
+    p.dy = static_cast<const uint16_t*>(dy);
+    p.h = static_cast<const uint16_t*>(h);
+    p.gamma = static_cast<const uint16_t*>(gamma);
     p.rstd = rstd;
-    p.dres = static_cast<const uint16_t*>(residual_grad_bf16);
+    p.dres = static_cast<const uint16_t*>(dres);
     p.rows = rows;
     p.cols = cols;
     p.lddy = lddy;
     p.ldh = ldh;
     p.ldres = ldres;
-    p.dx = static_cast<uint16_t*>(dx_bf16);
+    p.dx = static_cast<uint16_t*>(dx);
     p.dgamma = dgamma;
     p.accumulate = accumulate;
-    p.partials = static_cast<float*>(workspace);
-    return launch_rmsnorm_grad(p, reinterpret_cast<cudaStream_t>(stream), sms) == 0 ? FP8LL_OK : FP8LL_ERR_LAUNCH;
+    return p;
+}
+
+}  // namespace
+
+extern "C" {
+
+int fp8_rmsnorm_quantize(const void* x_bf16, const void* residual_bf16, const void* gamma_bf16, int64_t rows,
+                         int64_t cols, int64_t ldx, int64_t ldr, float eps, int fmt, void* h_bf16, float* rstd,
+                         void* y_bf16, uint8_t* q_rows, float* scale_rows, int64_t scale_ld_rows, uint8_t* q_cols,
+                         float* scale_cols, int64_t scale_ld_cols, fp8ll_stream_t stream) {
+    return block_norm(norm_params(x_bf16, residual_bf16, gamma_bf16, rows, cols, ldx, ldr, eps, h_bf16, rstd, y_bf16,
+                                  q_rows, q_cols),
+                      false, fmt, scale_rows, scale_ld_rows, scale_cols, scale_ld_cols, stream);
+}
+
+int fp8_mx_rmsnorm_quantize(const void* x_bf16, const void* residual_bf16, const void* gamma_bf16, int64_t rows,
+                            int64_t cols, int64_t ldx, int64_t ldr, float eps, int fmt, void* h_bf16, float* rstd,
+                            void* y_bf16, uint8_t* q_rows, uint8_t* sf_rows, uint8_t* q_cols, uint8_t* sf_cols,
+                            fp8ll_stream_t stream) {
+    return mx_norm(norm_params(x_bf16, residual_bf16, gamma_bf16, rows, cols, ldx, ldr, eps, h_bf16, rstd, y_bf16,
+                               q_rows, q_cols),
+                   false, fmt, sf_rows, sf_cols, stream);
+}
+
+int fp8_tensor_rmsnorm_quantize(const void* x_bf16, const void* residual_bf16, const void* gamma_bf16, int64_t rows,
+                                int64_t cols, int64_t ldx, int64_t ldr, float eps, int fmt, const float* amax_in,
+                                void* h_bf16, float* rstd, void* y_bf16, uint8_t* q_rows, uint8_t* q_cols,
+                                float* scale, float* amax_out, fp8ll_stream_t stream) {
+    return tensor_norm(norm_params(x_bf16, residual_bf16, gamma_bf16, rows, cols, ldx, ldr, eps, h_bf16, rstd, y_bf16,
+                                   q_rows, q_cols),
+                       false, fmt, amax_in, scale, amax_out, stream);
+}
+
+int fp8_layernorm_quantize(const void* x_bf16, const void* residual_bf16, const void* gamma_bf16, const void* beta_bf16,
+                           int64_t rows, int64_t cols, int64_t ldx, int64_t ldr, float eps, int fmt, void* h_bf16,
+                           float* mean, float* rstd, void* y_bf16, uint8_t* q_rows, float* scale_rows,
+                           int64_t scale_ld_rows, uint8_t* q_cols, float* scale_cols, int64_t scale_ld_cols,
+                           fp8ll_stream_t stream) {
+    return block_norm(layernorm_params(x_bf16, residual_bf16, gamma_bf16, beta_bf16, rows, cols, ldx, ldr, eps, h_bf16,
+                                       mean, rstd, y_bf16, q_rows, q_cols),
+                      true, fmt, scale_rows, scale_ld_rows, scale_cols, scale_ld_cols, stream);
+}
+
+int fp8_mx_layernorm_quantize(const void* x_bf16, const void* residual_bf16, const void* gamma_bf16,
+                              const void* beta_bf16, int64_t rows, int64_t cols, int64_t ldx, int64_t ldr, float eps,
+                              int fmt, void* h_bf16, float* mean, float* rstd, void* y_bf16, uint8_t* q_rows,
+                              uint8_t* sf_rows, uint8_t* q_cols, uint8_t* sf_cols, fp8ll_stream_t stream) {
+    return mx_norm(layernorm_params(x_bf16, residual_bf16, gamma_bf16, beta_bf16, rows, cols, ldx, ldr, eps, h_bf16,
+                                    mean, rstd, y_bf16, q_rows, q_cols),
+                   true, fmt, sf_rows, sf_cols, stream);
+}
+
+int fp8_tensor_layernorm_quantize(const void* x_bf16, const void* residual_bf16, const void* gamma_bf16,
+                                  const void* beta_bf16, int64_t rows, int64_t cols, int64_t ldx, int64_t ldr,
+                                  float eps, int fmt, const float* amax_in, void* h_bf16, float* mean, float* rstd,
+                                  void* y_bf16, uint8_t* q_rows, uint8_t* q_cols, float* scale, float* amax_out,
+                                  fp8ll_stream_t stream) {
+    return tensor_norm(layernorm_params(x_bf16, residual_bf16, gamma_bf16, beta_bf16, rows, cols, ldx, ldr, eps, h_bf16,
+                                        mean, rstd, y_bf16, q_rows, q_cols),
+                       true, fmt, amax_in, scale, amax_out, stream);
+}
+
+size_t fp8_rmsnorm_workspace_size(int64_t rows, int64_t cols) {
+    if (rows < 1 || cols < 1 || cols > kNormMaxCols) return 0;
+    return static_cast<size_t>(norm_grad_max_bands(rows)) * static_cast<size_t>(cols) * sizeof(float);
+}
+
+int fp8_rmsnorm_backward(const void* dy_bf16, const void* h_bf16, const void* gamma_bf16, const float* rstd,
+                         const void* residual_grad_bf16, int64_t rows, int64_t cols, int64_t lddy, int64_t ldh,
+                         int64_t ldres, void* dx_bf16, float* dgamma, int accumulate, void* workspace,
+                         size_t workspace_bytes, fp8ll_stream_t stream) {
+    return norm_backward(grad_params(dy_bf16, h_bf16, gamma_bf16, rstd, residual_grad_bf16, rows, cols, lddy, ldh,
+                                     ldres, dx_bf16, dgamma, accumulate),
+                         false, workspace, workspace_bytes,
+                         static_cast<int64_t>(fp8_rmsnorm_workspace_size(rows, cols)), stream);
+}
+
+size_t fp8_layernorm_workspace_size(int64_t rows, int64_t cols) {
+    if (rows < 1 || cols < 1 || cols > kLayerNormMaxCols) return 0;
+    return static_cast<size_t>(norm_grad_max_bands(rows)) * 2 * static_cast<size_t>(cols) * sizeof(float);
+}
+
+int fp8_layernorm_backward(const void* dy_bf16, const void* h_bf16, const void* gamma_bf16, const float* mean,
+                           const float* rstd, const void* residual_grad_bf16, int64_t rows, int64_t cols, int64_t lddy,
+                           int64_t ldh, int64_t ldres, void* dx_bf16, float* dgamma, float* dbeta, int accumulate,
+                           void* workspace, size_t workspace_bytes, fp8ll_stream_t stream) {
+    NormGradParams p = grad_params(dy_bf16, h_bf16, gamma_bf16, rstd, residual_grad_bf16, rows, cols, lddy, ldh, ldres,
+                                   dx_bf16, dgamma, accumulate);
+    p.mean = mean;
+    p.dbeta = dbeta;
+    return norm_backward(p, true, workspace, workspace_bytes,
+                         static_cast<int64_t>(fp8_layernorm_workspace_size(rows, cols)), stream);
+}
+
+int fp8_dropout(const void* x_bf16, const void* residual_bf16, int64_t rows, int64_t cols, int64_t ldx, int64_t ldr,
+                double p, uint64_t seed, uint32_t site, int64_t step, const int64_t* step_dev, void* out_bf16,
+                fp8ll_stream_t stream) {
+    if (rows < 0 || cols < 0 || !(p >= 0.0 && p < 1.0)) return FP8LL_ERR_INVALID_ARG;
+    if (rows == 0 || cols == 0) return FP8LL_OK;
+    if (rows >= kDropoutMaxElements || cols >= kDropoutMaxElements / rows + 1 || rows * cols >= kDropoutMaxElements)
+        return FP8LL_ERR_INVALID_ARG;
+    if (!x_bf16 || !aligned(x_bf16, 2) || ldx < cols || !spans(rows, ldx) || !out_bf16 || !aligned(out_bf16, 2))
+        return FP8LL_ERR_INVALID_ARG;
+    if (residual_bf16 && (!aligned(residual_bf16, 2) || ldr < cols || !spans(rows, ldr))) return FP8LL_ERR_INVALID_ARG;
+    if (!aligned(step_dev, 8)) return FP8LL_ERR_INVALID_ARG;
+    const Range out{out_bf16, rows * cols * 2}, x{x_bf16, ((rows - 1) * ldx + cols) * 2};
+    const Range res{residual_bf16, residual_bf16 ? ((rows - 1) * ldr + cols) * 2 : 0}, counter{step_dev, 8};
+    // the output may take the place of x or of the residual, element by element
+    if (share(out, x) && !(out_bf16 == x_bf16 && (ldx == cols || rows == 1))) return FP8LL_ERR_INVALID_ARG;
+    if (share(out, res) && !(out_bf16 == residual_bf16 && (ldr == cols || rows == 1))) return FP8LL_ERR_INVALID_ARG;
+    if (share(out, counter)) return FP8LL_ERR_INVALID_ARG;
+    int sms = 0;
+    const int rc = current_device_sms(&sms);
+    if (rc != FP8LL_OK) return rc;
+    DropoutParams d = {};
+    d.x = static_cast<const uint16_t*>(x_bf16);
+    d.res = static_cast<const uint16_t*>(residual_bf16);
+    d.out = static_cast<uint16_t*>(out_bf16);
+    d.rows = rows;
+    d.cols = cols;
+    d.ldx = ldx;
+    d.ldr = residual_bf16 ? ldr : 0;
+    d.threshold = static_cast<uint32_t>(p * 4294967296.0);
+    d.scale = static_cast<float>(1.0 / (1.0 - p));
+    d.key0 = static_cast<uint32_t>(seed);
+    d.key1 = static_cast<uint32_t>(seed >> 32);
+    d.site = site;
+    d.step = static_cast<uint64_t>(step);
+    d.step_dev = step_dev;
+    return launch_dropout(d, reinterpret_cast<cudaStream_t>(stream), sms) == 0 ? FP8LL_OK : FP8LL_ERR_LAUNCH;
 }
 
 size_t fp8_grad_norm_workspace_size(int64_t count) {

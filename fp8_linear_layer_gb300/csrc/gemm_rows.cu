@@ -33,7 +33,7 @@
 #include "gemm_rows.h"
 #include "launch.cuh"
 #include "ptx.cuh"
-#include "rmsnorm.h"
+#include "norm.h"
 
 namespace fp8ll {
 namespace {

@@ -4,7 +4,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
-#include "rmsnorm.h"
+#include "norm.h"
 
 namespace fp8ll {
 

@@ -298,10 +298,16 @@ __device__ __forceinline__ void tmem_ld_16x256b_x4_pairs2(uint32_t a, uint32_t b
 }
 
 // packed fp32x2 arithmetic on 64-bit register pairs (low half = first element);
-// each lane rounds to nearest exactly as the scalar mul / fma would
+// each lane rounds to nearest exactly as the scalar mul / add / fma would
 __device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
     uint64_t d;
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
 

@@ -17,8 +17,9 @@
  *   fp8_grouped_wgrad   per-group fp32 out_g (+)= A_g B_g^T, groups along K
  *   fp8_bgrad_from_operand  bias gradient as row sums of a 1x128-scaled operand
  *   fp8_gemm_linear     Y = act(A B^T + bias) + residual (also few rows)
- *   fp8_rmsnorm_*       RMS norm with the residual's addition and an fp8 output,
- *                       and its backward pass
+ *   fp8_rmsnorm_*, fp8_layernorm_*  RMS and layer norm with the residual's addition
+ *                       and an fp8 output, and their backward passes
+ *   fp8_dropout         dropout from a counter-based generator, added to a residual
  *   fp8_grad_norm, fp8_clip_grads  global gradient norm and clipping
  *
  * Conventions shared by every entry point
@@ -501,6 +502,67 @@ int fp8_rmsnorm_backward(const void* dy_bf16, const void* h_bf16, const void* ga
                          const void* residual_grad_bf16, int64_t rows, int64_t cols, int64_t lddy, int64_t ldh,
                          int64_t ldres, void* dx_bf16, float* dgamma, int accumulate, void* workspace,
                          size_t workspace_bytes, fp8ll_stream_t stream);
+
+/* Layer norm of a residual stream, cast to fp8 for the GEMMs:
+ *   h = bf16(x + residual)                  (h = x without a residual)
+ *   mean = mean(h), rstd = 1 / sqrt(mean((h - mean)^2) + eps)   per row, of the rounded h
+ *                                           (rstd 0 where that root is 0)
+ *   y = fma(fl32(fl32(h - mean) * rstd), gamma, beta)  -> codes and scales by the
+ *                                           cast rules, from fp32
+ *   beta: bf16 [cols], 16-byte aligned, or NULL (0).  mean: fp32 [rows], for the
+ *   backward pass.  cols <= 28672.  Everything else, the three recipes' outputs
+ *   among it, as fp8_rmsnorm_quantize.  With eps = 0 a constant row gives beta if
+ *   its mean is exact in fp32, else digits of the mean's rounding.  A row that
+ *   holds an infinity or a NaN, or whose sum of squares overflows fp32, has no
+ *   meaningful output (NaN, or codes of beta); the other rows are not touched by it. */
+int fp8_layernorm_quantize(const void* x_bf16, const void* residual_bf16, const void* gamma_bf16, const void* beta_bf16,
+                           int64_t rows, int64_t cols, int64_t ldx, int64_t ldr, float eps, int fmt, void* h_bf16,
+                           float* mean, float* rstd, void* y_bf16, uint8_t* q_rows, float* scale_rows,
+                           int64_t scale_ld_rows, uint8_t* q_cols, float* scale_cols, int64_t scale_ld_cols,
+                           fp8ll_stream_t stream);
+int fp8_mx_layernorm_quantize(const void* x_bf16, const void* residual_bf16, const void* gamma_bf16,
+                              const void* beta_bf16, int64_t rows, int64_t cols, int64_t ldx, int64_t ldr, float eps,
+                              int fmt, void* h_bf16, float* mean, float* rstd, void* y_bf16, uint8_t* q_rows,
+                              uint8_t* sf_rows, uint8_t* q_cols, uint8_t* sf_cols, fp8ll_stream_t stream);
+int fp8_tensor_layernorm_quantize(const void* x_bf16, const void* residual_bf16, const void* gamma_bf16,
+                                  const void* beta_bf16, int64_t rows, int64_t cols, int64_t ldx, int64_t ldr,
+                                  float eps, int fmt, const float* amax_in, void* h_bf16, float* mean, float* rstd,
+                                  void* y_bf16, uint8_t* q_rows, uint8_t* q_cols, float* scale, float* amax_out,
+                                  fp8ll_stream_t stream);
+
+/* Bytes of workspace fp8_layernorm_backward needs (partial sums of dgamma and dbeta). */
+size_t fp8_layernorm_workspace_size(int64_t rows, int64_t cols);
+
+/* Backward pass of the layer norm, with xhat = (h - mean) rstd and d = dy gamma:
+ *   dx = rstd (d - mean(d) - xhat mean(d xhat)) + residual_grad   (bf16 [rows][cols])
+ *   dgamma[c] (+)= sum over rows of dy xhat,  dbeta[c] (+)= sum over rows of dy
+ *   (fp32 [cols], 16-byte aligned; dbeta may be NULL)
+ *   mean, rstd: the forward call's.  cols <= 28672.  Everything else as
+ *   fp8_rmsnorm_backward. */
+int fp8_layernorm_backward(const void* dy_bf16, const void* h_bf16, const void* gamma_bf16, const float* mean,
+                           const float* rstd, const void* residual_grad_bf16, int64_t rows, int64_t cols, int64_t lddy,
+                           int64_t ldh, int64_t ldres, void* dx_bf16, float* dgamma, float* dbeta, int accumulate,
+                           void* workspace, size_t workspace_bytes, fp8ll_stream_t stream);
+
+/* Dropout whose mask is never stored, added to a residual stream:
+ *   out[i] = bf16(residual[i] + (w_i < floor(p 2^32) ? 0 : x[i] * fl32(1 / (1 - p))))
+ * for element i = r * cols + c of the matrix by rows, whatever its strides.  w_i
+ * is word i % 4 of the counter-based generator Philox4x32-10 (Salmon, Moraes, Dror
+ * and Shaw, "Parallel random numbers: as easy as 1, 2, 3", 2011) with the key
+ * (seed's low half, seed's high half) and the counter (i / 4, site, step's low
+ * half, step's high half).  The gradient of x is the same call on the output's
+ * gradient, with the same numbers and no residual; the residual's is that gradient
+ * itself.  A dropped element counts as zero whatever x holds there.
+ *   x, residual, out: bf16, 2-byte aligned; leading dimensions >= cols; residual may
+ *   be NULL; out [rows][cols] contiguous, x or the residual itself when that is
+ *   contiguous, else overlapping neither.  Faster where addresses and (with gaps
+ *   between rows) rows are 16-byte aligned.  rows * cols < 2^34.
+ *   p: 0 <= p < 1.  seed: of a run.  site: which dropout of the model.
+ *   step: step plus, if step_dev is not NULL, *step_dev (DEVICE, 8-byte aligned),
+ *   which a captured step can count up between replays; both wrap at 64 bits. */
+int fp8_dropout(const void* x_bf16, const void* residual_bf16, int64_t rows, int64_t cols, int64_t ldx, int64_t ldr,
+                double p, uint64_t seed, uint32_t site, int64_t step, const int64_t* step_dev, void* out_bf16,
+                fp8ll_stream_t stream);
 
 /* One gradient tensor: n elements of fp32 or bf16, contiguous, aligned to the
  * element.  out: where the clipped gradient goes, of the same type: grad itself
