@@ -19,7 +19,7 @@ LIB_PATH = os.path.join(HERE, "libfp8ll.so")
 E4M3, E5M2 = 0, 1
 EPI_NONE, EPI_BIAS, EPI_BIAS_GELU, EPI_DGELU, EPI_DGELU_BGRAD = 0, 1, 2, 3, 4
 ACC_FULL, ACC_FAST = 0, 1
-ACT_NONE, ACT_GELU = 0, 1
+ACT_NONE, ACT_GELU, ACT_SILU = 0, 1, 2
 F32, BF16 = 0, 1
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED_DEVICE, ERR_LAUNCH, ERR_TIMEOUT, ERR_WORKSPACE, ERR_SCRATCH = 0, -1, -2, -3, -4, -5, -6
 
@@ -34,7 +34,8 @@ EXPORTS = ("fp8_scale_ld", "fp8_quantize", "fp8_quantize_dual", "fp8_cast_f32", 
            "fp8_tensor_rmsnorm_quantize", "fp8_rmsnorm_workspace_size", "fp8_rmsnorm_backward",
            "fp8_grad_norm_workspace_size", "fp8_grad_norm", "fp8_clip_grads", "fp8_layernorm_quantize",
            "fp8_mx_layernorm_quantize", "fp8_tensor_layernorm_quantize", "fp8_layernorm_workspace_size",
-           "fp8_layernorm_backward", "fp8_dropout")
+           "fp8_layernorm_backward", "fp8_dropout", "fp8_gemm_gated", "fp8_mx_gemm_gated", "fp8_tensor_gemm_gated",
+           "fp8_gemm_gated_dgrad", "fp8_mx_gemm_gated_dgrad", "fp8_tensor_gemm_gated_dgrad")
 
 
 class Fp8Error(RuntimeError):
@@ -114,6 +115,12 @@ def lib():
         L.fp8_gemm_linear.argtypes = [i64, i64, i64, op, op, vp, i32, vp, i64, i32, vp, vp, vp]
         L.fp8_mx_gemm_linear.argtypes = [i64, i64, i64, mop, mop, vp, i32, vp, i64, vp, vp, vp]
         L.fp8_tensor_gemm_linear.argtypes = [i64, i64, i64, top, top, vp, i32, vp, i64, vp, vp, vp]
+        L.fp8_gemm_gated.argtypes = [i64, i64, i64, op, op, vp, i32, i32, vp, vp, vp]
+        L.fp8_mx_gemm_gated.argtypes = [i64, i64, i64, mop, mop, vp, i32, vp, vp, vp]
+        L.fp8_tensor_gemm_gated.argtypes = [i64, i64, i64, top, top, vp, i32, vp, vp, vp]
+        L.fp8_gemm_gated_dgrad.argtypes = [i64, i64, i64, op, op, vp, i32, i32, vp, vp]
+        L.fp8_mx_gemm_gated_dgrad.argtypes = [i64, i64, i64, mop, mop, vp, i32, vp, vp]
+        L.fp8_tensor_gemm_gated_dgrad.argtypes = [i64, i64, i64, top, top, vp, i32, vp, vp]
         norm = [vp, vp, vp, i64, i64, i64, i64, f32, i32]
         L.fp8_rmsnorm_quantize.argtypes = norm + [vp, vp, vp, vp, vp, i64, vp, vp, i64, vp]
         L.fp8_mx_rmsnorm_quantize.argtypes = norm + [vp, vp, vp, vp, vp, vp, vp, vp]
@@ -144,7 +151,9 @@ def lib():
                      "fp8_gemm_linear", "fp8_mx_gemm_linear", "fp8_tensor_gemm_linear", "fp8_rmsnorm_quantize",
                      "fp8_mx_rmsnorm_quantize", "fp8_tensor_rmsnorm_quantize", "fp8_rmsnorm_backward",
                      "fp8_grad_norm", "fp8_clip_grads", "fp8_layernorm_quantize", "fp8_mx_layernorm_quantize",
-                     "fp8_tensor_layernorm_quantize", "fp8_layernorm_backward", "fp8_dropout", "fp8_get_device_status",
+                     "fp8_tensor_layernorm_quantize", "fp8_layernorm_backward", "fp8_dropout", "fp8_gemm_gated",
+                     "fp8_mx_gemm_gated", "fp8_tensor_gemm_gated", "fp8_gemm_gated_dgrad",
+                     "fp8_mx_gemm_gated_dgrad", "fp8_tensor_gemm_gated_dgrad", "fp8_get_device_status",
                      "fp8_debug_starve_next_gemm"):
             getattr(L, name).restype = i32
         _lib = L

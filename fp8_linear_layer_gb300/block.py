@@ -1,7 +1,8 @@
 """The operators of a pre-norm residual block around the FP8 linear layer:
 RMS and layer norm with the residual's addition and an fp8 output, their backward
 passes, dropout on the way into the residual stream, the matrix product with bias,
-activation and residual, and gradient clipping.
+activation and residual, the gated product and its data gradient, and gradient
+clipping.
 
 Argument marshalling only, as in ``binding``: every computation happens in the
 CUDA library, on torch's current stream.
@@ -13,7 +14,7 @@ from typing import Optional, Sequence, Union
 import torch
 
 from . import binding as B
-from .binding import (ACC_FULL, ACT_GELU, ACT_NONE, Fp8MxTensor, Fp8Tensor, Fp8TensorScaled, _check, empty_fp8,
+from .binding import (ACC_FULL, ACT_GELU, ACT_NONE, ACT_SILU, Fp8MxTensor, Fp8Tensor, Fp8TensorScaled, _check, empty_fp8,
                       empty_mx, lib)
 
 _bf16, _f32, _u8 = torch.bfloat16, torch.float32, torch.uint8
@@ -470,6 +471,100 @@ def tensor_gemm_linear(A: Fp8TensorScaled, W: Fp8TensorScaled, bias: Optional[to
     _check(lib().fp8_tensor_gemm_linear(*sizes, ctypes.byref(oa), ctypes.byref(ob), *args, *dst, _stream()),
            "fp8_tensor_gemm_linear")
     return out, aux
+
+
+# ----------------------------------------------------------- gated product ----
+
+def _operand_scales(t, rows, k):
+    """The scales of an operand of the gated products, which have to cover its rows."""
+    if isinstance(t, Fp8Tensor):
+        s = t.scale
+        assert s.dtype is _f32 and s.shape[0] >= k // 128 and s.shape[1] >= rows and s.stride()[1] == 1
+    elif isinstance(t, Fp8MxTensor):
+        s = t.sf
+        assert s.dtype is _u8 and s.is_contiguous() and s.numel() >= k // 32 * (-(-rows // 256) * 256)
+    else:
+        s = t.scale
+        assert s.dtype is _f32 and s.numel() == 1
+    return s
+
+
+def _gated_args(A, W, N, *others):
+    """(sizes, operands) of a gated product: A [M][K], W of as many columns; all on the current device."""
+    (M, K), (R, KW) = A.q.shape, W.q.shape
+    assert K == KW and A.q.dtype is _u8 and W.q.dtype is _u8
+    assert A.q.stride()[1] == 1 and W.q.stride()[1] == 1
+    _on_device(A.q, W.q, _operand_scales(A, M, K), _operand_scales(W, R, K), *others)
+    return (M, N, K), (ctypes.byref(A.operand()), ctypes.byref(W.operand()))
+
+
+def _gated(kind, call, A, W, bias, act, acc, out, aux, want_aux):
+    assert type(A) is kind and type(W) is kind
+    M, N = A.q.shape[0], W.q.shape[0] // 2
+    assert W.q.shape[0] == 2 * N, "W holds the gate's rows, then as many of the up projection"
+    if out is None:
+        out = torch.empty((M, N), dtype=_bf16, device=A.q.device)
+    if aux is None and want_aux:
+        aux = torch.empty((M, 2 * N), dtype=_bf16, device=A.q.device)
+    sizes, ops = _gated_args(A, W, N, bias, out, aux)
+    _check(getattr(lib(), call)(*sizes, *ops, _packed(bias, _bf16, (2 * N,)), act, *acc, _packed(out, _bf16, (M, N)),
+                                _packed(aux, _bf16, (M, 2 * N)), _stream()), call)
+    return out, aux
+
+
+def gemm_gated(A: Fp8Tensor, W: Fp8Tensor, bias: Optional[torch.Tensor] = None, act: int = ACT_SILU,
+               acc: int = ACC_FULL, out: Optional[torch.Tensor] = None, aux: Optional[torch.Tensor] = None,
+               want_aux: bool = False):
+    """Y (bf16 [M][N]) = act(Z[:, :N]) Z[:, N:] with Z = A W^T + bias [M][2 N], both
+    projections in one kernel; W [2 N][K] holds the gate's rows, then the up
+    projection's.  Returns (Y, Z-or-None), Z (bf16) with ``want_aux`` or ``aux`` for
+    the backward pass.  act: ACT_SILU or ACT_GELU.  Few rows run a kernel of their own."""
+    return _gated(Fp8Tensor, "fp8_gemm_gated", A, W, bias, act, (int(acc),), out, aux, want_aux)
+
+
+def mx_gemm_gated(A: Fp8MxTensor, W: Fp8MxTensor, bias: Optional[torch.Tensor] = None, act: int = ACT_SILU,
+                  out: Optional[torch.Tensor] = None, aux: Optional[torch.Tensor] = None, want_aux: bool = False):
+    """``gemm_gated`` on MXFP8 operands."""
+    return _gated(Fp8MxTensor, "fp8_mx_gemm_gated", A, W, bias, act, (), out, aux, want_aux)
+
+
+def tensor_gemm_gated(A: Fp8TensorScaled, W: Fp8TensorScaled, bias: Optional[torch.Tensor] = None,
+                      act: int = ACT_SILU, out: Optional[torch.Tensor] = None, aux: Optional[torch.Tensor] = None,
+                      want_aux: bool = False):
+    """``gemm_gated`` on per-tensor scaled operands."""
+    return _gated(Fp8TensorScaled, "fp8_tensor_gemm_gated", A, W, bias, act, (), out, aux, want_aux)
+
+
+def _gated_dgrad(kind, call, A, W, aux, act, acc, out):
+    assert type(A) is kind and type(W) is kind
+    M, N = A.q.shape[0], W.q.shape[0]
+    if out is None:
+        out = torch.empty((M, 2 * N), dtype=_bf16, device=A.q.device)
+    sizes, ops = _gated_args(A, W, N, aux, out)
+    _check(getattr(lib(), call)(*sizes, *ops, _packed(aux, _bf16, (M, 2 * N)), act, *acc,
+                                _packed(out, _bf16, (M, 2 * N)), _stream()), call)
+    return out
+
+
+def gemm_gated_dgrad(A: Fp8Tensor, W: Fp8Tensor, aux: torch.Tensor, act: int = ACT_SILU, acc: int = ACC_FULL,
+                     out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """dZ (bf16 [M][2 N]), the gradient of ``gemm_gated``'s Z = ``aux``, from the
+    gradient of its output, C = A W^T [M][N] (W: the second product's weight
+    transposed): dZ[:, :N] = C Z[:, N:] act'(Z[:, :N]), dZ[:, N:] = C act(Z[:, :N]).
+    ``out`` may be ``aux`` itself."""
+    return _gated_dgrad(Fp8Tensor, "fp8_gemm_gated_dgrad", A, W, aux, act, (int(acc),), out)
+
+
+def mx_gemm_gated_dgrad(A: Fp8MxTensor, W: Fp8MxTensor, aux: torch.Tensor, act: int = ACT_SILU,
+                        out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """``gemm_gated_dgrad`` on MXFP8 operands."""
+    return _gated_dgrad(Fp8MxTensor, "fp8_mx_gemm_gated_dgrad", A, W, aux, act, (), out)
+
+
+def tensor_gemm_gated_dgrad(A: Fp8TensorScaled, W: Fp8TensorScaled, aux: torch.Tensor, act: int = ACT_SILU,
+                            out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """``gemm_gated_dgrad`` on per-tensor scaled operands."""
+    return _gated_dgrad(Fp8TensorScaled, "fp8_tensor_gemm_gated_dgrad", A, W, aux, act, (), out)
 
 
 # ---------------------------------------------------------------- clipping ----

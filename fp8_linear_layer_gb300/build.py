@@ -17,7 +17,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfp8ll.so")
 SOURCES = ["api.cu", "quantize.cu", "gemm_fprop.cu", "gemm_dgrad.cu", "gemm_wgrad.cu", "gemm_mx.cu", "gemm_tensor.cu", "noalloc.cu", "bgrad_operand.cu",
-           "api_block.cu", "rmsnorm.cu", "layernorm.cu", "dropout.cu", "grad_clip.cu", "gemm_linear.cu", "gemm_rows.cu"]
+           "api_block.cu", "rmsnorm.cu", "layernorm.cu", "dropout.cu", "grad_clip.cu", "gemm_linear.cu", "gemm_gated.cu", "gemm_rows.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

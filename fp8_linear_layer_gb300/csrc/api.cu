@@ -207,9 +207,9 @@ bool valid_mx_operand(const fp8ll_mx_operand_t* op, int64_t rows, int64_t K) {
     return true;
 }
 
-// shared setup of the three MXFP8 GEMM entry points
+// shared setup of the MXFP8 GEMM entry points; sfb_atoms: of B, in one load
 int mx_setup(int64_t M, int64_t N, int64_t K, const fp8ll_mx_operand_t* A, const fp8ll_mx_operand_t* B,
-             TensorMaps& maps, GemmParams& p, DeviceInfo** dev) {
+             TensorMaps& maps, GemmParams& p, DeviceInfo** dev, uint32_t sfb_atoms = 2) {
     if (!valid_mn(M, N) || K < 128 || K % 128 != 0 || K >= (1LL << 36)) return FP8LL_ERR_INVALID_ARG;
     if (!valid_mx_operand(A, M, K) || !valid_mx_operand(B, N, K)) return FP8LL_ERR_INVALID_ARG;
     int rc = current_device(dev);
@@ -221,7 +221,7 @@ int mx_setup(int64_t M, int64_t N, int64_t K, const fp8ll_mx_operand_t* A, const
     if (!encode_codes(A->q, A->ld_q, M, K, 128, &maps.a) ||
         !encode_codes(B->q, B->ld_q, N, K, kTileN / 2, &maps.b) ||
         !encode_sf_atoms(A->sf, (K / 128) * sfa_groups, 1, &maps.sa) ||
-        !encode_sf_atoms(B->sf, (K / 128) * sfb_groups, 2, &maps.sb))
+        !encode_sf_atoms(B->sf, (K / 128) * sfb_groups, sfb_atoms, &maps.sb))
         return FP8LL_ERR_LAUNCH;
     std::memset(&p, 0, sizeof(p));
     p.M = static_cast<int32_t>(M);
@@ -365,6 +365,32 @@ static int fill_linear(const LinearArgs& a, GemmParams& p, bool pairs) {
     }
     if (pairs && p.N % 2 != 0) return gelu ? kEpiLinearGeluOdd : kEpiLinearOdd;
     return gelu ? kEpiLinearGeluAny : kEpiLinearAny;
+}
+
+// The gated product's arguments and its data gradient's: out [M][N] and aux
+// [M][2 N], or out and aux [M][2 N], which may be one buffer.
+static bool valid_gated(int64_t M, int64_t N, int64_t K, const void* bias, int act, const void* out, const void* aux,
+                        bool grad) {
+    if (!valid_mn(M, N) || N > (1LL << 30) || !valid_mn(M, 2 * N) || N % kGatedN != 0 || !valid_k(K)) return false;
+    if (act != FP8LL_ACT_GELU && act != FP8LL_ACT_SILU) return false;
+    if (!out || !aligned16(out) || !aligned16(aux) || !aligned16(bias) || (grad && !aux)) return false;
+    const int64_t out_bytes = M * N * (grad ? 4 : 2), aux_bytes = M * N * 4;
+    if (aux && overlaps(out, out_bytes, aux, aux_bytes) && !(grad && out == aux)) return false;
+    return !bias || (!overlaps(bias, N * 4, out, out_bytes) && !(aux && overlaps(bias, N * 4, aux, aux_bytes)));
+}
+
+// the gated product's tiles are kGatedN columns wide, of both projections; B of the
+// maps and parameters as they were set up has 2 N rows
+static void gated_tiles(GemmParams& p, int64_t N, bool pairs) {
+    p.N = static_cast<int32_t>(N);
+    p.num_n_tiles = static_cast<int32_t>(N / kGatedN);
+    p.tiles_per_group = (pairs ? p.num_m_pairs : p.num_m_tiles) * p.num_n_tiles;
+    p.total_tiles = p.tiles_per_group;
+}
+
+static int gated_epi(int act, bool grad) {
+    if (grad) return act == FP8LL_ACT_GELU ? kEpiGatedGeluGrad : kEpiGatedSiluGrad;
+    return act == FP8LL_ACT_GELU ? kEpiGatedGelu : kEpiGatedSilu;
 }
 
 extern "C" {
@@ -1087,6 +1113,167 @@ int fp8_tensor_gemm_linear(int64_t M, int64_t N, int64_t K, const fp8ll_tensor_o
     } else {
         rc = launch_gemm_tensor(maps, p, epi, s);
     }
+    return rc == 0 ? FP8LL_OK : FP8LL_ERR_LAUNCH;
+}
+
+int fp8_gemm_gated(int64_t M, int64_t N, int64_t K, const fp8ll_operand_t* A, const fp8ll_operand_t* B,
+                   const void* bias_bf16, int act, int acc_mode, void* out_bf16, void* aux_bf16,
+                   fp8ll_stream_t stream) {
+    if (!valid_gated(M, N, K, bias_bf16, act, out_bf16, aux_bf16, false)) return FP8LL_ERR_INVALID_ARG;
+    if (acc_mode != FP8LL_ACC_FULL && acc_mode != FP8LL_ACC_FAST) return FP8LL_ERR_INVALID_ARG;
+    if (!valid_operand(A, M, K) || !valid_operand(B, 2 * N, K)) return FP8LL_ERR_INVALID_ARG;
+    DeviceInfo* dev = nullptr;
+    const int rc = current_device(&dev);
+    if (rc != FP8LL_OK) return rc;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (rows_kernel_taken(M, 2 * N, K, kRecipeBlock)) {
+        RowsParams r = rows_params(M, N, K, A->fmt, B->fmt, LinearArgs{bias_bf16, act, nullptr, 0, out_bf16, aux_bf16}, dev);
+        r.idesc |= 1u << 4;  // fp32 accumulators
+        RowsMaps rm;
+        if (!encode_operand(B, 2 * N, K, kRowsFeatures / 2, &rm.w, &rm.sw) ||
+            !encode_operand(A, M, K, static_cast<uint32_t>(rows_tokens(M)), &rm.x, &rm.sx))
+            return FP8LL_ERR_LAUNCH;
+        return launch_gemm_rows_gated(rm, r, kRecipeBlock, s) == 0 ? FP8LL_OK : FP8LL_ERR_LAUNCH;
+    }
+    TensorMaps maps;
+    if (!encode_operand(A, M, K, 128, &maps.a, &maps.sa) || !encode_operand(B, 2 * N, K, kGatedN, &maps.b, &maps.sb))
+        return FP8LL_ERR_LAUNCH;
+    std::memset(&maps.z, 0, sizeof(maps.z));
+    GemmParams p;
+    init_params(p, M, 2 * N, A, B, dev);
+    gated_tiles(p, N, false);
+    p.num_groups = 1;
+    p.groups[0] = GroupEntry{0, static_cast<int32_t>(K / 128), 0, 0};
+    p.out = out_bf16;
+    p.aux = aux_bf16;
+    p.bias = bias_bf16;
+    return launch_gemm_gated(maps, p, gated_epi(act, false), gemm_linear_parts(p), s, grid_for(p, dev)) == 0
+               ? FP8LL_OK
+               : FP8LL_ERR_LAUNCH;
+}
+
+int fp8_mx_gemm_gated(int64_t M, int64_t N, int64_t K, const fp8ll_mx_operand_t* A, const fp8ll_mx_operand_t* B,
+                      const void* bias_bf16, int act, void* out_bf16, void* aux_bf16, fp8ll_stream_t stream) {
+    if (!valid_gated(M, N, K, bias_bf16, act, out_bf16, aux_bf16, false)) return FP8LL_ERR_INVALID_ARG;
+    if (!valid_mx_operand(A, M, K) || !valid_mx_operand(B, 2 * N, K)) return FP8LL_ERR_INVALID_ARG;
+    DeviceInfo* dev = nullptr;
+    int rc = current_device(&dev);
+    if (rc != FP8LL_OK) return rc;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (rows_kernel_taken(M, 2 * N, K, kRecipeMx)) {
+        RowsParams r = rows_params(M, N, K, A->fmt, B->fmt, LinearArgs{bias_bf16, act, nullptr, 0, out_bf16, aux_bf16}, dev);
+        r.idesc |= 1u << 23;  // UE8M0 scales
+        r.groups_w = mx_sf_groups(2 * N);
+        r.groups_x = mx_sf_groups(M);
+        RowsMaps rm;
+        if (!encode_codes(B->q, B->ld_q, 2 * N, K, kRowsFeatures / 2, &rm.w) ||
+            !encode_codes(A->q, A->ld_q, M, K, static_cast<uint32_t>(rows_tokens(M)), &rm.x) ||
+            !encode_sf_atoms(B->sf, (K / 128) * r.groups_w, 1, &rm.sw) ||
+            !encode_sf_atoms(A->sf, (K / 128) * r.groups_x, 1, &rm.sx))
+            return FP8LL_ERR_LAUNCH;
+        return launch_gemm_rows_gated(rm, r, kRecipeMx, s) == 0 ? FP8LL_OK : FP8LL_ERR_LAUNCH;
+    }
+    TensorMaps maps;
+    GemmParams p;
+    rc = mx_setup(M, 2 * N, K, A, B, maps, p, &dev, 1);
+    if (rc != FP8LL_OK) return rc;
+    gated_tiles(p, N, true);
+    p.out = out_bf16;
+    p.aux = aux_bf16;
+    p.bias = bias_bf16;
+    const int epi = gated_epi(act, false);
+    rc = launch_gemm_mx_splits(p) ? launch_gemm_mx_split(maps, p, epi, s) : launch_gemm_mx(maps, p, epi, s);
+    return rc == 0 ? FP8LL_OK : FP8LL_ERR_LAUNCH;
+}
+
+int fp8_tensor_gemm_gated(int64_t M, int64_t N, int64_t K, const fp8ll_tensor_operand_t* A,
+                          const fp8ll_tensor_operand_t* B, const void* bias_bf16, int act, void* out_bf16,
+                          void* aux_bf16, fp8ll_stream_t stream) {
+    if (!valid_gated(M, N, K, bias_bf16, act, out_bf16, aux_bf16, false)) return FP8LL_ERR_INVALID_ARG;
+    if (!valid_tensor_operand(A, M, K) || !valid_tensor_operand(B, 2 * N, K)) return FP8LL_ERR_INVALID_ARG;
+    DeviceInfo* dev = nullptr;
+    int rc = current_device(&dev);
+    if (rc != FP8LL_OK) return rc;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (rows_kernel_taken(M, 2 * N, K, kRecipeTensor)) {
+        RowsParams r = rows_params(M, N, K, A->fmt, B->fmt, LinearArgs{bias_bf16, act, nullptr, 0, out_bf16, aux_bf16}, dev);
+        r.idesc |= 1u << 4;  // fp32 accumulators
+        r.tsw = B->scale;
+        r.tsx = A->scale;
+        RowsMaps rm = {};
+        if (!encode_codes(B->q, B->ld_q, 2 * N, K, kRowsFeatures / 2, &rm.w) ||
+            !encode_codes(A->q, A->ld_q, M, K, static_cast<uint32_t>(rows_tokens(M)), &rm.x))
+            return FP8LL_ERR_LAUNCH;
+        return launch_gemm_rows_gated(rm, r, kRecipeTensor, s) == 0 ? FP8LL_OK : FP8LL_ERR_LAUNCH;
+    }
+    TensorMaps maps;
+    GemmParams p;
+    rc = tensor_setup(M, 2 * N, K, A, B, maps, p, &dev);
+    if (rc != FP8LL_OK) return rc;
+    gated_tiles(p, N, true);
+    p.out = out_bf16;
+    p.aux = aux_bf16;
+    p.bias = bias_bf16;
+    const int epi = gated_epi(act, false);
+    rc = launch_gemm_tensor_splits(p) ? launch_gemm_tensor_split(maps, p, epi, s) : launch_gemm_tensor(maps, p, epi, s);
+    return rc == 0 ? FP8LL_OK : FP8LL_ERR_LAUNCH;
+}
+
+int fp8_gemm_gated_dgrad(int64_t M, int64_t N, int64_t K, const fp8ll_operand_t* A, const fp8ll_operand_t* B,
+                         const void* aux_bf16, int act, int acc_mode, void* out_bf16, fp8ll_stream_t stream) {
+    if (!valid_gated(M, N, K, nullptr, act, out_bf16, aux_bf16, true)) return FP8LL_ERR_INVALID_ARG;
+    if (acc_mode != FP8LL_ACC_FULL && acc_mode != FP8LL_ACC_FAST) return FP8LL_ERR_INVALID_ARG;
+    if (!valid_operand(A, M, K) || !valid_operand(B, N, K)) return FP8LL_ERR_INVALID_ARG;
+    DeviceInfo* dev = nullptr;
+    const int rc = current_device(&dev);
+    if (rc != FP8LL_OK) return rc;
+    TensorMaps maps;
+    if (!encode_operand(A, M, K, 128, &maps.a, &maps.sa) || !encode_operand(B, N, K, kTileN, &maps.b, &maps.sb))
+        return FP8LL_ERR_LAUNCH;
+    std::memset(&maps.z, 0, sizeof(maps.z));
+    GemmParams p;
+    init_params(p, M, N, A, B, dev);
+    p.num_groups = 1;
+    p.groups[0] = GroupEntry{0, static_cast<int32_t>(K / 128), 0, 0};
+    p.total_tiles = p.tiles_per_group;
+    p.out = out_bf16;
+    p.aux = const_cast<void*>(aux_bf16);
+    return launch_gemm_gated(maps, p, gated_epi(act, true), gemm_linear_parts(p), reinterpret_cast<cudaStream_t>(stream),
+                             grid_for(p, dev)) == 0
+               ? FP8LL_OK
+               : FP8LL_ERR_LAUNCH;
+}
+
+int fp8_mx_gemm_gated_dgrad(int64_t M, int64_t N, int64_t K, const fp8ll_mx_operand_t* A, const fp8ll_mx_operand_t* B,
+                            const void* aux_bf16, int act, void* out_bf16, fp8ll_stream_t stream) {
+    if (!valid_gated(M, N, K, nullptr, act, out_bf16, aux_bf16, true)) return FP8LL_ERR_INVALID_ARG;
+    TensorMaps maps;
+    GemmParams p;
+    DeviceInfo* dev = nullptr;
+    int rc = mx_setup(M, N, K, A, B, maps, p, &dev);
+    if (rc != FP8LL_OK) return rc;
+    p.out = out_bf16;
+    p.aux = const_cast<void*>(aux_bf16);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const int epi = gated_epi(act, true);
+    rc = launch_gemm_mx_splits(p) ? launch_gemm_mx_split(maps, p, epi, s) : launch_gemm_mx(maps, p, epi, s);
+    return rc == 0 ? FP8LL_OK : FP8LL_ERR_LAUNCH;
+}
+
+int fp8_tensor_gemm_gated_dgrad(int64_t M, int64_t N, int64_t K, const fp8ll_tensor_operand_t* A,
+                                const fp8ll_tensor_operand_t* B, const void* aux_bf16, int act, void* out_bf16,
+                                fp8ll_stream_t stream) {
+    if (!valid_gated(M, N, K, nullptr, act, out_bf16, aux_bf16, true)) return FP8LL_ERR_INVALID_ARG;
+    TensorMaps maps;
+    GemmParams p;
+    DeviceInfo* dev = nullptr;
+    int rc = tensor_setup(M, N, K, A, B, maps, p, &dev);
+    if (rc != FP8LL_OK) return rc;
+    p.out = out_bf16;
+    p.aux = const_cast<void*>(aux_bf16);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const int epi = gated_epi(act, true);
+    rc = launch_gemm_tensor_splits(p) ? launch_gemm_tensor_split(maps, p, epi, s) : launch_gemm_tensor(maps, p, epi, s);
     return rc == 0 ? FP8LL_OK : FP8LL_ERR_LAUNCH;
 }
 

@@ -125,6 +125,36 @@ constexpr bool is_odd_linear() {
     return EPI == kEpiLinearOdd || EPI == kEpiLinearGeluOdd;
 }
 
+template <int EPI>
+constexpr bool is_gated() {
+    return EPI == kEpiGatedSilu || EPI == kEpiGatedGelu;
+}
+template <int EPI>
+constexpr bool is_gated_grad() {
+    return EPI == kEpiGatedSiluGrad || EPI == kEpiGatedGeluGrad;
+}
+template <int EPI>
+constexpr bool is_gelu_gate() {
+    return EPI == kEpiGatedGelu || EPI == kEpiGatedGeluGrad;
+}
+// launched to overlap the end of the kernel before
+template <int EPI>
+constexpr bool is_dependent() {
+    return is_linear<EPI>() || is_gated<EPI>() || is_gated_grad<EPI>();
+}
+// output columns of a tile, and of them an epilogue warpgroup's
+template <int EPI>
+constexpr int tile_cols() {
+    return is_gated<EPI>() ? kGatedN : kTileN;
+}
+// The gated product's tile holds kGatedN columns of the gate and, behind them, the
+// same ones of the up projection.  A thread's chunks 0 to 7 are the gate's, 8 to 15
+// the up projection's of the same columns: this many columns are left out between.
+template <int EPI>
+constexpr int gate_skip() {
+    return is_gated<EPI>() ? kGatedN / 2 : 0;
+}
+
 // the linear epilogue of any sizes stages 8 rows x 128 columns per epilogue warp
 template <int EPI>
 constexpr size_t any_stage_bytes() {
@@ -829,6 +859,122 @@ __device__ __forceinline__ void store_linear(const GemmParams& p, int row0, int 
     }
 }
 
+// gated: Z = acc + bias, Y = act(Z_gate) Z_up, bf16 out [M][N] (+ bf16 aux Z
+// [M][2 N], the gate's columns first).  N % 128 == 0, so rows are 16-byte aligned
+// and columns beyond the matrix do not exist.  A thread's chunks c and c + 8 hold the
+// gate's and the up projection's sums of the same outputs.  ROWS as store_linear.
+template <bool GELU, int ROWS = 4>
+__device__ __forceinline__ void store_gated(const GemmParams& p, int row0, int col0,
+                                            const uint64_t (&acc)[4 * kChunks]) {
+    uint16_t* out = static_cast<uint16_t*>(p.out);
+    uint16_t* aux = static_cast<uint16_t*>(p.aux);
+    const uint16_t* bias = static_cast<const uint16_t*>(p.bias);
+    const int cq = (col0 >> 1) & 3;
+    const int cbase = col0 - 2 * cq;
+#pragma unroll
+    for (int g = 0; g < kChunks / 8; ++g) {
+        uint32_t yw[4][4], gw[4][4], uw[4][4];  // [row][chunk]
+        uint32_t bg[4], bu[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int col = col0 + 8 * (4 * g + j);
+            bg[j] = bias ? *reinterpret_cast<const uint32_t*>(bias + col) : 0u;
+            bu[j] = bias ? *reinterpret_cast<const uint32_t*>(bias + p.N + col) : 0u;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int c = 4 * g + j;
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r) {
+                float2 z = unpack_f32x2(acc[4 * c + r]), u = unpack_f32x2(acc[4 * (c + kChunks / 2) + r]);
+                z = make_float2(z.x + bf16_lo(bg[j]), z.y + bf16_hi(bg[j]));
+                u = make_float2(u.x + bf16_lo(bu[j]), u.y + bf16_hi(bu[j]));
+                const float2 a = gate2<GELU>(z.x, z.y);
+                yw[r][j] = pack_bf16x2(a.x * u.x, a.y * u.y);
+                gw[r][j] = pack_bf16x2(z.x, z.y);
+                uw[r][j] = pack_bf16x2(u.x, u.y);
+            }
+        }
+        const int vcol = cbase + 8 * (4 * g + cq);  // the lane's eight columns in the transposed order
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+            quad_transpose(yw[r], cq);
+            if (aux) {
+                quad_transpose(gw[r], cq);
+                quad_transpose(uw[r], cq);
+            }
+            const int64_t row = row0 + 8 * r;
+            if (row >= p.M) continue;
+            *reinterpret_cast<uint4*>(out + row * p.N + vcol) = make_uint4(yw[r][0], yw[r][1], yw[r][2], yw[r][3]);
+            if (aux) {
+                uint16_t* z = aux + 2 * row * p.N + vcol;
+                *reinterpret_cast<uint4*>(z) = make_uint4(gw[r][0], gw[r][1], gw[r][2], gw[r][3]);
+                *reinterpret_cast<uint4*>(z + p.N) = make_uint4(uw[r][0], uw[r][1], uw[r][2], uw[r][3]);
+            }
+        }
+    }
+}
+
+// gated gradient: dZ = (acc Z_up act'(Z_gate), acc act(Z_gate)), bf16 out [M][2 N]
+// with Z = aux [M][2 N], N % 128 == 0.  Z is read in the vectors that dZ is written
+// in, each lane its own before it writes them: out may be Z's own buffer.
+template <bool GELU, int ROWS = 4>
+__device__ __forceinline__ void store_gated_grad(const GemmParams& p, int row0, int col0,
+                                                 const uint64_t (&acc)[4 * kChunks]) {
+    uint16_t* out = static_cast<uint16_t*>(p.out);
+    const uint16_t* aux = static_cast<const uint16_t*>(p.aux);
+    const int cq = (col0 >> 1) & 3;
+    const int cbase = col0 - 2 * cq;
+    if (cbase >= p.N) return;  // the second half of the last tile of an odd number of 128-column blocks
+#pragma unroll
+    for (int g = 0; g < kChunks / 4; ++g) {
+        const int vcol = cbase + 8 * (4 * g + cq);
+        uint32_t gw[4][4], uw[4][4];  // [row][chunk]: Z, until dZ replaces it
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+            const int64_t row = row0 + 8 * r;
+            uint4 a = make_uint4(0, 0, 0, 0), b = a;
+            if (row < p.M) {
+                const uint16_t* z = aux + 2 * row * p.N + vcol;
+                a = *reinterpret_cast<const uint4*>(z);
+                b = *reinterpret_cast<const uint4*>(z + p.N);
+            }
+            gw[r][0] = a.x; gw[r][1] = a.y; gw[r][2] = a.z; gw[r][3] = a.w;
+            uw[r][0] = b.x; uw[r][1] = b.y; uw[r][2] = b.z; uw[r][3] = b.w;
+        }
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+            quad_transpose(gw[r], cq);
+            quad_transpose(uw[r], cq);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 c = unpack_f32x2(acc[4 * (4 * g + j) + r]);
+                float2 y, d;
+                gate_grad2<GELU>(bf16_lo(gw[r][j]), bf16_hi(gw[r][j]), y, d);
+                gw[r][j] = pack_bf16x2(c.x * bf16_lo(uw[r][j]) * d.x, c.y * bf16_hi(uw[r][j]) * d.y);
+                uw[r][j] = pack_bf16x2(c.x * y.x, c.y * y.y);
+            }
+            quad_transpose(gw[r], cq);
+            quad_transpose(uw[r], cq);
+            const int64_t row = row0 + 8 * r;
+            if (row >= p.M) continue;
+            uint16_t* o = out + 2 * row * p.N + vcol;
+            *reinterpret_cast<uint4*>(o) = make_uint4(gw[r][0], gw[r][1], gw[r][2], gw[r][3]);
+            *reinterpret_cast<uint4*>(o + p.N) = make_uint4(uw[r][0], uw[r][1], uw[r][2], uw[r][3]);
+        }
+    }
+}
+
+// asks for Z of a thread's tile rows in L2 while the K loop runs, as prefetch_residual
+__device__ __forceinline__ void prefetch_gates(const GemmParams& p, int prow, int pc0) {
+    if (prow >= p.M || pc0 >= p.N) return;
+    const uint16_t* z = static_cast<const uint16_t*>(p.aux) + 2 * static_cast<int64_t>(prow) * p.N + pc0;
+    prefetch_l2(z);
+    prefetch_l2(z + 64);
+    prefetch_l2(z + p.N);
+    prefetch_l2(z + p.N + 64);
+}
+
 // asks for the residual of a thread's tile rows in L2 while the K loop runs
 // (each lane of a quad one of the quad's four rows, 128 columns: three lines)
 __device__ __forceinline__ void prefetch_residual(const GemmParams& p, int prow, int pc0) {
@@ -970,7 +1116,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* const zs = reinterpret_cast<uint8_t*>(&sm) + sizeof(SmemLayout);  // Z, residual or output staging
     const bool z_staged = SPLIT == 1 && uses_z<EPI>() && p.z_tma != 0;
     bool exchanged = false;  // SPLIT > 1: this warp has passed the cluster's exchange barrier
-    if (is_linear<EPI>()) {
+    if (is_dependent<EPI>()) {
         await_dependency();
         release_dependents();
     }
@@ -992,7 +1138,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     int g, mt, nt;
                     decode_tile(p, t, g, mt, nt);
                     const GroupEntry ge = p.groups[g];
-                    const int m0 = mt * kBM, n0 = nt * kBN;
+                    const int m0 = mt * kBM, n0 = nt * tile_cols<EPI>();
                     const int kb_end = share(ge.nkb, 1);
                     for (int kb = share(ge.nkb, 0); kb < kb_end; ++kb) {
                         const int kbg = ge.kb_start + kb;
@@ -1004,6 +1150,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         mbar_arrive_expect_tx(fb, kBM * kBK + kBN * kBK);
                         tma_load_2d(smem_addr(sm.a[s]), &maps.a, fb, kbg * kBK, m0);
                         tma_load_2d(smem_addr(sm.b[s]), &maps.b, fb, kbg * kBK, n0);
+                        if (is_gated<EPI>())  // boxes of 128 rows: the gate's, and the up projection's
+                            tma_load_2d(smem_addr(sm.b[s] + kGatedN * kBK), &maps.b, fb, kbg * kBK, p.N + n0);
                         ++n_issued;
                         ring_advance<kStages>(s, ph);
                         if (!mbar_wait(smem_addr(&sm.sempty[ss]), sph ^ 1u, budget)) {
@@ -1014,6 +1162,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         mbar_arrive_expect_tx(sfb, (kBM + kBN) * 4);
                         tma_load_2d(smem_addr(sm.sa[ss]), &maps.sa, sfb, m0, kbg);
                         tma_load_2d(smem_addr(sm.sb[ss]), &maps.sb, sfb, n0, kbg);
+                        if (is_gated<EPI>())
+                            tma_load_2d(smem_addr(sm.sb[ss] + kGatedN), &maps.sb, sfb, p.N + n0, kbg);
                         ++ns_issued;
                         ring_advance<kSStages>(ss, sph);
                     }
@@ -1133,13 +1283,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             int g, mt, nt;
             decode_tile(p, t, g, mt, nt);
             const GroupEntry ge = p.groups[g];
-            const int m0 = mt * kBM, n0 = nt * kBN;
+            constexpr int kGroupN = tile_cols<EPI>() / kEpiGroups;  // output columns of a warpgroup
+            const int m0 = mt * kBM, n0 = nt * tile_cols<EPI>();
             uint64_t acc[4 * kChunks];  // packed fp32 pairs, layout described above the stores
 #pragma unroll
             for (int j = 0; j < 4 * kChunks; ++j) acc[j] = 0ull;
             const uint32_t tq = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
-                                static_cast<uint32_t>(half * kHalfN);
-            if (is_linear<EPI>()) {
+                                static_cast<uint32_t>(half * kGroupN);
+            if (is_gated_grad<EPI>()) {
+                prefetch_gates(p, m0 + q * 32 + g8 + 8 * cq, n0 + half * kHalfN);
+            } else if (is_linear<EPI>()) {
                 if (is_any_linear<EPI>() || SPLIT > 1) prefetch_residual(p, m0 + q * 32 + g8 + 8 * cq, n0 + half * kHalfN);
             } else if (uses_z<EPI>() && !z_staged) {
                 // the stored pre-activations of this tile are read once the K loop
@@ -1169,11 +1322,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float s = sm.sa[ss][q * 32 + g8 + 8 * r];
                     sa2[r] = pack_f32x2(s, s);
                 }
-                const float* sbp = &sm.sb[ss][half * kHalfN + 2 * cq];
+                const float* sbp = &sm.sb[ss][half * kGroupN + 2 * cq];
 #pragma unroll
                 for (int h = 0; h < 4; ++h) {
                     uint64_t plo[8], phi[8];
-                    tmem_ld_16x256b_x4_pairs2(tbuf + 32u * h, tbuf + (16u << 16) + 32u * h, plo, phi);
+                    const uint32_t tcol = 32u * h + (h >= 2 ? gate_skip<EPI>() : 0);
+                    tmem_ld_16x256b_x4_pairs2(tbuf + tcol, tbuf + (16u << 16) + tcol, plo, phi);
                     if (h == 3) {
                         // the block's partial sums are all in registers: hand the buffer back
                         tc_fence_before();
@@ -1183,7 +1337,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int c = 4 * h + i;
-                        const uint64_t sb = *reinterpret_cast<const uint64_t*>(sbp + 8 * c);
+                        const uint64_t sb =
+                            *reinterpret_cast<const uint64_t*>(sbp + 8 * c + (h >= 2 ? gate_skip<EPI>() : 0));
                         acc[4 * c + 0] = fma_f32x2(plo[2 * i], mul_f32x2(sa2[0], sb), acc[4 * c + 0]);
                         acc[4 * c + 1] = fma_f32x2(plo[2 * i + 1], mul_f32x2(sa2[1], sb), acc[4 * c + 1]);
                         acc[4 * c + 2] = fma_f32x2(phi[2 * i], mul_f32x2(sa2[2], sb), acc[4 * c + 2]);
@@ -1214,8 +1369,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 asm volatile("" : "+r"(t_again));
                 decode_tile(p, t_again, g, mt, nt);
                 const int row = mt * kBM + ((tid >> 5) & 3) * 32 + ((tid & 31) >> 2) + 8 * (4 / SPLIT) * part;
-                const int col = nt * kBN + (tid >> 7) * kHalfN + 2 * (tid & 3);
-                if (is_any_linear<EPI>())
+                const int col = nt * tile_cols<EPI>() + (tid >> 7) * kGroupN + 2 * (tid & 3);
+                if (is_gated<EPI>())
+                    store_gated<is_gelu_gate<EPI>(), 4 / SPLIT>(p, row, col, acc);
+                else if (is_gated_grad<EPI>())
+                    store_gated_grad<is_gelu_gate<EPI>(), 4 / SPLIT>(p, row, col, acc);
+                else if (is_any_linear<EPI>())
                     store_linear_any<is_gelu_linear<EPI>(), 4 / SPLIT>(
                         p, row, col, acc, tid & 31, reinterpret_cast<uint32_t*>(zs + (tid >> 5) * kAnyWarpBytes));
                 else
@@ -1224,8 +1383,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
             }
             const int row0 = m0 + q * 32 + g8;
-            const int col0 = n0 + half * kHalfN + 2 * cq;
-            if (EPI == kEpiWgrad) {
+            const int col0 = n0 + half * kGroupN + 2 * cq;
+            if (is_gated<EPI>()) {
+                store_gated<is_gelu_gate<EPI>()>(p, row0, col0, acc);
+            } else if (is_gated_grad<EPI>()) {
+                store_gated_grad<is_gelu_gate<EPI>()>(p, row0, col0, acc);
+            } else if (EPI == kEpiWgrad) {
                 store_wgrad(p, ge.out_index, row0, col0, acc);
             } else if (EPI == kEpiNone || EPI == kEpiBias || EPI == kEpiBiasGelu) {
                 store_fprop<EPI>(p, row0, col0, acc);
@@ -1309,7 +1472,7 @@ int launch_gemm_impl(const TensorMaps& maps, const GemmParams& p, cudaStream_t s
     int dev = 0;
     if (configure_gemm<EPI, 1>(&dev) != 0) return -3;
     auto kern = gemm_fp8_kernel<EPI, 1>;
-    if (is_linear<EPI>())
+    if (is_dependent<EPI>())
         return launch_dependent(kern, static_cast<unsigned>(grid), kThreads, smem_bytes<EPI>(), stream, maps, p) ==
                        cudaSuccess
                    ? 0

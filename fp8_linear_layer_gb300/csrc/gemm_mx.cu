@@ -152,7 +152,7 @@ __global__ void __cluster_dims__(2 * SPLIT, 1, 1) __launch_bounds__(kThreads, 1)
     cluster_sync();
     tc_fence_after();
     const uint32_t tmem_base = sm.tmem_base;
-    if (is_linear<EPI>()) {
+    if (is_dependent<EPI>()) {
         await_dependency();
         release_dependents();
     }
@@ -175,7 +175,8 @@ __global__ void __cluster_dims__(2 * SPLIT, 1, 1) __launch_bounds__(kThreads, 1)
                     int mt, nt;
                     decode_mx_tile(p, t, mt, nt);
                     const int m0 = mt * kMxRows + static_cast<int>(rank) * kBM;
-                    const int nb0 = nt * kBN + static_cast<int>(rank) * kMxBRows;
+                    // gated: the leader loads the gate's rows, its peer the up projection's
+                    const int nb0 = nt * tile_cols<EPI>() + static_cast<int>(rank) * (is_gated<EPI>() ? p.N : kMxBRows);
                     for (int kb = 0; kb < nkb; ++kb) {
                         if (!mbar_wait(smem_addr(&sm.empty[s]), ph ^ 1u, budget)) {
                             ok = false;
@@ -187,11 +188,15 @@ __global__ void __cluster_dims__(2 * SPLIT, 1, 1) __launch_bounds__(kThreads, 1)
                         tma_load_2d_pair(smem_addr(sm.a[s]), &maps.a, fbl, (kb_first + kb) * kBK, m0);
                         tma_load_2d_pair(smem_addr(sm.b[s]), &maps.b, fbl, (kb_first + kb) * kBK, nb0);
                         // scale atoms: rows of 128 words; A's atom of this CTA's 128-row group,
-                        // both atoms of the tile's 256 rows of B
+                        // both atoms of the tile's 256 rows of B (gated: one of each projection)
                         tma_load_2d_pair(smem_addr(sm.sfa[s]), &maps.sa, fbl, 0,
                                          static_cast<int32_t>((kb_first + kb) * p.sfa_groups + 2 * mt + static_cast<int>(rank)));
                         tma_load_2d_pair(smem_addr(sm.sfb[s]), &maps.sb, fbl, 0,
-                                         static_cast<int32_t>((kb_first + kb) * p.sfb_groups + 2 * nt));
+                                         static_cast<int32_t>((kb_first + kb) * p.sfb_groups +
+                                                              (is_gated<EPI>() ? nt : 2 * nt)));
+                        if (is_gated<EPI>())
+                            tma_load_2d_pair(smem_addr(sm.sfb[s] + 512), &maps.sb, fbl, 0,
+                                             static_cast<int32_t>((kb_first + kb) * p.sfb_groups + p.N / kGatedN + nt));
                         ++n_issued;
                         ring_advance<kMxStages>(s, ph);
                     }
@@ -309,7 +314,10 @@ __global__ void __cluster_dims__(2 * SPLIT, 1, 1) __launch_bounds__(kThreads, 1)
         for (int t = pair; t < p.total_tiles && ok; t += num_pairs) {  // SPLIT 2: one tile per cluster
             int mt, nt;
             decode_mx_tile(p, t, mt, nt);
-            const int m0 = mt * kMxRows + static_cast<int>(rank) * kBM, n0 = nt * kBN;
+            const int m0 = mt * kMxRows + static_cast<int>(rank) * kBM, n0 = nt * tile_cols<EPI>();
+            constexpr int kGroupN = tile_cols<EPI>() / kEpiGroups;  // output columns of a warpgroup
+            if (is_gated_grad<EPI>())
+                prefetch_gates(p, m0 + q * 32 + g8 + 8 * cq, n0 + half * kHalfN);
             if (is_linear<EPI>())
                 prefetch_residual(p, m0 + q * 32 + g8 + 8 * cq, n0 + half * kHalfN);
             if (EPI == kEpiDgelu || EPI == kEpiDgeluBgrad) {
@@ -327,11 +335,12 @@ __global__ void __cluster_dims__(2 * SPLIT, 1, 1) __launch_bounds__(kThreads, 1)
             if (!ok) break;
             tc_fence_after();
             uint64_t acc[4 * kChunks];
-            const uint32_t tq = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(half * kHalfN);
+            const uint32_t tq = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(half * kGroupN);
 #pragma unroll
             for (int h = 0; h < 4; ++h) {
                 uint64_t plo[8], phi[8];
-                tmem_ld_16x256b_x4_pairs2(tq + 32u * h, tq + (16u << 16) + 32u * h, plo, phi);
+                const uint32_t tcol = 32u * h + (h >= 2 ? gate_skip<EPI>() : 0);
+                tmem_ld_16x256b_x4_pairs2(tq + tcol, tq + (16u << 16) + tcol, plo, phi);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int c = 4 * h + i;
@@ -357,8 +366,12 @@ __global__ void __cluster_dims__(2 * SPLIT, 1, 1) __launch_bounds__(kThreads, 1)
             // only rows outside the matrix and stores nothing
             if (m0 >= p.M) continue;
             const int row0 = m0 + q * 32 + g8 + 16 * part;
-            const int col0 = n0 + half * kHalfN + 2 * cq;
-            if (EPI == kEpiWgrad) {
+            const int col0 = n0 + half * kGroupN + 2 * cq;
+            if (is_gated<EPI>()) {
+                store_gated<is_gelu_gate<EPI>(), 4 / SPLIT>(p, row0, col0, acc);
+            } else if (is_gated_grad<EPI>()) {
+                store_gated_grad<is_gelu_gate<EPI>(), 4 / SPLIT>(p, row0, col0, acc);
+            } else if (EPI == kEpiWgrad) {
                 store_wgrad(p, 0, row0, col0, acc);
             } else if (EPI == kEpiNone || EPI == kEpiBias || EPI == kEpiBiasGelu) {
                 store_fprop<EPI>(p, row0, col0, acc);
@@ -435,7 +448,7 @@ int launch_mx_impl(const TensorMaps& maps, const GemmParams& p, cudaStream_t str
     // one tile per cluster where its K blocks are split
     const int64_t clusters = SPLIT == 2 || p.total_tiles < slots ? p.total_tiles : slots;
     const unsigned grid = static_cast<unsigned>(2 * SPLIT * clusters);
-    if (is_linear<EPI>())
+    if (is_dependent<EPI>())
         return launch_dependent(gemm_mx_kernel<EPI, SPLIT>, grid, kThreads, kMxSmemBytes<EPI>, stream, maps, p) == cudaSuccess ? 0 : -3;
     gemm_mx_kernel<EPI, SPLIT><<<grid, kThreads, kMxSmemBytes<EPI>, stream>>>(maps, p);
     return cudaGetLastError() == cudaSuccess ? 0 : -3;
@@ -453,6 +466,10 @@ int launch_gemm_mx_split(const TensorMaps& maps, const GemmParams& p, int epi, c
         case kEpiLinearGeluAny: return launch_mx_impl<kEpiLinearGeluAny, 2>(maps, p, stream);
         case kEpiLinearOdd: return launch_mx_impl<kEpiLinearOdd, 2>(maps, p, stream);
         case kEpiLinearGeluOdd: return launch_mx_impl<kEpiLinearGeluOdd, 2>(maps, p, stream);
+        case kEpiGatedSilu: return launch_mx_impl<kEpiGatedSilu, 2>(maps, p, stream);
+        case kEpiGatedGelu: return launch_mx_impl<kEpiGatedGelu, 2>(maps, p, stream);
+        case kEpiGatedSiluGrad: return launch_mx_impl<kEpiGatedSiluGrad, 2>(maps, p, stream);
+        case kEpiGatedGeluGrad: return launch_mx_impl<kEpiGatedGeluGrad, 2>(maps, p, stream);
         default: return -3;
     }
 }
@@ -471,6 +488,10 @@ int launch_gemm_mx(const TensorMaps& maps, const GemmParams& p, int epi, cudaStr
         case kEpiLinearGeluAny: return launch_mx_impl<kEpiLinearGeluAny>(maps, p, stream);
         case kEpiLinearOdd: return launch_mx_impl<kEpiLinearOdd>(maps, p, stream);
         case kEpiLinearGeluOdd: return launch_mx_impl<kEpiLinearGeluOdd>(maps, p, stream);
+        case kEpiGatedSilu: return launch_mx_impl<kEpiGatedSilu>(maps, p, stream);
+        case kEpiGatedGelu: return launch_mx_impl<kEpiGatedGelu>(maps, p, stream);
+        case kEpiGatedSiluGrad: return launch_mx_impl<kEpiGatedSiluGrad>(maps, p, stream);
+        case kEpiGatedGeluGrad: return launch_mx_impl<kEpiGatedGeluGrad>(maps, p, stream);
         default: return -3;
     }
 }

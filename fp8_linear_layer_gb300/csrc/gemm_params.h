@@ -9,6 +9,7 @@ namespace fp8ll {
 constexpr int kMaxGroups = 256;
 constexpr int kTileM = 128;  // GEMM output tile rows
 constexpr int kTileN = 256;  // GEMM output tile columns
+constexpr int kGatedN = 128;  // of which the gated product makes this many outputs
 
 enum EpiKind : int {
     kEpiNone = 0,
@@ -25,6 +26,13 @@ enum EpiKind : int {
     kEpiLinearGeluAny = 10,
     kEpiLinearOdd = 11,   // the same for an odd N (CTA pairs)
     kEpiLinearGeluOdd = 12,
+    // Z = C + bias, C of the gate's rows of B and, p.N rows on, of the up projection's;
+    // Y = act(Z_gate) Z_up, aux = Z [M][2 N]
+    kEpiGatedSilu = 13,
+    kEpiGatedGelu = 14,
+    // dZ [M][2 N] = (C Z_up act'(Z_gate), C act(Z_gate)), aux = Z
+    kEpiGatedSiluGrad = 15,
+    kEpiGatedGeluGrad = 16,
 };
 
 // One schedulable group of output tiles: all tiles of a group share the same

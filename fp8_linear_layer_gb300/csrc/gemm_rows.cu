@@ -26,6 +26,10 @@
 //               of B per thread, all tokens; otherwise read the accumulator
 //               once at the end.
 //   all warps   epilogue: a thread takes two neighbouring features.
+// GATED: the 128 rows of B are 64 of the gate and the same 64 of the up projection,
+// so that a CTA holds both sums of an output.  MXFP8: their scales come from halves
+// of two atoms, which warp 3 puts together as a stage lands (a copy to tensor memory
+// takes whole atoms, and a TMA box no eight bytes).
 #include <atomic>
 #include <cuda_runtime.h>
 
@@ -50,13 +54,18 @@ constexpr int rows_ctas_per_sm() {
     return NT == 128 ? 1 : 2;
 }
 
-template <int NT>
+constexpr int kGateRows = kRowsFeatures / 2;  // GATED: output features of a tile
+
+// RAW: room for the two projections' scale atoms
+template <int NT, bool RAW>
 struct __align__(1024) RowsSmem {
     static constexpr int S = rows_stages<NT>();
     uint8_t w[S][kRowsFeatures * 128];
     uint8_t x[S][NT * 128];
     float sw[S][128];  // 1x128: scales of the block's rows; MXFP8: a 512-byte scale atom
     float sx[S][128];
+    float raw[RAW ? S : 1][RAW ? 256 : 4];
+    uint64_t sf_ready[S];  // RAW: stage s's atom is put together
     uint64_t full[S];
     uint64_t empty[S];
     uint64_t acc_full[kRowsAcc];
@@ -65,13 +74,13 @@ struct __align__(1024) RowsSmem {
     uint32_t tmem_base;
     int32_t failed;
 };
-template <int NT>
+template <int NT, bool RAW = false>
 constexpr size_t rows_smem_bytes() {
-    return sizeof(RowsSmem<NT>) + 1024;
+    return sizeof(RowsSmem<NT, RAW>) + 1024;
 }
 // two CTAs per SM; the sums [NT][128] take the place of the weights' stages
-static_assert(2 * (rows_smem_bytes<16>() + 1024) <= 233472 && 2 * (rows_smem_bytes<64>() + 1024) <= 233472 &&
-                  rows_smem_bytes<128>() <= 232448,
+static_assert(2 * (rows_smem_bytes<16, true>() + 1024) <= 233472 && 2 * (rows_smem_bytes<32, true>() + 1024) <= 233472 &&
+                  2 * (rows_smem_bytes<64, true>() + 1024) <= 233472 && rows_smem_bytes<128, true>() <= 232448,
               "two CTAs per SM, one at 128 tokens");
 static_assert(64 * kRowsFeatures * 4 <= rows_stages<64>() * kRowsFeatures * 128 &&
                   128 * kRowsFeatures * 4 <= rows_stages<128>() * kRowsFeatures * 128,
@@ -140,10 +149,11 @@ __device__ __forceinline__ void store_pair(uint16_t* p, int64_t off, bool one, b
     if (two) p[off + 1] = static_cast<uint16_t>(w >> 16);
 }
 
-template <int RECIPE, int NT>
+template <int RECIPE, int NT, bool GATED>
 __global__ void __launch_bounds__(kRowsThreads, rows_ctas_per_sm<NT>())
     gemm_rows_kernel(const __grid_constant__ RowsMaps maps, const __grid_constant__ RowsParams p) {
-    using Smem = RowsSmem<NT>;
+    constexpr bool RAW = GATED && RECIPE == kRecipeMx;
+    using Smem = RowsSmem<NT, RAW>;
     constexpr int S = Smem::S;
     extern __shared__ uint8_t smem_raw[];
     Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -153,7 +163,8 @@ __global__ void __launch_bounds__(kRowsThreads, rows_ctas_per_sm<NT>())
     const int cs = p.cluster;
     const int rank = static_cast<int>(blockIdx.x) % cs;
     const int64_t tile = blockIdx.x / cs;
-    const int64_t n0 = tile * kRowsFeatures;
+    constexpr int kFeatures = GATED ? kGateRows : kRowsFeatures;
+    const int64_t n0 = tile * kFeatures;
     const int m0 = static_cast<int>(blockIdx.y) * NT;  // a multiple of 128 where it is not 0
     const int kb0 = static_cast<int>(static_cast<int64_t>(p.nkb) * rank / cs);
     const int kb1 = static_cast<int>(static_cast<int64_t>(p.nkb) * (rank + 1) / cs);
@@ -161,6 +172,7 @@ __global__ void __launch_bounds__(kRowsThreads, rows_ctas_per_sm<NT>())
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
+            if (RAW) mbar_init(smem_addr(&sm.sf_ready[s]), 1);
             mbar_init(smem_addr(&sm.full[s]), 1);
             mbar_init(smem_addr(&sm.empty[s]), RECIPE == kRecipeBlock ? 5 : 1);  // the MMAs, and the scales' readers
         }
@@ -194,15 +206,27 @@ __global__ void __launch_bounds__(kRowsThreads, rows_ctas_per_sm<NT>())
                 if (!ok) break;
                 const uint32_t bar = smem_addr(&sm.full[s]);
                 mbar_arrive_expect_tx(bar, (kRowsFeatures + NT) * 128 + (RECIPE == kRecipeBlock  ? 512 + NT * 4
+                                                                         : RAW                 ? 1536
                                                                          : RECIPE == kRecipeMx ? 1024
                                                                                                : 0));
                 tma_load_2d(smem_addr(sm.w[s]), &maps.w, bar, kb * 128, static_cast<int32_t>(n0));
+                if (GATED)
+                    tma_load_2d(smem_addr(sm.w[s] + kGateRows * 128), &maps.w, bar, kb * 128,
+                                static_cast<int32_t>(p.N + n0));
                 tma_load_2d(smem_addr(sm.x[s]), &maps.x, bar, kb * 128, m0);
                 if (RECIPE == kRecipeBlock) {
                     tma_load_2d(smem_addr(sm.sw[s]), &maps.sw, bar, static_cast<int32_t>(n0), kb);
+                    if (GATED)
+                        tma_load_2d(smem_addr(sm.sw[s] + kGateRows), &maps.sw, bar, static_cast<int32_t>(p.N + n0), kb);
                     tma_load_2d(smem_addr(sm.sx[s]), &maps.sx, bar, m0, kb);
                 } else if (RECIPE == kRecipeMx) {
-                    tma_load_2d(smem_addr(sm.sw[s]), &maps.sw, bar, 0, static_cast<int32_t>(kb * p.groups_w + tile));
+                    if (RAW) {
+                        const int32_t atom = static_cast<int32_t>(kb * p.groups_w + tile / 2);
+                        tma_load_2d(smem_addr(sm.raw[RAW ? s : 0]), &maps.sw, bar, 0, atom);
+                        tma_load_2d(smem_addr(sm.raw[RAW ? s : 0] + 128), &maps.sw, bar, 0, atom + p.N / 128);
+                    } else {
+                        tma_load_2d(smem_addr(sm.sw[s]), &maps.sw, bar, 0, static_cast<int32_t>(kb * p.groups_w + tile));
+                    }
                     tma_load_2d(smem_addr(sm.sx[s]), &maps.sx, bar, 0, 
                                 static_cast<int32_t>(kb * p.groups_x + m0 / 128));
                 }
@@ -230,6 +254,7 @@ __global__ void __launch_bounds__(kRowsThreads, rows_ctas_per_sm<NT>())
         for (int kb = kb0; kb < kb1; ++kb) {
             if (RECIPE == kRecipeBlock) ok = mbar_wait_warp(smem_addr(&sm.acc_empty[ab]), aph ^ 1u, budget);
             if (ok) ok = mbar_wait_warp(smem_addr(&sm.full[s]), ph, budget);
+            if (RAW && ok) ok = mbar_wait_warp(smem_addr(&sm.sf_ready[s]), ph, budget);
             if (!ok) break;
             tc_fence_after();
             if (lane == 0) {
@@ -267,6 +292,27 @@ __global__ void __launch_bounds__(kRowsThreads, rows_ctas_per_sm<NT>())
         if (lane == 0) mma_commit(smem_addr(&sm.drain));
         __syncwarp();
         if (!mbar_wait_warp(smem_addr(&sm.drain), 0, budget)) ok = false;
+    } else if (RAW && warp == 3) {
+        // a row of an atom is 16 bytes, one word for each 32 rows of the operand: this
+        // tile's 64 rows are words 0 and 1 of both atoms, or 2 and 3
+        const int first = 2 * static_cast<int>(tile & 1);
+        int s = 0;
+        uint32_t ph = 0;
+        for (int kb = kb0; kb < kb1; ++kb) {
+            ok = mbar_wait_warp(smem_addr(&sm.full[s]), ph, budget);
+            if (!ok) break;
+            const float* raw = sm.raw[RAW ? s : 0] + 4 * lane + first;
+            const float2 gate = *reinterpret_cast<const float2*>(raw), up = *reinterpret_cast<const float2*>(raw + 128);
+            *reinterpret_cast<float4*>(sm.sw[s] + 4 * lane) = make_float4(gate.x, gate.y, up.x, up.y);
+            // read by the copy to tensor memory, and the raw atoms are refilled by TMA
+            fence_proxy_async_smem();
+            __syncwarp();
+            mbar_arrive_lane0(smem_addr(&sm.sf_ready[s]), lane);
+            if (++s == S) {
+                s = 0;
+                ph ^= 1u;
+            }
+        }
     } else if (warp >= 4) {
         const int q = warp & 3;
         const uint32_t tq = tmem + (static_cast<uint32_t>(q * 32) << 16);
@@ -345,6 +391,69 @@ __global__ void __launch_bounds__(kRowsThreads, rows_ctas_per_sm<NT>())
                      : "r"(mapa_shared(smem_addr(&sm.failed), static_cast<uint32_t>(r))));
         write = write && f == 0u;
     }
+    if (GATED) {
+        // a thread takes two neighbouring features, both projections, and every (8 cs)-th
+        // token, two tokens at a time so that their loads overlap
+        const int nl = 2 * (threadIdx.x & 31);
+        const int64_t n = n0 + nl;
+        if (write) {
+            const uint32_t bg = p.bias ? *reinterpret_cast<const uint32_t*>(p.bias + n) : 0u;
+            const uint32_t bu = p.bias ? *reinterpret_cast<const uint32_t*>(p.bias + p.N + n) : 0u;
+            const float scale = RECIPE == kRecipeTensor ? __fmul_rn(*p.tsx, *p.tsw) : 1.0f;
+            const int rows = p.M - m0 < NT ? p.M - m0 : NT;
+            constexpr int U = 2;
+            for (int i0 = 8 * rank + warp; i0 < rows; i0 += 8 * U * cs) {
+                float2 v[U][2][8];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int i = i0 + 8 * u * cs;
+                    if (i >= rows) continue;
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        const float* own = &sums[i][nl + kGateRows * b];
+                        if (cs == 1) {
+                            v[u][b][0] = *reinterpret_cast<const float2*>(own);
+                        } else {
+                            const uint32_t a = smem_addr(own);
+#pragma unroll
+                            for (int r = 0; r < 8; ++r)
+                                if (r < cs) v[u][b][r] = ld_cluster_f32x2(mapa_shared(a, static_cast<uint32_t>(r)));
+                        }
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int i = i0 + 8 * u * cs;
+                    if (i >= rows) continue;
+                    float2 z[2];
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        z[b] = v[u][b][0];
+#pragma unroll
+                        for (int r = 1; r < 8; ++r) {
+                            if (r < cs) {
+                                z[b].x = __fadd_rn(z[b].x, v[u][b][r].x);
+                                z[b].y = __fadd_rn(z[b].y, v[u][b][r].y);
+                            }
+                        }
+                        if (RECIPE == kRecipeTensor) z[b] = make_float2(__fmul_rn(z[b].x, scale), __fmul_rn(z[b].y, scale));
+                        const uint32_t bias = b ? bu : bg;
+                        z[b] = make_float2(__fadd_rn(z[b].x, bf16_lo(bias)), __fadd_rn(z[b].y, bf16_hi(bias)));
+                    }
+                    const float2 a = p.gelu ? gate2<true>(z[0].x, z[0].y) : gate2<false>(z[0].x, z[0].y);
+                    const int64_t row = m0 + i;
+                    *reinterpret_cast<uint32_t*>(p.out + row * p.N + n) = pack_bf16x2(a.x * z[1].x, a.y * z[1].y);
+                    if (p.aux) {
+                        uint16_t* aux = p.aux + 2 * row * p.N + n;
+                        *reinterpret_cast<uint32_t*>(aux) = pack_bf16x2(z[0].x, z[0].y);
+                        *reinterpret_cast<uint32_t*>(aux + p.N) = pack_bf16x2(z[1].x, z[1].y);
+                    }
+                }
+            }
+        }
+        if (cs > 1) cluster_sync();  // the peers have read this CTA's sums
+        return;
+    }
     // a thread takes two neighbouring features and every (4 cs)-th token, four
     // tokens at a time so that their loads overlap
     const int nl = 2 * (threadIdx.x & 63);
@@ -405,26 +514,28 @@ __global__ void __launch_bounds__(kRowsThreads, rows_ctas_per_sm<NT>())
     if (cs > 1) cluster_sync();  // the peers have read this CTA's sums
 }
 
-template <int RECIPE, int NT>
+template <int RECIPE, int NT, bool GATED>
 int launch_rows_impl(const RowsMaps& maps, const RowsParams& p, cudaStream_t stream) {
-    auto kern = gemm_rows_kernel<RECIPE, NT>;
+    auto kern = gemm_rows_kernel<RECIPE, NT, GATED>;
+    constexpr size_t smem = rows_smem_bytes<NT, GATED && RECIPE == kRecipeMx>();
     static PerDevice allowed;
-    if (allow_shared_memory(allowed, kern, rows_smem_bytes<NT>()) != 0) return -3;
-    const int64_t tiles = (static_cast<int64_t>(p.N) + kRowsFeatures - 1) / kRowsFeatures;
+    if (allow_shared_memory(allowed, kern, smem) != 0) return -3;
+    constexpr int features = GATED ? kGateRows : kRowsFeatures;
+    const int64_t tiles = (static_cast<int64_t>(p.N) + features - 1) / features;
     const dim3 grid(static_cast<unsigned>(tiles * p.cluster), static_cast<unsigned>((p.M + NT - 1) / NT));
-    return launch_dependent_clusters(kern, grid, static_cast<unsigned>(p.cluster), kRowsThreads, rows_smem_bytes<NT>(),
-                                     stream, maps, p) == cudaSuccess
+    return launch_dependent_clusters(kern, grid, static_cast<unsigned>(p.cluster), kRowsThreads, smem, stream, maps,
+                                     p) == cudaSuccess
                ? 0
                : -3;
 }
 
-template <int RECIPE>
+template <int RECIPE, bool GATED>
 int launch_rows_recipe(const RowsMaps& maps, const RowsParams& p, cudaStream_t stream) {
     switch (rows_tokens(p.M)) {
-        case 16: return launch_rows_impl<RECIPE, 16>(maps, p, stream);
-        case 32: return launch_rows_impl<RECIPE, 32>(maps, p, stream);
-        case 64: return launch_rows_impl<RECIPE, 64>(maps, p, stream);
-        default: return launch_rows_impl<RECIPE, 128>(maps, p, stream);
+        case 16: return launch_rows_impl<RECIPE, 16, GATED>(maps, p, stream);
+        case 32: return launch_rows_impl<RECIPE, 32, GATED>(maps, p, stream);
+        case 64: return launch_rows_impl<RECIPE, 64, GATED>(maps, p, stream);
+        default: return launch_rows_impl<RECIPE, 128, GATED>(maps, p, stream);
     }
 }
 
@@ -440,7 +551,7 @@ static int rows_slots(int c) {
     std::atomic<int>& slot = known[dev][c == 2 ? 0 : c == 4 ? 1 : 2];
     int n = slot.load(std::memory_order_relaxed);
     if (n == 0) {
-        auto kern = gemm_rows_kernel<kRecipeBlock, NT>;
+        auto kern = gemm_rows_kernel<kRecipeBlock, NT, false>;
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  static_cast<int>(rows_smem_bytes<NT>())) != cudaSuccess)
             return 0;
@@ -492,13 +603,22 @@ int rows_cluster(int64_t M, int64_t N, int64_t nkb) {
     return c;
 }
 
-int launch_gemm_rows(const RowsMaps& maps, RowsParams p, int recipe, cudaStream_t stream) {
-    p.cluster = rows_cluster(p.M, p.N, p.nkb);
+template <bool GATED>
+static int launch_rows(const RowsMaps& maps, RowsParams p, int recipe, cudaStream_t stream) {
+    p.cluster = rows_cluster(p.M, (GATED ? 2LL : 1LL) * p.N, p.nkb);  // of as many tiles of B
     switch (recipe) {
-        case kRecipeBlock: return launch_rows_recipe<kRecipeBlock>(maps, p, stream);
-        case kRecipeMx: return launch_rows_recipe<kRecipeMx>(maps, p, stream);
-        default: return launch_rows_recipe<kRecipeTensor>(maps, p, stream);
+        case kRecipeBlock: return launch_rows_recipe<kRecipeBlock, GATED>(maps, p, stream);
+        case kRecipeMx: return launch_rows_recipe<kRecipeMx, GATED>(maps, p, stream);
+        default: return launch_rows_recipe<kRecipeTensor, GATED>(maps, p, stream);
     }
+}
+
+int launch_gemm_rows(const RowsMaps& maps, RowsParams p, int recipe, cudaStream_t stream) {
+    return launch_rows<false>(maps, p, recipe, stream);
+}
+
+int launch_gemm_rows_gated(const RowsMaps& maps, RowsParams p, int recipe, cudaStream_t stream) {
+    return launch_rows<true>(maps, p, recipe, stream);
 }
 
 }  // namespace fp8ll

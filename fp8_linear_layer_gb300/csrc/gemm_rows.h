@@ -36,15 +36,15 @@ inline bool rows_kernel_taken(int64_t M, int64_t N, int64_t K, int recipe) {
 }
 
 struct RowsMaps {
-    CUtensorMap w, x;    // codes: boxes of 128 rows of B, of rows_tokens(M) rows of A, 128 bytes each
+    CUtensorMap w, x;    // codes: boxes of 128 (gated: 64) rows of B, of rows_tokens(M) rows of A, 128 bytes each
     CUtensorMap sw, sx;  // 1x128: their scales, one K block; MXFP8: one 512-byte scale atom
 };
 
 struct RowsParams {
-    int32_t M, N, nkb;
+    int32_t M, N, nkb;      // N: output columns; gated: B has 2 N rows, the gate's first
     int32_t cluster;        // CTAs that share the K blocks of an output tile (set by the launcher)
     uint32_t idesc;         // tcgen05 instruction descriptor without the MMA's N
-    int32_t gelu;
+    int32_t gelu;           // gated: else SiLU
     int32_t debug_starve;   // test hook: the producer issues no loads
     uint64_t budget_ns;     // wall-clock budget of each pipeline wait
     int* status;
@@ -55,9 +55,12 @@ struct RowsParams {
     const uint16_t* res;    // bf16 [M][ldr] or null
     int64_t ldr;
     uint16_t* out;          // bf16 [M][N]
-    uint16_t* aux;          // bf16 [M][N] or null
+    uint16_t* aux;          // bf16 [M][N] (gated: [M][2 N]) or null
 };
 
+// The gated product Y = act(Z_gate) Z_up for few rows: an output tile takes 64 rows
+// of B from each projection.  N % 128 == 0.
+int launch_gemm_rows_gated(const RowsMaps& maps, RowsParams p, int recipe, cudaStream_t stream);
 int launch_gemm_rows(const RowsMaps& maps, RowsParams p, int recipe, cudaStream_t stream);
 
 }  // namespace fp8ll

@@ -56,6 +56,9 @@ bool launch_gemm_mx_splits(const GemmParams& p);
 bool launch_gemm_tensor_splits(const GemmParams& p);
 int launch_gemm_mx_split(const TensorMaps& maps, const GemmParams& p, int epi, cudaStream_t stream);
 int launch_gemm_tensor_split(const TensorMaps& maps, const GemmParams& p, int epi, cudaStream_t stream);
+// The gated product and its data gradient (kEpiGated*), whole and, where K is
+// split, as launch_gemm_linear_parts.
+int launch_gemm_gated(const TensorMaps& maps, const GemmParams& p, int epi, int parts, cudaStream_t stream, int grid);
 int launch_bgrad_finalize(const float* ws, int64_t num_bands, int64_t N, float* bgrad, cudaStream_t stream,
                           int num_sms);
 

@@ -17,6 +17,8 @@
  *   fp8_grouped_wgrad   per-group fp32 out_g (+)= A_g B_g^T, groups along K
  *   fp8_bgrad_from_operand  bias gradient as row sums of a 1x128-scaled operand
  *   fp8_gemm_linear     Y = act(A B^T + bias) + residual (also few rows)
+ *   fp8_gemm_gated      Y = act(A Bg^T + bg) (A Bu^T + bu) in one kernel, and the
+ *   fp8_gemm_gated_dgrad  data gradient through both factors
  *   fp8_rmsnorm_*, fp8_layernorm_*  RMS and layer norm with the residual's addition
  *                       and an fp8 output, and their backward passes
  *   fp8_dropout         dropout from a counter-based generator, added to a residual
@@ -416,8 +418,9 @@ int fp8_tensor_gemm_wgrad(int64_t M, int64_t N, int64_t K, const fp8ll_tensor_op
                           const fp8ll_tensor_operand_t* B, float* out, int accumulate, fp8ll_stream_t stream);
 
 /* ---- the residual block around the layer ----------------------------------
- * Activations of fp8_gemm_linear: none, or the tanh GELU above. */
-enum { FP8LL_ACT_NONE = 0, FP8LL_ACT_GELU = 1 };
+ * Activations of fp8_gemm_linear: none, or the tanh GELU above; of
+ * fp8_gemm_gated: that GELU, or silu(z) = z / (1 + e^-z). */
+enum { FP8LL_ACT_NONE = 0, FP8LL_ACT_GELU = 1, FP8LL_ACT_SILU = 2 };
 
 /* Types of fp8ll_grad_t. */
 enum { FP8LL_F32 = 0, FP8LL_BF16 = 1 };
@@ -445,6 +448,43 @@ int fp8_mx_gemm_linear(int64_t M, int64_t N, int64_t K, const fp8ll_mx_operand_t
 int fp8_tensor_gemm_linear(int64_t M, int64_t N, int64_t K, const fp8ll_tensor_operand_t* A,
                            const fp8ll_tensor_operand_t* B, const void* bias_bf16, int act, const void* residual_bf16,
                            int64_t ldr, void* out_bf16, void* aux_bf16, fp8ll_stream_t stream);
+
+/* Gated product of a feed-forward block, both projections in one kernel:
+ *   Z = A B^T + bias  (fp32, [M][2 N]);  Y[i][j] = act(Z[i][j]) * Z[i][N + j]
+ * rounded once to bf16.
+ *   A: M x K operand.  B: 2 N x K operand, the gate's N rows first, then the up
+ *   projection's: one operand, cast as one matrix, whose weight and bias gradients
+ *   are one matrix's too.  N % 128 == 0 (the product that follows contracts over
+ *   it); M, K, acc_mode as fp8_gemm_linear.
+ *   bias_bf16: [2 N], 16-byte aligned, or NULL.  act: FP8LL_ACT_SILU or _GELU.
+ *   out_bf16:  [M][N]; aux_bf16: [M][2 N] receives Z for the backward pass, or NULL;
+ *              both contiguous and 16-byte aligned, apart from each other and the bias.
+ * Few rows, or few output tiles, run a kernel that splits K, as in fp8_gemm_linear. */
+int fp8_gemm_gated(int64_t M, int64_t N, int64_t K, const fp8ll_operand_t* A, const fp8ll_operand_t* B,
+                   const void* bias_bf16, int act, int acc_mode, void* out_bf16, void* aux_bf16,
+                   fp8ll_stream_t stream);
+int fp8_mx_gemm_gated(int64_t M, int64_t N, int64_t K, const fp8ll_mx_operand_t* A, const fp8ll_mx_operand_t* B,
+                      const void* bias_bf16, int act, void* out_bf16, void* aux_bf16, fp8ll_stream_t stream);
+int fp8_tensor_gemm_gated(int64_t M, int64_t N, int64_t K, const fp8ll_tensor_operand_t* A,
+                          const fp8ll_tensor_operand_t* B, const void* bias_bf16, int act, void* out_bf16,
+                          void* aux_bf16, fp8ll_stream_t stream);
+
+/* The gradient of Z through the gate, in the epilogue of the product that makes the
+ * gradient of Y:
+ *   C = A B^T  (A: M x K, the gradient behind the block's second product; B: N x K,
+ *              that product's weight transposed)
+ *   dZ[i][j] = C[i][j] Z[i][N + j] act'(Z[i][j]),  dZ[i][N + j] = C[i][j] act(Z[i][j])
+ * rounded once to bf16.  aux_bf16: Z [M][2 N] as fp8_gemm_gated left it.  out_bf16:
+ * dZ [M][2 N], Z's own buffer or apart from it; both 16-byte aligned.  N % 128 == 0.
+ * The gradients of A, of B and of the bias of fp8_gemm_gated are those of one product
+ * with 2 N features: fp8_gemm_linear(dZ, B^T), fp8_gemm_wgrad, fp8_quantize_dbias. */
+int fp8_gemm_gated_dgrad(int64_t M, int64_t N, int64_t K, const fp8ll_operand_t* A, const fp8ll_operand_t* B,
+                         const void* aux_bf16, int act, int acc_mode, void* out_bf16, fp8ll_stream_t stream);
+int fp8_mx_gemm_gated_dgrad(int64_t M, int64_t N, int64_t K, const fp8ll_mx_operand_t* A, const fp8ll_mx_operand_t* B,
+                            const void* aux_bf16, int act, void* out_bf16, fp8ll_stream_t stream);
+int fp8_tensor_gemm_gated_dgrad(int64_t M, int64_t N, int64_t K, const fp8ll_tensor_operand_t* A,
+                                const fp8ll_tensor_operand_t* B, const void* aux_bf16, int act, void* out_bf16,
+                                fp8ll_stream_t stream);
 
 /* Root-mean-square norm of a residual stream, cast to fp8 for the GEMMs:
  *   h = bf16(x + residual)               (h = x without a residual)
