@@ -70,49 +70,49 @@ __device__ __forceinline__ float2 dgelu_tanh2(float z0, float z1) {
     return unpack_f32x2(fma_f32x2(mul_f32x2(v, sp), sm, sp));
 }
 
-// The gates' activations y and their derivatives d, with the same intrinsics:
-//   y = z / (1 + e^-x),  d = sp + v sp sm,  sp = s(x), sm = s(-x) = e^-x sp
-// with x = v = z for SiLU and the x and v above for GELU.  x is clamped to +-88: e^88
-// is finite, and the approximate divide by anything above 2^126 (x < -87.4) gives 0,
-// which is the limit of both.  z is clamped to +-64 in v, where its factor sp sm is
-// 0 already, so that v stays finite for any z.  A NaN stays one.
-__device__ __forceinline__ float clamp_88(float x) {
-    float r;
-    asm("{\n\t.reg .f32 t;\n\tmax.NaN.f32 t, %1, %2;\n\tmin.NaN.f32 %0, t, %3;\n\t}"
-        : "=f"(r)
-        : "f"(x), "f"(-88.0f), "f"(88.0f));
+// The gates' activations y and their derivatives d:
+//   y = z s(x),  d = s(x) (1 + v (1 - s(x))),  s(x) = 1 / (1 + e^-x)
+// with x = v = z for SiLU and the x and v above for GELU.  The approximate
+// exponential (2 + 1.17 |x| ulp) and reciprocal (1 ulp) flush subnormals: where e^-x
+// is infinite or its reciprocal would be subnormal (x < -87.3), s is 0, which is the
+// limit of both, and nothing has to be clamped but GELU's v, to stay finite where its
+// factor s (1 - s) is 0 already (|z| > 64).  1 - s is rounded to 2^-24, next to a 1.
+// One exponential and one reciprocal per element and few other instructions: they
+// are what the gradient's epilogue is made of.
+__device__ __forceinline__ float logistic(float x) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
     return r;
 }
 
+// s(x) of a pair
 template <bool GELU>
-__device__ __forceinline__ float2 gate_exp2(float z0, float z1) {
-    float2 x = make_float2(z0, z1);
-    if (GELU) {
-        uint64_t z2;
-        x = unpack_f32x2(gelu_arg2(pack_f32x2(z0, z1), z2));
-    }
-    return make_float2(__expf(-clamp_88(x.x)), __expf(-clamp_88(x.y)));
+__device__ __forceinline__ uint64_t gate_logistic2(uint64_t z) {
+    uint64_t z2;
+    const float2 x = unpack_f32x2(GELU ? gelu_arg2(z, z2) : z);
+    return pack_f32x2(logistic(x.x), logistic(x.y));
 }
 
 template <bool GELU>
 __device__ __forceinline__ float2 gate2(float z0, float z1) {
-    const float2 e = gate_exp2<GELU>(z0, z1);
-    return make_float2(__fdividef(z0, 1.0f + e.x), __fdividef(z1, 1.0f + e.y));
+    const uint64_t z = pack_f32x2(z0, z1);
+    return unpack_f32x2(mul_f32x2(z, gate_logistic2<GELU>(z)));
 }
 
 template <bool GELU>
-__device__ __forceinline__ void gate_grad2(float z0, float z1, float2& y, float2& d) {
-    const float2 e = gate_exp2<GELU>(z0, z1);
-    uint64_t v = pack_f32x2(fminf(fmaxf(z0, -64.0f), 64.0f), fminf(fmaxf(z1, -64.0f), 64.0f));
+__device__ __forceinline__ void gate_grad2(uint64_t z, uint64_t& y, uint64_t& d) {
+    const uint64_t one = pack_f32x2(1.0f, 1.0f), s = gate_logistic2<GELU>(z);
+    uint64_t v = z;
     if (GELU) {
+        const float2 f = unpack_f32x2(z);
+        v = pack_f32x2(fminf(fmaxf(f.x, -64.0f), 64.0f), fminf(fmaxf(f.y, -64.0f), 64.0f));
         const uint64_t c2 = pack_f32x2(1.5957691216057308f, 1.5957691216057308f);
         const uint64_t k3 = pack_f32x2(3.0f * 0.044715f, 3.0f * 0.044715f);
-        v = mul_f32x2(mul_f32x2(c2, v), fma_f32x2(mul_f32x2(v, v), k3, pack_f32x2(1.0f, 1.0f)));
+        v = mul_f32x2(mul_f32x2(c2, v), fma_f32x2(mul_f32x2(v, v), k3, one));
     }
-    const uint64_t sp = pack_f32x2(__fdividef(1.0f, 1.0f + e.x), __fdividef(1.0f, 1.0f + e.y));
-    const uint64_t sm = mul_f32x2(pack_f32x2(e.x, e.y), sp);
-    y = unpack_f32x2(mul_f32x2(pack_f32x2(z0, z1), sp));
-    d = unpack_f32x2(fma_f32x2(mul_f32x2(v, sp), sm, sp));
+    y = mul_f32x2(z, s);
+    d = mul_f32x2(s, fma_f32x2(v, fma_f32x2(s, pack_f32x2(-1.0f, -1.0f), one), one));
 }
 
 // Hint that a global cache line will be read soon: fetched into L2 ahead of use.

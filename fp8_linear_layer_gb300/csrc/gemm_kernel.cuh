@@ -917,7 +917,8 @@ __device__ __forceinline__ void store_gated(const GemmParams& p, int row0, int c
 
 // gated gradient: dZ = (acc Z_up act'(Z_gate), acc act(Z_gate)), bf16 out [M][2 N]
 // with Z = aux [M][2 N], N % 128 == 0.  Z is read in the vectors that dZ is written
-// in, each lane its own before it writes them: out may be Z's own buffer.
+// in, each lane its own before it writes them: out may be Z's own buffer.  A row's
+// vectors of the next 32 columns are on their way while the ones before are used.
 template <bool GELU, int ROWS = 4>
 __device__ __forceinline__ void store_gated_grad(const GemmParams& p, int row0, int col0,
                                                  const uint64_t (&acc)[4 * kChunks]) {
@@ -926,41 +927,44 @@ __device__ __forceinline__ void store_gated_grad(const GemmParams& p, int row0, 
     const int cq = (col0 >> 1) & 3;
     const int cbase = col0 - 2 * cq;
     if (cbase >= p.N) return;  // the second half of the last tile of an odd number of 128-column blocks
+    uint4 gate[ROWS], up[ROWS];
+    auto fetch = [&](int g, int r) {
+        const int64_t row = row0 + 8 * r;
+        gate[r] = up[r] = make_uint4(0, 0, 0, 0);
+        if (row < p.M) {
+            const uint16_t* z = aux + 2 * row * p.N + cbase + 8 * (4 * g + cq);
+            gate[r] = *reinterpret_cast<const uint4*>(z);
+            up[r] = *reinterpret_cast<const uint4*>(z + p.N);
+        }
+    };
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) fetch(0, r);
 #pragma unroll
     for (int g = 0; g < kChunks / 4; ++g) {
-        const int vcol = cbase + 8 * (4 * g + cq);
-        uint32_t gw[4][4], uw[4][4];  // [row][chunk]: Z, until dZ replaces it
 #pragma unroll
         for (int r = 0; r < ROWS; ++r) {
-            const int64_t row = row0 + 8 * r;
-            uint4 a = make_uint4(0, 0, 0, 0), b = a;
-            if (row < p.M) {
-                const uint16_t* z = aux + 2 * row * p.N + vcol;
-                a = *reinterpret_cast<const uint4*>(z);
-                b = *reinterpret_cast<const uint4*>(z + p.N);
-            }
-            gw[r][0] = a.x; gw[r][1] = a.y; gw[r][2] = a.z; gw[r][3] = a.w;
-            uw[r][0] = b.x; uw[r][1] = b.y; uw[r][2] = b.z; uw[r][3] = b.w;
-        }
-#pragma unroll
-        for (int r = 0; r < ROWS; ++r) {
-            quad_transpose(gw[r], cq);
-            quad_transpose(uw[r], cq);
+            uint32_t gw[4] = {gate[r].x, gate[r].y, gate[r].z, gate[r].w};  // Z, until dZ replaces it
+            uint32_t uw[4] = {up[r].x, up[r].y, up[r].z, up[r].w};
+            if (g + 1 < kChunks / 4) fetch(g + 1, r);
+            quad_transpose(gw, cq);
+            quad_transpose(uw, cq);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float2 c = unpack_f32x2(acc[4 * (4 * g + j) + r]);
-                float2 y, d;
-                gate_grad2<GELU>(bf16_lo(gw[r][j]), bf16_hi(gw[r][j]), y, d);
-                gw[r][j] = pack_bf16x2(c.x * bf16_lo(uw[r][j]) * d.x, c.y * bf16_hi(uw[r][j]) * d.y);
-                uw[r][j] = pack_bf16x2(c.x * y.x, c.y * y.y);
+                const uint64_t c = acc[4 * (4 * g + j) + r];
+                uint64_t y, d;
+                gate_grad2<GELU>(pack_f32x2(bf16_lo(gw[j]), bf16_hi(gw[j])), y, d);
+                const float2 a = unpack_f32x2(mul_f32x2(mul_f32x2(c, pack_f32x2(bf16_lo(uw[j]), bf16_hi(uw[j]))), d));
+                const float2 b = unpack_f32x2(mul_f32x2(c, y));
+                gw[j] = pack_bf16x2(a.x, a.y);
+                uw[j] = pack_bf16x2(b.x, b.y);
             }
-            quad_transpose(gw[r], cq);
-            quad_transpose(uw[r], cq);
+            quad_transpose(gw, cq);
+            quad_transpose(uw, cq);
             const int64_t row = row0 + 8 * r;
             if (row >= p.M) continue;
-            uint16_t* o = out + 2 * row * p.N + vcol;
-            *reinterpret_cast<uint4*>(o) = make_uint4(gw[r][0], gw[r][1], gw[r][2], gw[r][3]);
-            *reinterpret_cast<uint4*>(o + p.N) = make_uint4(uw[r][0], uw[r][1], uw[r][2], uw[r][3]);
+            uint16_t* o = out + 2 * row * p.N + cbase + 8 * (4 * g + cq);
+            *reinterpret_cast<uint4*>(o) = make_uint4(gw[0], gw[1], gw[2], gw[3]);
+            *reinterpret_cast<uint4*>(o + p.N) = make_uint4(uw[0], uw[1], uw[2], uw[3]);
         }
     }
 }
