@@ -36,12 +36,40 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return t.data_ptr()
 
 
-def _on_device(*tensors):
-    """The tensors (or none) are on torch's current device, whose stream the call uses."""
-    here = tensors[0].get_device()
+# What the calls of the layer norm, of dropout and of the gated product check of a
+# tensor: that it is on torch's current device, whose stream the call uses, its type
+# and its size.  One pass over each tensor: a call of few tokens is bound by it.
+
+def _current(t: torch.Tensor) -> int:
+    """The current device, on which t is."""
+    here = t.get_device()
     assert here >= 0 and here == _C._cuda_getDevice(), "the tensors are not on the current GPU"
-    for t in tensors[1:]:
-        assert t is None or t.get_device() == here, "the tensors are on several devices"
+    return here
+
+
+def _vector(t, dtype, n, here):
+    """Address of a contiguous tensor of n elements (or none)."""
+    if t is None:
+        return None
+    assert t.numel() == n and t.dtype is dtype and t.is_contiguous() and t.get_device() == here
+    return t.data_ptr()
+
+
+def _matrix(t, dtype, shape, here):
+    """Address of a contiguous tensor of this shape (or none)."""
+    if t is None:
+        return None
+    assert t.shape == shape and t.dtype is dtype and t.is_contiguous() and t.get_device() == here
+    return t.data_ptr()
+
+
+def _strided(t, shape, here):
+    """Address and leading dimension of a bf16 matrix with packed rows (or none)."""
+    if t is None:
+        return None, 0
+    ld, one = t.stride()
+    assert t.shape == shape and t.dtype is _bf16 and (one == 1 or shape[1] == 1) and t.get_device() == here
+    return t.data_ptr(), ld if shape[0] > 1 else shape[1]
 
 
 # -------------------------------------------------------------------- norm ----
@@ -259,33 +287,34 @@ def empty_tensor_layernorm(rows: int, cols: int, fmt: int, rows_too: bool = True
     return _with_mean(empty_tensor_rmsnorm(rows, cols, fmt, rows_too, cols_too, residual, y, device))
 
 
-def _layernorm_args(x, shape, gamma, beta, eps, fmt, residual, out):
-    _on_device(x, gamma, beta, residual, out.h, out.mean, out.rstd, out.y)
-    a = _norm_args(x, shape, gamma, eps, fmt, residual, out)
-    return a[:3] + (_packed(beta, _bf16, (shape[1],)),) + a[3:]
+def _layernorm_args(x, gamma, beta, eps, fmt, residual, out):
+    """(the current device, the arguments that the three recipes share, in front and behind)"""
+    here, shape = _current(x), x.shape
+    m, k = shape
+    xp, ldx = _strided(x, shape, here)
+    rp, ldr = _strided(residual, shape, here)
+    assert residual is None or out.h is not None, "the sum x + residual needs its place (h)"
+    return (here, (xp, rp, _vector(gamma, _bf16, k, here), _vector(beta, _bf16, k, here), m, k, ldx, ldr, eps, fmt),
+            (_matrix(out.h, _bf16, shape, here), _vector(out.mean, _f32, m, here), _vector(out.rstd, _f32, m, here),
+             _matrix(out.y, _bf16, shape, here)))
 
 
-def _layernorm_outs(shape, out):
-    h, rstd, y = _norm_outs(shape, out)
-    return h, _packed(out.mean, _f32, (shape[0],)), rstd, y
-
-
-def _block_codes(t, fmt, shape):
+def _block_codes(t, fmt, shape, here):
     """(codes, scales, the scales' leading dimension) of an operand that a cast writes, or of none."""
     if t is None:
         return None, None, 0
-    _on_device(t.q, t.scale)
-    ld, one = t.scale.stride()
-    assert t.scale.dtype is _f32 and one == 1 and t.scale.shape[0] == shape[1] // 128 and t.scale.shape[1] >= shape[0]
-    return _codes(t, fmt, *shape), t.scale.data_ptr(), ld
+    scale = t.scale
+    (kb, rows), (ld, one) = scale.shape, scale.stride()
+    assert t.fmt == fmt and scale.dtype is _f32 and one == 1 and kb == shape[1] // 128 and rows >= shape[0]
+    assert scale.get_device() == here
+    return _matrix(t.q, _u8, shape, here), scale.data_ptr(), ld
 
 
-def _mx_codes(t, fmt, shape):
+def _mx_codes(t, fmt, shape, here):
     if t is None:
         return None, None
-    _on_device(t.q, t.sf)
-    assert t.sf.dtype is _u8 and t.sf.is_contiguous() and t.sf.numel() >= B.mx_sf_bytes(*shape)
-    return _codes(t, fmt, *shape), t.sf.data_ptr()
+    assert t.fmt == fmt
+    return _matrix(t.q, _u8, shape, here), _vector(t.sf, _u8, B.mx_sf_bytes(*shape), here)
 
 
 def layernorm_quantize(x: torch.Tensor, gamma: torch.Tensor, beta: Optional[torch.Tensor], eps: float, fmt: int,
@@ -293,13 +322,13 @@ def layernorm_quantize(x: torch.Tensor, gamma: torch.Tensor, beta: Optional[torc
                        cols: bool = False, y: bool = False) -> LayerNorm:
     """h = x + residual (bf16), then its layer norm y = (h - mean) rstd gamma + beta
     cast from fp32, as ``rmsnorm_quantize`` casts its output."""
-    shape = x.shape
-    m, k = shape
+    m, k = x.shape
     if out is None:
         out = empty_layernorm(m, k, fmt, rows, cols, residual is not None, y, x.device)
-    _check(lib().fp8_layernorm_quantize(*_layernorm_args(x, shape, gamma, beta, eps, fmt, residual, out),
-                                        *_layernorm_outs(shape, out), *_block_codes(out.rows, fmt, (m, k)),
-                                        *_block_codes(out.cols, fmt, (k, m)), _stream()), "fp8_layernorm_quantize")
+    here, args, outs = _layernorm_args(x, gamma, beta, eps, fmt, residual, out)
+    _check(lib().fp8_layernorm_quantize(*args, *outs, *_block_codes(out.rows, fmt, (m, k), here),
+                                        *_block_codes(out.cols, fmt, (k, m), here), _stream()),
+           "fp8_layernorm_quantize")
     return out
 
 
@@ -307,13 +336,12 @@ def mx_layernorm_quantize(x: torch.Tensor, gamma: torch.Tensor, beta: Optional[t
                           residual: Optional[torch.Tensor] = None, out: Optional[LayerNorm] = None, rows: bool = True,
                           cols: bool = False, y: bool = False) -> LayerNorm:
     """``layernorm_quantize`` with MXFP8 operands (one power-of-two scale per 32 elements)."""
-    shape = x.shape
-    m, k = shape
+    m, k = x.shape
     if out is None:
         out = empty_mx_layernorm(m, k, fmt, rows, cols, residual is not None, y, x.device)
-    _check(lib().fp8_mx_layernorm_quantize(*_layernorm_args(x, shape, gamma, beta, eps, fmt, residual, out),
-                                           *_layernorm_outs(shape, out), *_mx_codes(out.rows, fmt, (m, k)),
-                                           *_mx_codes(out.cols, fmt, (k, m)), _stream()),
+    here, args, outs = _layernorm_args(x, gamma, beta, eps, fmt, residual, out)
+    _check(lib().fp8_mx_layernorm_quantize(*args, *outs, *_mx_codes(out.rows, fmt, (m, k), here),
+                                           *_mx_codes(out.cols, fmt, (k, m), here), _stream()),
            "fp8_mx_layernorm_quantize")
     return out
 
@@ -325,28 +353,24 @@ def tensor_layernorm_quantize(x: torch.Tensor, gamma: torch.Tensor, beta: Option
     """``layernorm_quantize`` with one scale for the tensor, made of ``amax_in`` (a
     1-element device tensor: the largest amax of earlier steps); ``amax`` of the
     result receives this call's max|y|."""
-    shape = x.shape
-    m, k = shape
+    m, k = x.shape
     if out is None:
         out = empty_tensor_layernorm(m, k, fmt, rows, cols, residual is not None, y, x.device)
-    args = _layernorm_args(x, shape, gamma, beta, eps, fmt, residual, out)
+    here, args, outs = _layernorm_args(x, gamma, beta, eps, fmt, residual, out)
     qr = qc = scale = None
-    for t in (out.rows, out.cols):
-        if t is None:
-            continue
-        assert scale is None or scale.data_ptr() == t.scale.data_ptr(), "both orientations share one scale"
-        scale = t.scale
-        _on_device(t.q, scale)
     if out.rows is not None:
-        qr = _codes(out.rows, fmt, m, k)
+        assert out.rows.fmt == fmt
+        qr, scale = _matrix(out.rows.q, _u8, (m, k), here), _vector(out.rows.scale, _f32, 1, here)
     if out.cols is not None:
-        qc = _codes(out.cols, fmt, k, m)
+        assert out.cols.fmt == fmt
+        qc, other = _matrix(out.cols.q, _u8, (k, m), here), _vector(out.cols.scale, _f32, 1, here)
+        assert scale in (None, other), "both orientations share one scale"
+        scale = other
     if scale is None:  # only the bf16 form was asked for
-        scale = torch.empty((1,), dtype=_f32, device=x.device)
-    _on_device(x, amax_in, out.amax)
-    assert amax_in.dtype is _f32 and amax_in.numel() == 1 and scale.dtype is _f32 and scale.numel() == 1
-    _check(lib().fp8_tensor_layernorm_quantize(*args, amax_in.data_ptr(), *_layernorm_outs(shape, out), qr, qc,
-                                               scale.data_ptr(), _packed(out.amax, _f32, (1,)), _stream()),
+        spare = torch.empty((1,), dtype=_f32, device=x.device)
+        scale = spare.data_ptr()
+    _check(lib().fp8_tensor_layernorm_quantize(*args, _vector(amax_in, _f32, 1, here), *outs, qr, qc, scale,
+                                               _vector(out.amax, _f32, 1, here), _stream()),
            "fp8_tensor_layernorm_quantize")
     return out
 
@@ -378,14 +402,13 @@ def layernorm_backward(dy: torch.Tensor, h: torch.Tensor, gamma: torch.Tensor, m
         dbeta = torch.empty((cols,), dtype=_f32, device=h.device)
     if workspace is None:
         workspace = layernorm_workspace(rows, cols, h.device)
-    assert workspace.is_contiguous()
-    _on_device(h, dy, gamma, mean, rstd, r, out, dgamma, dbeta, workspace)
-    ldd, ldh, ldr = _rows(dy, shape), _rows(h, shape), 0 if r is None else _rows(r, shape)
-    _check(lib().fp8_layernorm_backward(dy.data_ptr(), h.data_ptr(), _packed(gamma, _bf16, (cols,)),
-                                        _packed(mean, _f32, (rows,)), _packed(rstd, _f32, (rows,)),
-                                        None if r is None else r.data_ptr(), rows, cols, ldd, ldh, ldr,
-                                        _packed(out, _bf16, shape), _packed(dgamma, _f32, (cols,)),
-                                        _packed(dbeta, _f32, (cols,)), int(accumulate), workspace.data_ptr(),
+    here = _current(h)
+    (hp, ldh), (dp, ldd), (rp, ldr) = _strided(h, shape, here), _strided(dy, shape, here), _strided(r, shape, here)
+    assert workspace.is_contiguous() and workspace.get_device() == here
+    _check(lib().fp8_layernorm_backward(dp, hp, _vector(gamma, _bf16, cols, here), _vector(mean, _f32, rows, here),
+                                        _vector(rstd, _f32, rows, here), rp, rows, cols, ldd, ldh, ldr,
+                                        _matrix(out, _bf16, shape, here), _vector(dgamma, _f32, cols, here),
+                                        _vector(dbeta, _f32, cols, here), int(accumulate), workspace.data_ptr(),
                                         workspace.nbytes, _stream()), "fp8_layernorm_backward")
     return out, dgamma, dbeta
 
@@ -401,21 +424,19 @@ def dropout(x: torch.Tensor, p: float, seed: int, site: int = 0, step: Union[int
     1-element int64 device tensor that a captured step counts up), and is never
     stored: the gradient of x is this call on the output's gradient, with the same
     numbers and no residual.  ``out`` may be x or the residual itself."""
-    shape = x.shape
-    ldx, ldr = _rows(x, shape), 0 if residual is None else _rows(residual, shape)
+    here, shape = _current(x), x.shape
+    rows, cols = shape
+    (xp, ldx), (rp, ldr) = _strided(x, shape, here), _strided(residual, shape, here)
     assert 0 <= seed < 1 << 64 and 0 <= site < 1 << 32
     if out is None:
-        out = torch.empty(tuple(shape), dtype=_bf16, device=x.device)
+        out = torch.empty((rows, cols), dtype=_bf16, device=x.device)
     counter = None
     if isinstance(step, torch.Tensor):
-        assert step.dtype is torch.int64 and step.numel() == 1
-        counter, step = step, 0
+        counter, step = _vector(step, torch.int64, 1, here), 0
     else:
         assert -(1 << 63) <= step < 1 << 63
-    _on_device(x, residual, out, counter)
-    _check(lib().fp8_dropout(x.data_ptr(), None if residual is None else residual.data_ptr(), shape[0], shape[1], ldx,
-                             ldr, p, seed, site, step, None if counter is None else counter.data_ptr(),
-                             _packed(out, _bf16, shape), _stream()), "fp8_dropout")
+    _check(lib().fp8_dropout(xp, rp, rows, cols, ldx, ldr, p, seed, site, step, counter,
+                             _matrix(out, _bf16, shape, here), _stream()), "fp8_dropout")
     return out
 
 
@@ -475,40 +496,36 @@ def tensor_gemm_linear(A: Fp8TensorScaled, W: Fp8TensorScaled, bias: Optional[to
 
 # ----------------------------------------------------------- gated product ----
 
-def _operand_scales(t, rows, k):
-    """The scales of an operand of the gated products, which have to cover its rows."""
-    if isinstance(t, Fp8Tensor):
-        s = t.scale
-        assert s.dtype is _f32 and s.shape[0] >= k // 128 and s.shape[1] >= rows and s.stride()[1] == 1
-    elif isinstance(t, Fp8MxTensor):
-        s = t.sf
-        assert s.dtype is _u8 and s.is_contiguous() and s.numel() >= k // 32 * (-(-rows // 256) * 256)
-    else:
-        s = t.scale
-        assert s.dtype is _f32 and s.numel() == 1
-    return s
-
-
-def _gated_args(A, W, N, *others):
-    """(sizes, operands) of a gated product: A [M][K], W of as many columns; all on the current device."""
-    (M, K), (R, KW) = A.q.shape, W.q.shape
-    assert K == KW and A.q.dtype is _u8 and W.q.dtype is _u8
-    assert A.q.stride()[1] == 1 and W.q.stride()[1] == 1
-    _on_device(A.q, W.q, _operand_scales(A, M, K), _operand_scales(W, R, K), *others)
-    return (M, N, K), (ctypes.byref(A.operand()), ctypes.byref(W.operand()))
+def _operand(t, kind, here):
+    """(rows, K, the C struct) of an operand of the gated products."""
+    assert type(t) is kind
+    q = t.q
+    (rows, k), (ld, one) = q.shape, q.stride()
+    assert one == 1 and q.dtype is _u8 and q.get_device() == here
+    if kind is Fp8Tensor:
+        scale = t.scale
+        (kb, n), (sld, one) = scale.shape, scale.stride()
+        assert kb * 128 >= k and n >= rows and one == 1 and scale.dtype is _f32 and scale.get_device() == here
+        return rows, k, B.OperandStruct(q.data_ptr(), scale.data_ptr(), ld, sld, t.fmt, 0)
+    if kind is Fp8MxTensor:
+        sf = t.sf
+        assert sf.numel() >= k // 32 * (-(-rows // 256) * 256) and sf.dtype is _u8 and sf.is_contiguous()
+        assert sf.get_device() == here
+        return rows, k, B.MxOperandStruct(q.data_ptr(), sf.data_ptr(), ld, t.fmt, 0)
+    return rows, k, B.TensorOperandStruct(q.data_ptr(), _vector(t.scale, _f32, 1, here), ld, t.fmt, 0)
 
 
 def _gated(kind, call, A, W, bias, act, acc, out, aux, want_aux):
-    assert type(A) is kind and type(W) is kind
-    M, N = A.q.shape[0], W.q.shape[0] // 2
-    assert W.q.shape[0] == 2 * N, "W holds the gate's rows, then as many of the up projection"
+    here = _current(A.q)
+    (M, K, a), (R, KW, w) = _operand(A, kind, here), _operand(W, kind, here)
+    N = R // 2
+    assert K == KW and R == 2 * N, "W holds the gate's rows, then as many of the up projection"
     if out is None:
         out = torch.empty((M, N), dtype=_bf16, device=A.q.device)
     if aux is None and want_aux:
-        aux = torch.empty((M, 2 * N), dtype=_bf16, device=A.q.device)
-    sizes, ops = _gated_args(A, W, N, bias, out, aux)
-    _check(getattr(lib(), call)(*sizes, *ops, _packed(bias, _bf16, (2 * N,)), act, *acc, _packed(out, _bf16, (M, N)),
-                                _packed(aux, _bf16, (M, 2 * N)), _stream()), call)
+        aux = torch.empty((M, R), dtype=_bf16, device=A.q.device)
+    _check(getattr(lib(), call)(M, N, K, ctypes.byref(a), ctypes.byref(w), _vector(bias, _bf16, R, here), act, *acc,
+                                _matrix(out, _bf16, (M, N), here), _matrix(aux, _bf16, (M, R), here), _stream()), call)
     return out, aux
 
 
@@ -536,13 +553,13 @@ def tensor_gemm_gated(A: Fp8TensorScaled, W: Fp8TensorScaled, bias: Optional[tor
 
 
 def _gated_dgrad(kind, call, A, W, aux, act, acc, out):
-    assert type(A) is kind and type(W) is kind
-    M, N = A.q.shape[0], W.q.shape[0]
+    here = _current(A.q)
+    (M, K, a), (N, KW, w) = _operand(A, kind, here), _operand(W, kind, here)
+    assert K == KW
     if out is None:
         out = torch.empty((M, 2 * N), dtype=_bf16, device=A.q.device)
-    sizes, ops = _gated_args(A, W, N, aux, out)
-    _check(getattr(lib(), call)(*sizes, *ops, _packed(aux, _bf16, (M, 2 * N)), act, *acc,
-                                _packed(out, _bf16, (M, 2 * N)), _stream()), call)
+    _check(getattr(lib(), call)(M, N, K, ctypes.byref(a), ctypes.byref(w), _matrix(aux, _bf16, (M, 2 * N), here), act,
+                                *acc, _matrix(out, _bf16, (M, 2 * N), here), _stream()), call)
     return out
 
 
