@@ -121,7 +121,9 @@ __global__ void zero_word_kernel(float* word) {
 
 // max|y| over the block into *amax_out, one atomic per block: non-negative
 // floats order like their bits, and a maximum does not depend on the order.  A
-// single block stores it; otherwise the word was zeroed before.
+// single block stores it; otherwise the word was zeroed before.  LOOK: only where the
+// word is smaller yet (a block per row: thousands of atomics in one place are slow).
+template <bool LOOK>
 __device__ __forceinline__ void fold_amax(float top, float* part, float* amax_out) {
 #pragma unroll
     for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
@@ -130,16 +132,20 @@ __device__ __forceinline__ void fold_amax(float top, float* part, float* amax_ou
     __syncthreads();
     if (threadIdx.x == 0) {
         for (int w = 1; w < static_cast<int>(blockDim.x >> 5); ++w) top = fmaxf(top, part[w]);
+        unsigned* word = reinterpret_cast<unsigned*>(amax_out);
         if (gridDim.x == 1)
             *amax_out = top;
-        else
-            atomicMax(reinterpret_cast<unsigned*>(amax_out), __float_as_uint(top));
+        else if (!LOOK || __float_as_uint(top) > *reinterpret_cast<volatile unsigned*>(word))
+            atomicMax(word, __float_as_uint(top));
     }
 }
 
-// GREG: gamma (CENTER: and beta) stays in registers for all rows of the CTA
-template <bool CENTER, int FMT, int RECIPE, int V, int MAXT, bool GREG>
-__global__ void __launch_bounds__(MAXT) norm_rows_kernel(const __grid_constant__ NormParams p) {
+// GREG: gamma (CENTER, V = 1: and beta) stays in registers for all rows of the CTA.
+// PRE: the next row is loaded while the current one is reduced and cast (else, where a
+// CTA has another one at all, behind it).  MINB: CTAs
+// of MAXT threads that the registers leave room for (0: no matter).
+template <bool CENTER, int FMT, int RECIPE, int V, int MAXT, bool GREG, bool PRE, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) norm_rows_kernel(const __grid_constant__ NormParams p) {
     __shared__ float part[2][32];
     await_dependency();
     // the columns kernel and kernels behind a short one come in early; behind a long
@@ -150,10 +156,11 @@ __global__ void __launch_bounds__(MAXT) norm_rows_kernel(const __grid_constant__
     const int lane = threadIdx.x & 31;
     const int64_t mx_groups = 2 * ((p.rows + 255) / 256);
     float inv_t = 1.0f, s_t = 1.0f, top = 0.0f;
-    if (RECIPE == kRecipeTensor) {
+    auto tensor_scale = [&] {
         block_scale<FMT>(*p.amax_in, inv_t, s_t);
         if (blockIdx.x == 0 && threadIdx.x == 0) *p.scale = s_t;
-    }
+    };
+    if (RECIPE == kRecipeTensor && !CENTER) tensor_scale();
     const uint4 zero = make_uint4(0, 0, 0, 0);
     uint4 xv[V], rv[V];  // the next row, loaded while the current one is reduced and cast
     auto fetch = [&](int64_t r) {
@@ -172,17 +179,20 @@ __global__ void __launch_bounds__(MAXT) norm_rows_kernel(const __grid_constant__
     auto load_beta = [&](int v) { return p.beta ? load_weight(p.beta, v) : zero; };
     int64_t r = blockIdx.x;
     fetch(r);
-    uint4 gv[GREG ? V : 1], bv[GREG && CENTER ? V : 1];
+    if (RECIPE == kRecipeTensor && CENTER) tensor_scale();  // the row is on its way meanwhile
+    constexpr bool BREG = GREG && CENTER && V == 1;
+    uint4 gv[GREG ? V : 1], bv[BREG ? V : 1];
     if (GREG) {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             gv[v] = load_weight(p.gamma, v);
-            if (CENTER) bv[CENTER ? v : 0] = load_beta(v);
+            if (BREG) bv[BREG ? v : 0] = load_beta(v);
         }
     }
     for (int k = 0; r < p.rows; r += gridDim.x, ++k) {
         uint4 hv[V];
-        float sq = 0.0f, mean = 0.0f;  // CENTER: sq is the row's sum first
+        float sq = 0.0f, mean = 0.0f;
+        uint64_t sum2 = 0ull;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int i = threadIdx.x + v * T;
@@ -198,25 +208,33 @@ __global__ void __launch_bounds__(MAXT) norm_rows_kernel(const __grid_constant__
                 unpack8(hv[v], f);
             }
             if (p.h && i < nv) *reinterpret_cast<uint4*>(p.h + r * p.cols + 8 * i) = hv[v];
+            if (CENTER) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sq = CENTER ? sq + f[e] : fmaf(f[e], f[e], sq);
+                for (int e = 0; e < 4; ++e) sum2 = add_f32x2(pack_f32x2(f[2 * e], f[2 * e + 1]), sum2);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sq = fmaf(f[e], f[e], sq);
+            }
         }
-        fetch(r + gridDim.x);
+        if (PRE) fetch(r + gridDim.x);
         if (CENTER) {
-            mean = __fdiv_rn(block_sum(sq, part[0]), static_cast<float>(p.cols));
+            const float2 s = unpack_f32x2(sum2);
+            mean = __fdiv_rn(block_sum(s.x + s.y, part[0]), static_cast<float>(p.cols));
             if (threadIdx.x == 0) p.mean[r] = mean;
-            sq = 0.0f;
+            const uint64_t minus_mean2 = pack_f32x2(-mean, -mean);
+            sum2 = 0ull;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                float f[8];
-                unpack8(hv[v], f);
                 if (threadIdx.x + v * T >= nv) continue;
+                const uint32_t w[4] = {hv[v].x, hv[v].y, hv[v].z, hv[v].w};
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float c = f[e] - mean;
-                    sq = fmaf(c, c, sq);
+                for (int e = 0; e < 4; ++e) {
+                    const uint64_t c = add_f32x2(pack_f32x2(bf16_lo(w[e]), bf16_hi(w[e])), minus_mean2);
+                    sum2 = fma_f32x2(c, c, sum2);
                 }
             }
+            const float2 q = unpack_f32x2(sum2);
+            sq = q.x + q.y;
         }
         sq = block_sum(sq, part[CENTER ? 1 : k & 1]);
         // correctly rounded: an ulp here moves every code of the row that lies near a tie
@@ -231,7 +249,7 @@ __global__ void __launch_bounds__(MAXT) norm_rows_kernel(const __grid_constant__
         for (int v = 0; v < V; ++v) {
             const uint4 g = GREG ? gv[GREG ? v : 0] : load_weight(p.gamma, v);
             if (CENTER)
-                center8(hv[v], g, GREG ? bv[GREG && CENTER ? v : 0] : load_beta(v), pack_f32x2(-mean, -mean), rstd2, y[v]);
+                center8(hv[v], g, BREG ? bv[BREG ? v : 0] : load_beta(v), pack_f32x2(-mean, -mean), rstd2, y[v]);
             else
                 norm8(hv[v], g, rstd2, y[v]);
             amax[v] = amax8(y[v]);  // 0 beyond the row
@@ -250,7 +268,10 @@ __global__ void __launch_bounds__(MAXT) norm_rows_kernel(const __grid_constant__
                 if (i < nv) *reinterpret_cast<uint4*>(p.y + r * p.cols + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
             }
         }
-        if (!p.qr) continue;
+        if (!p.qr) {
+            if (!PRE) fetch(r + gridDim.x);
+            continue;
+        }
         float inv[V];
         if (RECIPE == kRecipeTensor) {
 #pragma unroll
@@ -268,8 +289,16 @@ __global__ void __launch_bounds__(MAXT) norm_rows_kernel(const __grid_constant__
                 const int i = threadIdx.x + v * T;
                 const int e = mx_exponent<FMT>(amax[v]);
                 inv[v] = mx_inverse_scale(e);
-                if (i < nv && (i & 3) == 0)
+                if (CENTER) {
+                    // the four bytes of a 128-block stand side by side: one store of its first lane
+                    uint32_t b = static_cast<uint32_t>(e + 127) << (8 * ((lane >> 2) & 3));
+                    b |= __shfl_xor_sync(0xffffffffu, b, 4);
+                    b |= __shfl_xor_sync(0xffffffffu, b, 8);
+                    if (i < nv && (i & 15) == 0)
+                        *reinterpret_cast<uint32_t*>(p.sfr + mx_sf_offset(i >> 4, mx_groups, r, 0)) = b;
+                } else if (i < nv && (i & 3) == 0) {
                     p.sfr[mx_sf_offset(i >> 4, mx_groups, r, (i >> 2) & 3)] = static_cast<uint8_t>(e + 127);
+                }
             }
         }
         if (RECIPE == kRecipeBlock) {
@@ -294,6 +323,7 @@ __global__ void __launch_bounds__(MAXT) norm_rows_kernel(const __grid_constant__
             const int i = threadIdx.x + v * T;
             if (i < nv) __stcs(reinterpret_cast<uint2*>(p.qr + r * p.cols + 8 * i), encode8_pairs<FMT>(y[v], inv[v]));
         }
+        if (!PRE) fetch(r + gridDim.x);
     }
     if (RECIPE == kRecipeMx && p.qr) {
         // the scale bytes of rows beyond the matrix hold 127
@@ -301,7 +331,7 @@ __global__ void __launch_bounds__(MAXT) norm_rows_kernel(const __grid_constant__
             for (int64_t i = threadIdx.x; i < p.cols / 128; i += T)
                 *reinterpret_cast<uint32_t*>(p.sfr + mx_sf_offset(i, mx_groups, r, 0)) = 0x7F7F7F7Fu;
     }
-    if (RECIPE == kRecipeTensor && p.amax_out) fold_amax(top, part[0], p.amax_out);
+    if (RECIPE == kRecipeTensor && p.amax_out) fold_amax<!PRE>(top, part[0], p.amax_out);
 }
 
 // Column codes of y from h, rstd and gamma, in 128 x 128 tiles of h staged in
@@ -312,7 +342,13 @@ __global__ void __launch_bounds__(MAXT) norm_rows_kernel(const __grid_constant__
 // a column's maximum needs one product per element and gamma once.  CENTER: y is a
 // monotone function of xhat = fl(fl(h - mean) rstd) along a column, so |y| is
 // largest at its smallest or its largest xhat.
-constexpr int kColsCtas = 3;
+// CTAs per SM: shared memory has room for three, in which the layer norm's registers
+// spill (8192 x 4096, rows and columns, three / two: 63.6 / 61.1 us on 1x128, 69.2 /
+// 67.9 in MXFP8, 58.7 / 57.9 per tensor)
+template <bool CENTER>
+constexpr int cols_ctas() {
+    return CENTER ? 2 : 3;
+}
 struct ColsStage {
     uint32_t tile[128][64];
     float rstd[4][36];  // part p's 32 rows, banks apart
@@ -328,7 +364,7 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
 }
 
 template <bool CENTER, int FMT, int RECIPE>
-__global__ void __launch_bounds__(256, kColsCtas) norm_cols_kernel(const __grid_constant__ NormParams p) {
+__global__ void __launch_bounds__(256, cols_ctas<CENTER>()) norm_cols_kernel(const __grid_constant__ NormParams p) {
     extern __shared__ __align__(16) uint8_t stage_raw[];
     await_dependency();
     ColsStage* stage = reinterpret_cast<ColsStage*>(stage_raw);
@@ -459,7 +495,7 @@ int launch_cols(const NormParams& p, cudaStream_t stream, int num_sms) {
     auto kern = norm_cols_kernel<CENTER, FMT, RECIPE>;
     static PerDevice allowed;
     if (allow_shared_memory(allowed, kern, 2 * sizeof(ColsStage)) != 0) return -3;
-    const int64_t tiles = p.rows / 128 * (p.cols / 128), cap = static_cast<int64_t>(num_sms) * kColsCtas;
+    const int64_t tiles = p.rows / 128 * (p.cols / 128), cap = static_cast<int64_t>(num_sms) * cols_ctas<CENTER>();
     return launch_dependent(kern, static_cast<unsigned>(tiles < cap ? tiles : cap), 256, 2 * sizeof(ColsStage), stream,
                             p) == cudaSuccess
                ? 0
@@ -473,15 +509,38 @@ void row_shape(int64_t cols, int& T, int& V) {
     T = static_cast<int>(((nv + V - 1) / V + 31) / 32 * 32);
 }
 
+// The layer norm: whether each row has a CTA of its own, of four vectors a thread,
+// without a row loaded ahead.  Its 62 to 64 registers let 1024 threads run on an SM
+// where the next row's would leave 512, and other rows' CTAs hide what a row waits
+// for (its loads, two sums).  us, this / persistent CTAs with the next row ahead
+// (rows x cols, with residual; 1x128 | MXFP8 | per tensor):
+//   4096 x 8192  43.0 / 48.8 | 47.4 / 53.7 | 45.6 / 56.5
+//   777 x 7168   10.9 / 13.0 | 12.3 / 15.1 | 13.2 / 14.2
+// where those have two vectors a thread or one, and 768 or more threads on an SM:
+//   8192 x 4096  41.2 / 43.8 | 45.4 / 47.4 | 43.0 / 41.0
+//   16384 x 1024 22.6 / 24.3 | 24.9 / 27.0 | 23.8 / 24.0
+//   777 x 2048    4.2 /  4.3 |  5.0 /  4.7 |  5.6 /  4.6
+//   400 x 4096    4.2 /  4.0 |  5.8 /  4.6 |  5.4 /  4.6
+// The number of rows does not count: a row's sums are added in one order in any batch.
+inline bool row_alone(int64_t cols, int recipe) {
+    return cols > (recipe == kRecipeBlock ? 512 : 4096);
+}
+
 template <bool CENTER, int FMT, int RECIPE>
 int launch_norm(const NormParams& p, cudaStream_t stream, int num_sms) {
     int T, V;
     row_shape(p.cols, T, V);
+    const bool alone = CENTER && row_alone(p.cols, RECIPE);
+    if (alone) {
+        V = 4;
+        T = static_cast<int>(((p.cols / 8 + V - 1) / V + 31) / 32 * 32);
+    }
     // 768 (1024) threads of rows per SM; from 4224 columns on the kernels' 118 to 121
     // registers let only 512 run at once (at 7168 columns two CTAs of 224 threads, three
     // launched): the rest start where the first ones end
     int64_t grid = RECIPE == kRecipeMx ? (p.rows + 255) / 256 * 256 : p.rows;
     const int64_t cap = static_cast<int64_t>(num_sms) * ((V == 1 ? 1024 : 768) / T < 1 ? 1 : (V == 1 ? 1024 : 768) / T);
+    const int64_t grid_rows = grid;
     if (grid > cap) grid = cap;
     const unsigned g = static_cast<unsigned>(grid);
     // a kernel of one thread: a memset node cost 4 us here
@@ -489,12 +548,23 @@ int launch_norm(const NormParams& p, cudaStream_t stream, int num_sms) {
         launch_dependent(zero_word_kernel, 1, 1, 0, stream, p.amax_out) != cudaSuccess)
         return -3;
     cudaError_t rc;
-    switch (V) {
-        case 1: rc = launch_dependent(norm_rows_kernel<CENTER, FMT, RECIPE, 1, 128, true>, g, T, 0, stream, p); break;
-        case 2: rc = launch_dependent(norm_rows_kernel<CENTER, FMT, RECIPE, 2, 256, true>, g, T, 0, stream, p); break;
-        default:
-            rc = T <= 512 ? launch_dependent(norm_rows_kernel<CENTER, FMT, RECIPE, 4, 512, !CENTER>, g, T, 0, stream, p)
-                          : launch_dependent(norm_rows_kernel<CENTER, FMT, RECIPE, 4, 1024, false>, g, T, 0, stream, p);
+    if constexpr (CENTER) {
+        if (alone) {
+            const unsigned all = static_cast<unsigned>(grid_rows);
+            rc = T <= 512 ? launch_dependent(norm_rows_kernel<CENTER, FMT, RECIPE, 4, 512, false, false, 2>, all, T, 0, stream, p)
+                          : launch_dependent(norm_rows_kernel<CENTER, FMT, RECIPE, 4, 1024, false, false, 1>, all, T, 0, stream, p);
+        } else {
+            rc = V == 1 ? launch_dependent(norm_rows_kernel<CENTER, FMT, RECIPE, 1, 128, true, true, 0>, g, T, 0, stream, p)
+                        : launch_dependent(norm_rows_kernel<CENTER, FMT, RECIPE, 2, 256, true, true, 3>, g, T, 0, stream, p);
+        }
+    } else {
+        switch (V) {
+            case 1: rc = launch_dependent(norm_rows_kernel<CENTER, FMT, RECIPE, 1, 128, true, true, 0>, g, T, 0, stream, p); break;
+            case 2: rc = launch_dependent(norm_rows_kernel<CENTER, FMT, RECIPE, 2, 256, true, true, 0>, g, T, 0, stream, p); break;
+            default:
+                rc = T <= 512 ? launch_dependent(norm_rows_kernel<CENTER, FMT, RECIPE, 4, 512, true, true, 0>, g, T, 0, stream, p)
+                              : launch_dependent(norm_rows_kernel<CENTER, FMT, RECIPE, 4, 1024, false, true, 0>, g, T, 0, stream, p);
+        }
     }
     if (rc != cudaSuccess) return -3;
     return p.qc ? launch_cols<CENTER, FMT, RECIPE>(p, stream, num_sms) : 0;
@@ -524,8 +594,8 @@ __device__ __forceinline__ void unpack_pairs(const uint4& w, uint64_t (&f)[4]) {
     for (int e = 0; e < 4; ++e) f[e] = pack_f32x2(bf16_lo(u[e]), bf16_hi(u[e]));
 }
 
-template <bool CENTER, int V, int MAXT, bool SMEM, bool PRE, int LANES>
-__global__ void __launch_bounds__(MAXT, 1) norm_grad_kernel(const __grid_constant__ NormGradParams p) {
+template <bool CENTER, int V, int MAXT, bool SMEM, bool PRE, int LANES, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) norm_grad_kernel(const __grid_constant__ NormGradParams p) {
     static_assert(LANES == 0 || !SMEM, "a warp's sums stay in registers");
     constexpr bool WARP = LANES != 0;
     constexpr int kRowsPerCta = WARP ? 256 / (WARP ? LANES : 1) : 1;
@@ -573,13 +643,21 @@ __global__ void __launch_bounds__(MAXT, 1) norm_grad_kernel(const __grid_constan
     const int64_t step = static_cast<int64_t>(gridDim.x) * kRowsPerCta;
     const int own = WARP ? static_cast<int>(threadIdx.x) / (WARP ? LANES : 1) : 0;  // the row within the CTA
     int64_t r = static_cast<int64_t>(blockIdx.x) * kRowsPerCta + own;
+    // CENTER: the next row's statistics (a load in front of each row is what its chain would begin with)
+    float rstd_next = 0.0f, mean_next = 0.0f;
+    auto statistics = [&](int64_t row) {
+        rstd_next = row < p.rows ? p.rstd[row] : 0.0f;
+        mean_next = row < p.rows ? p.mean[row] : 0.0f;
+    };
+    if (CENTER) statistics(r);
     const int second = LANES == 16 ? own & 1 : 0;  // the halves of a warp leave the loop together
     if (PRE) fetch(r);
     for (int k = 0; r - second < p.rows; r += step, ++k) {
         uint4 dv[V], hv[V], sv[V];
-        const float rstd = r < p.rows ? p.rstd[r] : 0.0f;
+        const float rstd = CENTER ? rstd_next : r < p.rows ? p.rstd[r] : 0.0f;
         const uint64_t rstd2 = pack_f32x2(rstd, rstd);
-        const float minus_mean = CENTER && r < p.rows ? -p.mean[r] : 0.0f;
+        const float minus_mean = CENTER ? -mean_next : 0.0f;
+        if (CENTER) statistics(r + step);
         const uint64_t minus_mean2 = pack_f32x2(minus_mean, minus_mean);
         uint64_t dot2 = 0ull, sum2 = 0ull;
 #pragma unroll
@@ -724,12 +802,23 @@ __global__ void __launch_bounds__(1024) norm_grad_finalize_kernel(const float* w
     }
 }
 
+// the sum of the bands that a gradient's kernel left
+template <bool CENTER>
+int launch_finalize(const NormGradParams& p, int bands, cudaStream_t stream) {
+    constexpr int sums = CENTER ? 2 : 1;
+    const dim3 grid(static_cast<unsigned>((p.cols + 31) / 32), CENTER && p.dbeta ? 2 : 1);
+    return launch_dependent_clusters(norm_grad_finalize_kernel, grid, 0, 1024, 0, stream, p.partials, bands, sums * p.cols,
+                                     p.cols, p.dgamma, p.dbeta, p.accumulate) == cudaSuccess
+               ? 0
+               : -3;
+}
+
 // T threads per CTA (a warp per row: 256), up to `per_sm` CTAs per SM: each leaves
 // one band of partial sums.  (They run at once, but for up to 256 columns, where
 // registers let two of the four.)
-template <bool CENTER, int V, int MAXT, bool SMEM, bool PRE, int LANES>
+template <bool CENTER, int V, int MAXT, bool SMEM, bool PRE, int LANES, int MINB = 1>
 int launch_grad(const NormGradParams& p, int T, int num_sms, int per_sm, cudaStream_t stream) {
-    auto kern = norm_grad_kernel<CENTER, V, MAXT, SMEM, PRE, LANES>;
+    auto kern = norm_grad_kernel<CENTER, V, MAXT, SMEM, PRE, LANES, MINB>;
     constexpr int rows_per_cta = LANES ? 256 / (LANES ? LANES : 1) : 1;
     constexpr int sums = CENTER ? 2 : 1;
     const size_t smem = SMEM || LANES ? static_cast<size_t>(p.cols) * 4 * (SMEM ? sums : rows_per_cta) : 0;
@@ -743,11 +832,7 @@ int launch_grad(const NormGradParams& p, int T, int num_sms, int per_sm, cudaStr
     const int bands = static_cast<int>(want < cap ? want : cap);
     if (launch_dependent(kern, static_cast<unsigned>(bands), static_cast<unsigned>(T), smem, stream, p) != cudaSuccess)
         return -3;
-    const dim3 grid(static_cast<unsigned>((p.cols + 31) / 32), CENTER && p.dbeta ? 2 : 1);
-    return launch_dependent_clusters(norm_grad_finalize_kernel, grid, 0, 1024, 0, stream, p.partials, bands, sums * p.cols,
-                                     p.cols, p.dgamma, p.dbeta, p.accumulate) == cudaSuccess
-               ? 0
-               : -3;
+    return launch_finalize<CENTER>(p, bands, stream);
 }
 
 }  // namespace
