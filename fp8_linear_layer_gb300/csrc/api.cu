@@ -1238,7 +1238,7 @@ int fp8_gemm_gated_dgrad(int64_t M, int64_t N, int64_t K, const fp8ll_operand_t*
     p.total_tiles = p.tiles_per_group;
     p.out = out_bf16;
     p.aux = const_cast<void*>(aux_bf16);
-    return launch_gemm_gated(maps, p, gated_epi(act, true), gemm_linear_parts(p), reinterpret_cast<cudaStream_t>(stream),
+    return launch_gemm_gated(maps, p, gated_epi(act, true), gemm_gated_grad_parts(p), reinterpret_cast<cudaStream_t>(stream),
                              grid_for(p, dev)) == 0
                ? FP8LL_OK
                : FP8LL_ERR_LAUNCH;
@@ -1256,7 +1256,7 @@ int fp8_mx_gemm_gated_dgrad(int64_t M, int64_t N, int64_t K, const fp8ll_mx_oper
     p.aux = const_cast<void*>(aux_bf16);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const int epi = gated_epi(act, true);
-    rc = launch_gemm_mx_splits(p) ? launch_gemm_mx_split(maps, p, epi, s) : launch_gemm_mx(maps, p, epi, s);
+    rc = launch_gemm_mx_splits_gates(p) ? launch_gemm_mx_split(maps, p, epi, s) : launch_gemm_mx(maps, p, epi, s);
     return rc == 0 ? FP8LL_OK : FP8LL_ERR_LAUNCH;
 }
 
@@ -1273,7 +1273,7 @@ int fp8_tensor_gemm_gated_dgrad(int64_t M, int64_t N, int64_t K, const fp8ll_ten
     p.aux = const_cast<void*>(aux_bf16);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const int epi = gated_epi(act, true);
-    rc = launch_gemm_tensor_splits(p) ? launch_gemm_tensor_split(maps, p, epi, s) : launch_gemm_tensor(maps, p, epi, s);
+    rc = launch_gemm_tensor_splits_gates(p) ? launch_gemm_tensor_split(maps, p, epi, s) : launch_gemm_tensor(maps, p, epi, s);
     return rc == 0 ? FP8LL_OK : FP8LL_ERR_LAUNCH;
 }
 

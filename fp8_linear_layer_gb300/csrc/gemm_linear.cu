@@ -60,10 +60,14 @@ static int split_slots() {
 //   1000 x 2111 over 768    14.3 / 19.5   13.4 / 15.4
 //   1000 x 2110 over 768    11.8 / 15.5   12.2 / 14.0
 int gemm_linear_parts(const GemmParams& p) {
-    const int nkb = p.groups[0].nkb;
     const bool odd_rows = p.N % 8 != 0;
-    if (nkb >= (odd_rows ? 6 : 16) && p.total_tiles <= split_slots<4>()) return 4;
-    if (nkb >= (odd_rows ? 6 : 12) && p.total_tiles <= split_slots<2>()) return 2;
+    return gemm_parts(p, odd_rows ? 6 : 16, odd_rows ? 6 : 12);
+}
+
+int gemm_parts(const GemmParams& p, int blocks4, int blocks2) {
+    const int nkb = p.groups[0].nkb;
+    if (nkb >= blocks4 && p.total_tiles <= split_slots<4>()) return 4;
+    if (nkb >= blocks2 && p.total_tiles <= split_slots<2>()) return 2;
     return 1;
 }
 

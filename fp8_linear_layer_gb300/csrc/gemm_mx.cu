@@ -458,6 +458,10 @@ bool launch_gemm_mx_splits(const GemmParams& p) {
     return split_pays(p, launch_mx_impl_slots<kEpiLinear, 2>());
 }
 
+bool launch_gemm_mx_splits_gates(const GemmParams& p) {
+    return split_gates_pays(p, launch_mx_impl_slots<kEpiLinear, 2>());
+}
+
 int launch_gemm_mx_split(const TensorMaps& maps, const GemmParams& p, int epi, cudaStream_t stream) {
     switch (epi) {
         case kEpiLinear: return launch_mx_impl<kEpiLinear, 2>(maps, p, stream);

@@ -373,6 +373,10 @@ bool launch_gemm_tensor_splits(const GemmParams& p) {
     return split_pays(p, launch_tensor_impl_slots<kEpiLinear, 2>());
 }
 
+bool launch_gemm_tensor_splits_gates(const GemmParams& p) {
+    return split_gates_pays(p, launch_tensor_impl_slots<kEpiLinear, 2>());
+}
+
 int launch_gemm_tensor_split(const TensorMaps& maps, const GemmParams& p, int epi, cudaStream_t stream) {
     switch (epi) {
         case kEpiLinear: return launch_tensor_impl<kEpiLinear, 2>(maps, p, stream);

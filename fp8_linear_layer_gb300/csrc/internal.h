@@ -49,15 +49,21 @@ int launch_gemm_tensor(const TensorMaps& maps, const GemmParams& p, int epi, cud
 // 1x128: over how many CTAs of a cluster the K blocks of each tile are split
 // (1: not), and the kernel that does it (linear epilogues alone)
 int gemm_linear_parts(const GemmParams& p);
+// the same where four (two) parts pay from this many K blocks on
+int gemm_parts(const GemmParams& p, int blocks4, int blocks2);
 int launch_gemm_linear_parts(const TensorMaps& maps, const GemmParams& p, int epi, int parts, cudaStream_t stream);
 // The same with the K blocks of each tile split over two pairs, for the linear
 // epilogues: whether that pays for these sizes, and the launch.
 bool launch_gemm_mx_splits(const GemmParams& p);
 bool launch_gemm_tensor_splits(const GemmParams& p);
+// and for the gated gradient's
+bool launch_gemm_mx_splits_gates(const GemmParams& p);
+bool launch_gemm_tensor_splits_gates(const GemmParams& p);
 int launch_gemm_mx_split(const TensorMaps& maps, const GemmParams& p, int epi, cudaStream_t stream);
 int launch_gemm_tensor_split(const TensorMaps& maps, const GemmParams& p, int epi, cudaStream_t stream);
 // The gated product and its data gradient (kEpiGated*), whole and, where K is
 // split, as launch_gemm_linear_parts.
+int gemm_gated_grad_parts(const GemmParams& p);
 int launch_gemm_gated(const TensorMaps& maps, const GemmParams& p, int epi, int parts, cudaStream_t stream, int grid);
 int launch_bgrad_finalize(const float* ws, int64_t num_bands, int64_t N, float* bgrad, cudaStream_t stream,
                           int num_sms);

@@ -120,4 +120,14 @@ inline bool split_pays(const GemmParams& p, int slots) {
     return p.total_tiles <= slots && p.groups[0].nkb >= (p.N % 8 != 0 ? 6 : 16);
 }
 
+// The gated gradient, whose rows are dear (two read and two written for one of the
+// linear GEMM's), earlier.  us, split / whole, MXFP8 | per tensor:
+//   1000 x 2048 over 1024  12.0 / 12.6 | 11.5 / 12.8
+//                     512  11.1 / 11.2 | 10.7 / 11.4
+//   300 x 1024 over 1024   10.8 / 12.2 | 10.4 / 12.5
+inline constexpr int kGatesSplitBlocks = 8;
+inline bool split_gates_pays(const GemmParams& p, int slots) {
+    return p.total_tiles <= slots && p.groups[0].nkb >= kGatesSplitBlocks;
+}
+
 }  // namespace fp8ll
