@@ -185,6 +185,21 @@ bool encode_codes(const uint8_t* q, int64_t ld_q, int64_t rows, int64_t kext, ui
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The same codes for an operand whose rows are a multiple of 8, in boxes of two
+// neighbouring rows out of every 8: kOrderedBox rows, for the kernels that order B's
+// rows by the places of the sums' columns.
+bool encode_ordered(const uint8_t* q, int64_t ld_q, int64_t rows, int64_t kext, CUtensorMap* qmap) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return false;
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(kext), 8, static_cast<cuuint64_t>(rows / 8)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld_q), 8 * static_cast<cuuint64_t>(ld_q)};
+    const cuuint32_t box[3] = {128, 2, kOrderedBox / 2};
+    return enc(qmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(q), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // TMA descriptor for an MXFP8 scale-atom array (512-byte atoms, the MX cast's
 // layout) viewed as rows of 128 32-bit words: boxes of `atoms` whole atoms.
 bool encode_sf_atoms(const uint8_t* sf, int64_t num_atoms, uint32_t atoms, CUtensorMap* map) {
@@ -388,7 +403,8 @@ static void gated_tiles(GemmParams& p, int64_t N, bool pairs) {
     p.total_tiles = p.tiles_per_group;
 }
 
-static int gated_epi(int act, bool grad) {
+static int gated_epi(int act, bool grad, bool ordered = false) {
+    if (ordered) return act == FP8LL_ACT_GELU ? kEpiGatedGeluGradOrdered : kEpiGatedSiluGradOrdered;
     if (grad) return act == FP8LL_ACT_GELU ? kEpiGatedGeluGrad : kEpiGatedSiluGrad;
     return act == FP8LL_ACT_GELU ? kEpiGatedGelu : kEpiGatedSilu;
 }
@@ -1238,7 +1254,10 @@ int fp8_gemm_gated_dgrad(int64_t M, int64_t N, int64_t K, const fp8ll_operand_t*
     p.total_tiles = p.tiles_per_group;
     p.out = out_bf16;
     p.aux = const_cast<void*>(aux_bf16);
-    return launch_gemm_gated(maps, p, gated_epi(act, true), gemm_gated_grad_parts(p), reinterpret_cast<cudaStream_t>(stream),
+    const int parts = gemm_gated_grad_parts(p);
+    const bool ordered = parts == 1 && gemm_gated_grad_ordered(p);
+    if (ordered && !encode_ordered(B->q, B->ld_q, N, K, &maps.b)) return FP8LL_ERR_LAUNCH;
+    return launch_gemm_gated(maps, p, gated_epi(act, true, ordered), parts, reinterpret_cast<cudaStream_t>(stream),
                              grid_for(p, dev)) == 0
                ? FP8LL_OK
                : FP8LL_ERR_LAUNCH;
@@ -1269,10 +1288,11 @@ int fp8_tensor_gemm_gated_dgrad(int64_t M, int64_t N, int64_t K, const fp8ll_ten
     DeviceInfo* dev = nullptr;
     int rc = tensor_setup(M, N, K, A, B, maps, p, &dev);
     if (rc != FP8LL_OK) return rc;
+    if (!encode_ordered(B->q, B->ld_q, N, K, &maps.b)) return FP8LL_ERR_LAUNCH;
     p.out = out_bf16;
     p.aux = const_cast<void*>(aux_bf16);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const int epi = gated_epi(act, true);
+    const int epi = gated_epi(act, true, true);
     rc = launch_gemm_tensor_splits_gates(p) ? launch_gemm_tensor_split(maps, p, epi, s) : launch_gemm_tensor(maps, p, epi, s);
     return rc == 0 ? FP8LL_OK : FP8LL_ERR_LAUNCH;
 }

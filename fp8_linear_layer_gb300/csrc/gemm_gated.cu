@@ -13,7 +13,8 @@
 // 1013 us (1899 TFLOP/s), with Z 1071; MXFP8 597 and 624, per tensor 556 and 640.
 // Gradient: four bytes read and four written per output of the product, which an
 // epilogue of two warps per scheduler handles a step at a time (7.5 us a tile, of 26):
-// 8192 x 14336 over 4096, 629 us (1530 TFLOP/s), MXFP8 387, per tensor 376.
+// 8192 x 14336 over 4096, 629 us (1530 TFLOP/s), MXFP8 387.  With B's rows ordered it
+// needs no shuffles: per tensor 351 (with them 376).
 #include "gemm_kernel.cuh"
 
 namespace fp8ll {
@@ -45,12 +46,21 @@ static int launch(const TensorMaps& maps, const GemmParams& p, int parts, cudaSt
 //                     512  11.0   11.1
 int gemm_gated_grad_parts(const GemmParams& p) { return gemm_parts(p, kGatesSplitBlocks, kGatesSplitBlocks); }
 
+// The ordered epilogue takes 5 us a tile instead of 7.5, but its K loop gets registers
+// that need moves: 0.66 us a block instead of 0.58.  8192 x 14336, us, ordered / not:
+//   over 128    156 / 214        over 2048   384 / 403
+//   over 1024   259 / 294        over 4096   640 / 628
+// (epilogues of other shapes moved these by a few per cent and not the crossing point)
+bool gemm_gated_grad_ordered(const GemmParams& p) { return p.groups[0].nkb <= 24; }
+
 int launch_gemm_gated(const TensorMaps& maps, const GemmParams& p, int epi, int parts, cudaStream_t stream, int grid) {
     switch (epi) {
         case kEpiGatedSilu: return launch<kEpiGatedSilu>(maps, p, parts, stream, grid);
         case kEpiGatedGelu: return launch<kEpiGatedGelu>(maps, p, parts, stream, grid);
         case kEpiGatedSiluGrad: return launch<kEpiGatedSiluGrad>(maps, p, parts, stream, grid);
         case kEpiGatedGeluGrad: return launch<kEpiGatedGeluGrad>(maps, p, parts, stream, grid);
+        case kEpiGatedSiluGradOrdered: return launch_gemm_impl<kEpiGatedSiluGradOrdered>(maps, p, stream, grid);
+        case kEpiGatedGeluGradOrdered: return launch_gemm_impl<kEpiGatedGeluGradOrdered>(maps, p, stream, grid);
         default: return -1;
     }
 }

@@ -131,11 +131,22 @@ constexpr bool is_gated() {
 }
 template <int EPI>
 constexpr bool is_gated_grad() {
-    return EPI == kEpiGatedSiluGrad || EPI == kEpiGatedGeluGrad;
+    return EPI == kEpiGatedSiluGrad || EPI == kEpiGatedGeluGrad || EPI == kEpiGatedSiluGradOrdered ||
+           EPI == kEpiGatedGeluGradOrdered;
 }
 template <int EPI>
 constexpr bool is_gelu_gate() {
-    return EPI == kEpiGatedGelu || EPI == kEpiGatedGeluGrad;
+    return EPI == kEpiGatedGelu || EPI == kEpiGatedGeluGrad || EPI == kEpiGatedGeluGradOrdered;
+}
+// The accumulators' layout leaves a lane with columns 8 c + 2 (lane % 4) + {0, 1} of
+// every chunk c of 8 columns.  Where B's rows are taken in another order, so are its
+// columns: row 32 g + 8 q + 2 j + e of each 128 of B (j, q and g below 4) goes to place
+// 32 j + 8 g + 2 q + e, four loads of pairs of rows with a stride of 8, and lane
+// q of a quad has the eight neighbouring columns 32 g + 8 q .. + 7 in chunks g, 4 + g,
+// 8 + g and 12 + g: its memory accesses are vectors without a shuffle.
+template <int EPI>
+constexpr bool ordered_columns() {
+    return EPI == kEpiGatedSiluGradOrdered || EPI == kEpiGatedGeluGradOrdered;
 }
 // launched to overlap the end of the kernel before
 template <int EPI>
@@ -973,6 +984,55 @@ __device__ __forceinline__ void store_gated_grad(const GemmParams& p, int row0, 
     }
 }
 
+// The same where the lane's sums of a step are of the columns of its vectors: no
+// shuffles.  A row at a time, the next row's vectors on their way.
+template <bool GELU, int ROWS = 4>
+__device__ __forceinline__ void store_gated_grad_ordered(const GemmParams& p, int row0, int col0,
+                                                         const uint64_t (&acc)[4 * kChunks]) {
+    constexpr int kSteps = kChunks / 4;
+    uint16_t* out = static_cast<uint16_t*>(p.out);
+    const uint16_t* aux = static_cast<const uint16_t*>(p.aux);
+    const int cq = (col0 >> 1) & 3;
+    const int cbase = col0 - 2 * cq;
+    if (cbase >= p.N) return;
+    uint4 gate[kSteps], up[kSteps];
+    auto fetch = [&](int g, int r) {
+        const int64_t row = row0 + 8 * r;
+        gate[g] = up[g] = make_uint4(0, 0, 0, 0);
+        if (row < p.M) {
+            const uint16_t* z = aux + 2 * row * p.N + cbase + 8 * (4 * g + cq);
+            gate[g] = *reinterpret_cast<const uint4*>(z);
+            up[g] = *reinterpret_cast<const uint4*>(z + p.N);
+        }
+    };
+#pragma unroll
+    for (int g = 0; g < kSteps; ++g) fetch(g, 0);
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+#pragma unroll
+        for (int g = 0; g < kSteps; ++g) {
+            uint32_t gw[4] = {gate[g].x, gate[g].y, gate[g].z, gate[g].w};  // Z, until dZ replaces it
+            uint32_t uw[4] = {up[g].x, up[g].y, up[g].z, up[g].w};
+            if (r + 1 < ROWS) fetch(g, r + 1);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint64_t c = acc[4 * (4 * j + g) + r];
+                uint64_t y, d;
+                gate_grad2<GELU>(pack_f32x2(bf16_lo(gw[j]), bf16_hi(gw[j])), y, d);
+                const float2 a = unpack_f32x2(mul_f32x2(mul_f32x2(c, pack_f32x2(bf16_lo(uw[j]), bf16_hi(uw[j]))), d));
+                const float2 b = unpack_f32x2(mul_f32x2(c, y));
+                gw[j] = pack_bf16x2(a.x, a.y);
+                uw[j] = pack_bf16x2(b.x, b.y);
+            }
+            const int64_t row = row0 + 8 * r;
+            if (row >= p.M) continue;
+            uint16_t* o = out + 2 * row * p.N + cbase + 8 * (4 * g + cq);
+            *reinterpret_cast<uint4*>(o) = make_uint4(gw[0], gw[1], gw[2], gw[3]);
+            *reinterpret_cast<uint4*>(o + p.N) = make_uint4(uw[0], uw[1], uw[2], uw[3]);
+        }
+    }
+}
+
 // asks for Z of a thread's tile rows in L2 while the K loop runs, as prefetch_residual
 __device__ __forceinline__ void prefetch_gates(const GemmParams& p, int prow, int pc0) {
     if (prow >= p.M || pc0 >= p.N) return;
@@ -1157,7 +1217,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint32_t fb = smem_addr(&sm.full[s]);
                         mbar_arrive_expect_tx(fb, kBM * kBK + kBN * kBK);
                         tma_load_2d(smem_addr(sm.a[s]), &maps.a, fb, kbg * kBK, m0);
-                        tma_load_2d(smem_addr(sm.b[s]), &maps.b, fb, kbg * kBK, n0);
+                        if (ordered_columns<EPI>()) {  // see there
+#pragma unroll
+                            for (int i = 0; i < kBN / kOrderedBox; ++i)
+                                tma_load_3d(smem_addr(sm.b[s] + i * kOrderedBox * kBK), &maps.b, fb, kbg * kBK, 2 * (i & 3),
+                                            n0 / 8 + 16 * (i >> 2));
+                        } else {
+                            tma_load_2d(smem_addr(sm.b[s]), &maps.b, fb, kbg * kBK, n0);
+                        }
                         if (is_gated<EPI>())  // boxes of 128 rows: the gate's, and the up projection's
                             tma_load_2d(smem_addr(sm.b[s] + kGatedN * kBK), &maps.b, fb, kbg * kBK, p.N + n0);
                         ++n_issued;
@@ -1330,7 +1397,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float s = sm.sa[ss][q * 32 + g8 + 8 * r];
                     sa2[r] = pack_f32x2(s, s);
                 }
-                const float* sbp = &sm.sb[ss][half * kGroupN + 2 * cq];
+                constexpr bool kOrdered = ordered_columns<EPI>();
+                const float* sbp = &sm.sb[ss][half * kGroupN + (kOrdered ? 8 : 2) * cq];
 #pragma unroll
                 for (int h = 0; h < 4; ++h) {
                     uint64_t plo[8], phi[8];
@@ -1345,8 +1413,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int c = 4 * h + i;
-                        const uint64_t sb =
-                            *reinterpret_cast<const uint64_t*>(sbp + 8 * c + (h >= 2 ? gate_skip<EPI>() : 0));
+                        const uint64_t sb = *reinterpret_cast<const uint64_t*>(
+                            sbp + (kOrdered ? 32 * i + 2 * h : 8 * c) + (h >= 2 ? gate_skip<EPI>() : 0));
                         acc[4 * c + 0] = fma_f32x2(plo[2 * i], mul_f32x2(sa2[0], sb), acc[4 * c + 0]);
                         acc[4 * c + 1] = fma_f32x2(plo[2 * i + 1], mul_f32x2(sa2[1], sb), acc[4 * c + 1]);
                         acc[4 * c + 2] = fma_f32x2(phi[2 * i], mul_f32x2(sa2[2], sb), acc[4 * c + 2]);
@@ -1394,6 +1462,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int col0 = n0 + half * kGroupN + 2 * cq;
             if (is_gated<EPI>()) {
                 store_gated<is_gelu_gate<EPI>()>(p, row0, col0, acc);
+            } else if (ordered_columns<EPI>()) {
+                store_gated_grad_ordered<is_gelu_gate<EPI>()>(p, row0, col0, acc);
             } else if (is_gated_grad<EPI>()) {
                 store_gated_grad<is_gelu_gate<EPI>()>(p, row0, col0, acc);
             } else if (EPI == kEpiWgrad) {

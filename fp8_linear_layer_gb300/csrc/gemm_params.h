@@ -10,6 +10,7 @@ constexpr int kMaxGroups = 256;
 constexpr int kTileM = 128;  // GEMM output tile rows
 constexpr int kTileN = 256;  // GEMM output tile columns
 constexpr int kGatedN = 128;  // of which the gated product makes this many outputs
+constexpr int kOrderedBox = 32;  // rows of B in a load that orders them
 
 enum EpiKind : int {
     kEpiNone = 0,
@@ -33,6 +34,8 @@ enum EpiKind : int {
     // dZ [M][2 N] = (C Z_up act'(Z_gate), C act(Z_gate)), aux = Z
     kEpiGatedSiluGrad = 15,
     kEpiGatedGeluGrad = 16,
+    kEpiGatedSiluGradOrdered = 17,  // B's rows ordered by the places of the sums' columns
+    kEpiGatedGeluGradOrdered = 18,
 };
 
 // One schedulable group of output tiles: all tiles of a group share the same

@@ -139,7 +139,14 @@ __global__ void __cluster_dims__(2 * SPLIT, 1, 1) __launch_bounds__(kThreads, 1)
                         if (leader) mbar_arrive_expect_tx(fb, 2 * kTpStageBytes);
                         const uint32_t fbl = mapa_shared(fb, lead);
                         tma_load_2d_pair(smem_addr(sm.a[s]), &maps.a, fbl, (kb_first + kb) * kBK, m0);
-                        tma_load_2d_pair(smem_addr(sm.b[s]), &maps.b, fbl, (kb_first + kb) * kBK, nb0);
+                        if (ordered_columns<EPI>()) {
+#pragma unroll
+                            for (int i = 0; i < kTpBRows / kOrderedBox; ++i)
+                                tma_load_3d_pair(smem_addr(sm.b[s] + i * kOrderedBox * kBK), &maps.b, fbl,
+                                                 (kb_first + kb) * kBK, 2 * i, nb0 / 8);
+                        } else {
+                            tma_load_2d_pair(smem_addr(sm.b[s]), &maps.b, fbl, (kb_first + kb) * kBK, nb0);
+                        }
                         ++n_issued;
                         ring_advance<kTpStages>(s, ph);
                     }
@@ -285,7 +292,7 @@ __global__ void __cluster_dims__(2 * SPLIT, 1, 1) __launch_bounds__(kThreads, 1)
             if (is_gated<EPI>()) {
                 store_gated<is_gelu_gate<EPI>(), 4 / SPLIT>(p, row0, col0, acc);
             } else if (is_gated_grad<EPI>()) {
-                store_gated_grad<is_gelu_gate<EPI>(), 4 / SPLIT>(p, row0, col0, acc);
+                store_gated_grad_ordered<is_gelu_gate<EPI>(), 4 / SPLIT>(p, row0, col0, acc);
             } else if (EPI == kEpiWgrad) {
                 store_wgrad(p, 0, row0, col0, acc);
             } else if (EPI == kEpiNone || EPI == kEpiBias || EPI == kEpiBiasGelu) {
@@ -387,8 +394,8 @@ int launch_gemm_tensor_split(const TensorMaps& maps, const GemmParams& p, int ep
         case kEpiLinearGeluOdd: return launch_tensor_impl<kEpiLinearGeluOdd, 2>(maps, p, stream);
         case kEpiGatedSilu: return launch_tensor_impl<kEpiGatedSilu, 2>(maps, p, stream);
         case kEpiGatedGelu: return launch_tensor_impl<kEpiGatedGelu, 2>(maps, p, stream);
-        case kEpiGatedSiluGrad: return launch_tensor_impl<kEpiGatedSiluGrad, 2>(maps, p, stream);
-        case kEpiGatedGeluGrad: return launch_tensor_impl<kEpiGatedGeluGrad, 2>(maps, p, stream);
+        case kEpiGatedSiluGradOrdered: return launch_tensor_impl<kEpiGatedSiluGradOrdered, 2>(maps, p, stream);
+        case kEpiGatedGeluGradOrdered: return launch_tensor_impl<kEpiGatedGeluGradOrdered, 2>(maps, p, stream);
         default: return -3;
     }
 }
@@ -409,8 +416,8 @@ int launch_gemm_tensor(const TensorMaps& maps, const GemmParams& p, int epi, cud
         case kEpiLinearGeluOdd: return launch_tensor_impl<kEpiLinearGeluOdd>(maps, p, stream);
         case kEpiGatedSilu: return launch_tensor_impl<kEpiGatedSilu>(maps, p, stream);
         case kEpiGatedGelu: return launch_tensor_impl<kEpiGatedGelu>(maps, p, stream);
-        case kEpiGatedSiluGrad: return launch_tensor_impl<kEpiGatedSiluGrad>(maps, p, stream);
-        case kEpiGatedGeluGrad: return launch_tensor_impl<kEpiGatedGeluGrad>(maps, p, stream);
+        case kEpiGatedSiluGradOrdered: return launch_tensor_impl<kEpiGatedSiluGradOrdered>(maps, p, stream);
+        case kEpiGatedGeluGradOrdered: return launch_tensor_impl<kEpiGatedGeluGradOrdered>(maps, p, stream);
         default: return -3;
     }
 }

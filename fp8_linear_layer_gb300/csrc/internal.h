@@ -64,6 +64,7 @@ int launch_gemm_tensor_split(const TensorMaps& maps, const GemmParams& p, int ep
 // The gated product and its data gradient (kEpiGated*), whole and, where K is
 // split, as launch_gemm_linear_parts.
 int gemm_gated_grad_parts(const GemmParams& p);
+bool gemm_gated_grad_ordered(const GemmParams& p);  // B's rows ordered (whole tiles only)
 int launch_gemm_gated(const TensorMaps& maps, const GemmParams& p, int epi, int parts, cudaStream_t stream, int grid);
 int launch_bgrad_finalize(const float* ws, int64_t num_bands, int64_t N, float* bgrad, cudaStream_t stream,
                           int num_sms);

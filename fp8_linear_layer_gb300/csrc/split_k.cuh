@@ -125,6 +125,7 @@ inline bool split_pays(const GemmParams& p, int slots) {
 //   1000 x 2048 over 1024  12.0 / 12.6 | 11.5 / 12.8
 //                     512  11.1 / 11.2 | 10.7 / 11.4
 //   300 x 1024 over 1024   10.8 / 12.2 | 10.4 / 12.5
+// (per tensor with shuffles; without, 11.0 and 10.2 split)
 inline constexpr int kGatesSplitBlocks = 8;
 inline bool split_gates_pays(const GemmParams& p, int slots) {
     return p.total_tiles <= slots && p.groups[0].nkb >= kGatesSplitBlocks;

@@ -66,6 +66,8 @@ SHAPES = [(1, 128, 128), (1, 256, 4096), (2, 384, 256), (3, 128, 896), (8, 640, 
           (17, 384, 384), (33, 1152, 512), (64, 128, 1024), (50, 256, 4096), (100, 256, 640), (129, 128, 256),
           (300, 512, 384), (150, 256, 4096), (257, 128, 2048), (128, 1024, 4096), (800, 2176, 256), (1000, 1920, 128),
           (1000, 896, 2048), (900, 1152, 4096), (650, 1408, 2304), (2600, 1792, 384)]
+# gradients of whole tiles, on both sides of the sum's length at which B's rows are ordered
+WHOLE = [(1300, 2176, 2944), (1250, 2176, 3200)]
 
 
 @pytest.mark.parametrize("recipe", RECIPES)
@@ -89,7 +91,7 @@ def test_forward(fp8, recipe, M, N, K):
 
 
 @pytest.mark.parametrize("recipe", RECIPES)
-@pytest.mark.parametrize("M,N,K", [s for s in SHAPES if s[0] > 8 or s[0] == 1])
+@pytest.mark.parametrize("M,N,K", [s for s in SHAPES if s[0] > 8 or s[0] == 1] + WHOLE)
 def test_gradient(fp8, recipe, M, N, K):
     seed = M + N + K
     A, B, acc, S = operands(fp8, recipe, workloads.normal_bf16((M, K), seed, "a", std=0.02),
