@@ -931,9 +931,9 @@ __device__ __forceinline__ void store_gated(const GemmParams& p, int row0, int c
 // in, each lane its own before it writes them: out may be Z's own buffer.  A row's
 // vectors of the next 32 columns are on their way while the ones before are used.
 // (Z and dZ by TMA through shared memory, in the accumulators' order, take half of
-// the instructions, but their way there competes with the operands' during the K
-// loop: 8192 x 14336 over 128 169 us instead of 214, over 4096 671 instead of 629.
-// Rows together instead of one by one cost the K loop its registers: 746.)
+// the instructions, 8192 x 14336 over 128 169 us instead of 214, but the K loop comes
+// out slower: over 4096 671 instead of 629.  Rows together instead of one by one: 746.
+// Z in words, without the shuffles in front: 725.)
 template <bool GELU, int ROWS = 4>
 __device__ __forceinline__ void store_gated_grad(const GemmParams& p, int row0, int col0,
                                                  const uint64_t (&acc)[4 * kChunks]) {
