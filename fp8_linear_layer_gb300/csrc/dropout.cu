@@ -12,15 +12,18 @@
 // floor(p 2^32) / 2^32, and the ten rounds are paid once for four elements.
 // Scaling and addition are one fused multiply-add, rounded to bf16 once.
 //
-// Bound by HBM: 8192 x 4096 with residual 34.1 us, 0.88 of the measured copy rate
+// Bound by HBM: 8192 x 4096 with residual 33.1 us, 0.91 of the measured copy rate
 // (a mask in memory would cost a byte or a bit an element twice more).  Each thread
 // has four 16-byte vectors of both inputs in flight, or one where there are too few
 // to give every SM as many: the generator's chain of twenty products per group is
-// hidden by other threads.  CTAs are not persistent.  129 x 1001 takes 1.6 us.
+// hidden by other threads.  CTAs are not persistent; each asks for the inputs of the CTA
+// half as many behind it as run at once, in L2 (34.1 us without; 16384 x 7168 108.7, with it
+// 102.8; as far behind as run at once 34.3, twice as far 37.1).  129 x 1001 takes 1.6 us.
 #include <cuda_runtime.h>
 
 #include "common.cuh"
 #include "dropout.h"
+#include "l2_prefetch.cuh"
 #include "launch.cuh"
 
 namespace fp8ll {
@@ -85,6 +88,13 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const __grid_constant
     const int64_t n = p.rows * p.cols, vectors = n / 8;
     const uint32_t per_row = static_cast<uint32_t>(p.cols / 8);
     const int64_t first = static_cast<int64_t>(blockIdx.x) * (kThreads * U) + threadIdx.x;
+    if (FLAT && U > 1 && threadIdx.x == 0) {
+        const int64_t later = (blockIdx.x + p.ahead) * (kThreads * U);
+        if (later + kThreads * U <= vectors) {
+            prefetch_l2_rows(p.x + 8 * later, 16 * kThreads * U);
+            if (p.res) prefetch_l2_rows(p.res + 8 * later, 16 * kThreads * U);
+        }
+    }
     uint4 x[U], res[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -127,6 +137,7 @@ bool vectors_fit(const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 1
 
 int launch_dropout(const DropoutParams& given, cudaStream_t stream, int num_sms) {
     DropoutParams p = given;
+    p.ahead = 2 * static_cast<int64_t>(num_sms);
     const int64_t n = p.rows * p.cols;
     const bool flat = p.rows == 1 || (p.ldx == p.cols && (!p.res || p.ldr == p.cols));
     if (flat) {

@@ -13,6 +13,7 @@ struct DropoutParams {
     const uint16_t* res;  // bf16 [rows][ldr] or null
     uint16_t* out;        // bf16 [rows][cols]
     int64_t rows, cols, ldx, ldr;
+    int64_t ahead;       // a CTA asks for the inputs of the one so many behind it in L2
     uint32_t threshold;  // words below it drop their element
     float scale;         // of a kept element: 1 / (1 - p)
     uint32_t key0, key1;

@@ -8,8 +8,8 @@
 // The deviations are summed in a second pass over the row, which stays in
 // registers, so that a mean far from zero costs no digits.
 //
-// Bound by HBM where there are rows enough: 8192 x 4096 with residual on 1x128 41.6
-// us, 0.85 of the measured copy rate; the columns kernel 20 us more at that size
+// Bound by HBM where there are rows enough: 8192 x 4096 with residual on 1x128 40.6
+// us, 0.87 of the measured copy rate; the columns kernel 20 us more at that size
 // (half of h from L2, and a pass over a tile for the maxima in front of the cast's).
 // The backward pass 16384 x 7168 with the residual's gradient 169 us, 0.83: one row
 // at a time per SM there, 1260 cycles of instructions in the 2950 that it takes.  (Two

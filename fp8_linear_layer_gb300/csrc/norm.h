@@ -19,6 +19,7 @@ struct NormParams {
     const uint16_t* gamma;     // bf16 [cols]
     const uint16_t* beta;      // layer norm: bf16 [cols] or null
     int64_t rows, cols, ldx, ldr;
+    int64_t ahead;  // a CTA asks for the row so many behind its own in L2 (0: for none)
     float eps;
     uint16_t* h;    // bf16 [rows][cols] or null: x + residual
     float* mean;    // layer norm: [rows]

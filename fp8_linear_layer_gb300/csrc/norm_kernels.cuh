@@ -16,6 +16,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "l2_prefetch.cuh"
 #include "launch.cuh"
 #include "mx_rule.cuh"
 #include "norm.h"
@@ -179,6 +180,14 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_rows_kernel(const __grid_cons
     auto load_beta = [&](int v) { return p.beta ? load_weight(p.beta, v) : zero; };
     int64_t r = blockIdx.x;
     fetch(r);
+    if (!PRE && threadIdx.x == 0) {  // row_alone: L2 has the row when its CTA starts
+        const int64_t later = r + p.ahead;
+        if (p.ahead > 0 && later < p.rows) {
+            const uint32_t bytes = static_cast<uint32_t>(2 * p.cols);
+            prefetch_l2_rows(p.x + later * p.ldx, bytes);
+            if (p.residual) prefetch_l2_rows(p.residual + later * p.ldr, bytes);
+        }
+    }
     if (RECIPE == kRecipeTensor && CENTER) tensor_scale();  // the row is on its way meanwhile
     constexpr bool BREG = GREG && CENTER && V == 1;
     uint4 gv[GREG ? V : 1], bv[BREG ? V : 1];
@@ -515,26 +524,32 @@ void row_shape(int64_t cols, int& T, int& V) {
 // where the next row's would leave 512, and other rows' CTAs hide what a row waits
 // for (its loads, two sums).  us, this / persistent CTAs with the next row ahead
 // (rows x cols, with residual; 1x128 | MXFP8 | per tensor):
-//   4096 x 8192  43.0 / 48.8 | 47.4 / 53.7 | 45.6 / 56.5
-//   777 x 7168   10.9 / 13.0 | 12.3 / 15.1 | 13.2 / 14.2
+//   4096 x 8192  41.9 / 48.8 | 46.2 / 53.7 | 42.9 / 56.5
+//   777 x 7168   10.6 / 13.0 | 11.7 / 15.1 | 12.0 / 14.2
 // where those have two vectors a thread or one, and 768 or more threads on an SM:
-//   8192 x 4096  41.2 / 43.8 | 45.4 / 47.4 | 43.0 / 41.0
+//   8192 x 4096  40.6 / 43.8 | 45.4 / 47.4 | 43.0 / 41.0
 //   16384 x 1024 22.6 / 24.3 | 24.9 / 27.0 | 23.8 / 24.0
 //   777 x 2048    4.2 /  4.3 |  5.0 /  4.7 |  5.6 /  4.6
 //   400 x 4096    4.2 /  4.0 |  5.8 /  4.6 |  5.4 /  4.6
 // The number of rows does not count: a row's sums are added in one order in any batch.
+// From 128 threads a row on, a CTA asks for the inputs of the row half as many CTAs
+// behind it as run at once, in L2: 16384 x 7168 on 1x128 141 us without, 134 with it,
+// 8192 x 4096 41.5 and 40.6 (as far behind as run at once: 135 and 42.2, twice as far 140;
+// 8192 x 2048 23.1 either way).
 inline bool row_alone(int64_t cols, int recipe) {
     return cols > (recipe == kRecipeBlock ? 512 : 4096);
 }
 
 template <bool CENTER, int FMT, int RECIPE>
-int launch_norm(const NormParams& p, cudaStream_t stream, int num_sms) {
+int launch_norm(const NormParams& given, cudaStream_t stream, int num_sms) {
+    NormParams p = given;
     int T, V;
     row_shape(p.cols, T, V);
     const bool alone = CENTER && row_alone(p.cols, RECIPE);
     if (alone) {
         V = 4;
         T = static_cast<int>(((p.cols / 8 + V - 1) / V + 31) / 32 * 32);
+        p.ahead = T < 128 ? 0 : static_cast<int64_t>(num_sms) * (T > 512 ? 1 : 512 / T);
     }
     // 768 (1024) threads of rows per SM; from 4224 columns on the RMS norm's 118 to 121
     // registers let only 512 run at once (at 7168 columns two CTAs of 224 threads, three
@@ -827,6 +842,10 @@ int launch_grad(const NormGradParams& p, int T, int num_sms, int per_sm, cudaStr
         static PerDevice allowed;
         if (allow_shared_memory(allowed, kern, CENTER ? kLayerNormMaxCols * 8 : kNormMaxCols * 4) != 0) return -3;
     }
+    // Few rows: fewer bands to add up.  Layer norm, us, two CTAs per SM / four (2048 columns) or six
+    // (1280): 600 rows 6.8 / 9.0 and 5.8 / 7.8, 1000 rows 8.5 / 9.9 and 7.7 / 8.5, 1400 rows 10.1 / 10.6
+    // and 8.9 / 9.9, 2000 rows 11.8 / 12.2 and 10.7 / 10.4, 4000 rows 20.1 / 17.6 and 17.5 / 13.8
+    if (CENTER && LANES == 0 && per_sm > 2 && p.rows <= 10 * static_cast<int64_t>(num_sms)) per_sm = 2;
     int64_t cap = static_cast<int64_t>(num_sms) * (per_sm < 1 ? 1 : per_sm);
     if (cap > kGradMaxBands) cap = kGradMaxBands;
     const int64_t want = (p.rows + rows_per_cta - 1) / rows_per_cta;
