@@ -47,7 +47,8 @@ static int launch(const TensorMaps& maps, const GemmParams& p, int parts, cudaSt
 int gemm_gated_grad_parts(const GemmParams& p) { return gemm_parts(p, kGatesSplitBlocks, kGatesSplitBlocks); }
 
 // The ordered epilogue takes 5 us a tile instead of 7.5, but the K loop in front of it
-// comes out with 296 instructions a warp and block instead of 280: 0.66 us for 0.58.  8192 x 14336, us, ordered / not:
+// comes out with 296 instructions a warp and block instead of 280: 0.66 us for 0.58.
+// 8192 x 14336, us, ordered / not:
 //   over 128    156 / 214        over 2048   384 / 403
 //   over 1024   259 / 294        over 4096   640 / 628
 // (epilogues of other shapes moved these by a few per cent and not the crossing point)
