@@ -168,6 +168,27 @@ def test_stream_in_place(fp8, onto):
     assert torch.equal(got.rstd, want.rstd) and torch.equal(r2 if onto == "x" else x2, r if onto == "x" else x)
 
 
+@pytest.mark.parametrize("rows,cols", [(702, 7168), (1300, 4096), (330, 16384)])
+def test_more_rows_than_run_at_once(fp8, rows, cols):
+    # wide rows, whose inputs are asked for ahead: packed, with gaps, and with the stream in the place of x
+    x, r, (gamma, beta) = stream(rows, cols, 13), stream(rows, cols, 14), weights(cols, 15)
+    parts = [fp8.layernorm_quantize(x[i:i + 97], gamma, beta, EPS, fp8.E4M3, residual=r[i:i + 97])
+             for i in range(0, rows, 97)]
+    room = torch.full((rows, cols + 8), float("nan"), dtype=torch.bfloat16, device="cuda")
+    room[:, :cols] = x
+    place = x.clone()
+    out = fp8.empty_layernorm(rows, cols, fp8.E4M3, residual=True)
+    out.h = place
+    for got in (fp8.layernorm_quantize(x, gamma, beta, EPS, fp8.E4M3, residual=r),
+                fp8.layernorm_quantize(room[:, :cols], gamma, beta, EPS, fp8.E4M3, residual=r),
+                fp8.layernorm_quantize(place, gamma, beta, EPS, fp8.E4M3, residual=r, out=out)):
+        torch.cuda.synchronize()
+        for name in ("h", "mean", "rstd"):
+            assert torch.equal(getattr(got, name), torch.cat([getattr(p, name) for p in parts])), name
+        assert torch.equal(got.rows.q, torch.cat([p.rows.q for p in parts]))
+        assert torch.equal(got.rows.scale[:, :rows], torch.cat([p.rows.scale[:, :len(p.mean)] for p in parts], 1))
+
+
 @pytest.mark.parametrize("cols", [128, 896, 2048, 4096])
 def test_rows_with_nan_and_infinity_stay_alone(fp8, cols):
     rows = 640
@@ -267,7 +288,8 @@ def check_backward(got, dy, h, gamma, mean, rstd, res, before=None):
 
 @pytest.mark.parametrize("rows,cols", [(1, 8), (1, 4096), (2, 24), (7, 520), (333, 1000), (1000, 2048), (64, 7168),
                                        (5, 14336), (3, 16392), (4, 28672), (2500, 136), (5001, 128),
-                                       (700, 504), (31, 1024), (33, 8192), (9, 8200), (1300, 5000)])
+                                       (700, 504), (31, 1024), (33, 8192), (9, 8200), (1300, 5000), (1520, 1280),
+                                       (1531, 2048)])
 @pytest.mark.parametrize("with_residual", [False, True])
 def test_backward(fp8, rows, cols, with_residual):
     pad = 8 if rows % 2 else 0
