@@ -102,9 +102,10 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const __grid_constant
         if (v >= vectors) continue;
         int64_t ox = 8 * v, orr = 8 * v;
         if (!FLAT) {
-            const uint32_t r = static_cast<uint32_t>(v) / per_row, c = static_cast<uint32_t>(v) - r * per_row;
-            ox = r * p.ldx + 8 * c;
-            orr = r * p.ldr + 8 * c;
+            const uint32_t r = static_cast<uint32_t>(v) / per_row;
+            const int64_t c = 8 * static_cast<int64_t>(static_cast<uint32_t>(v) - r * per_row);  // from 2^32 on in wide rows
+            ox = r * p.ldx + c;
+            orr = r * p.ldr + c;
         }
         x[u] = __ldcs(reinterpret_cast<const uint4*>(p.x + ox));
         res[u] = p.res ? __ldcs(reinterpret_cast<const uint4*>(p.res + orr)) : make_uint4(0, 0, 0, 0);

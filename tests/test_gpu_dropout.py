@@ -170,6 +170,19 @@ def test_more_than_two_to_the_31_elements(fp8):
     assert torch.equal(got.view(-1)[-4096:] != 0, words)
 
 
+def test_rows_of_more_than_two_to_the_32_columns_with_gaps(fp8):
+    rows, cols, tail = 2, (1 << 32) + 8, 64
+    room = torch.zeros(rows, cols + 8, dtype=torch.bfloat16, device="cuda")  # 17 GB
+    x, res = room[:, :cols], room[:, 8:]  # each row of the residual lies 8 elements behind the row of x
+    room[:, -tail:] = matrix(rows, tail, 1)
+    got = fp8.dropout(x, 0.5, 21, 1, 1, residual=res)
+    for r in range(rows):
+        first = r * cols + cols - tail
+        kept = torch.from_numpy(last_words(first, tail, 21, 1, 1) >= np.uint64(2 ** 31)).cuda()
+        want = torch.where(kept, 2 * x[r, -tail:].float(), 0.0) + res[r, -tail:].float()  # p = 1/2: one rounding
+        assert torch.equal(got[r, -tail:], want.bfloat16())
+
+
 def last_words(first, n, seed, site, step):
     """Words first .. first + n - 1 (first a multiple of 4) without those before."""
     low, half = np.uint64(0xFFFFFFFF), np.uint64(32)
