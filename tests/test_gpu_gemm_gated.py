@@ -1,5 +1,7 @@
 """The gated product and its data gradient, in the three recipes, against the
 oracle's fp64 product."""
+import dataclasses
+
 import numpy as np
 import pytest
 import torch
@@ -285,3 +287,48 @@ def test_a_starved_pipeline_reports_and_returns(fp8, recipe, M, grad):
         y, _ = forward(fp8, recipe)(A, B)
         torch.cuda.synchronize()
         check_forward(y, None, acc, S, None, fp8.ACT_SILU)
+
+
+def cast(fp8, recipe, x, fmt):
+    if recipe == "tensor":
+        return fp8.tensor_quantize(x, fmt, fp8.tensor_amax(x))[0]
+    return (fp8.quantize if recipe == "block" else fp8.mx_quantize)(x, fmt)
+
+
+def spaced(t):
+    """The operand with NaN codes between its rows and NaN scales between those of its K blocks."""
+    rows, k = t.q.shape
+    q = torch.full((rows, k + 128), 0x7F, dtype=torch.uint8, device="cuda")  # NaN in both formats
+    q[:, :k] = t.q
+    scale = {}
+    if hasattr(t, "scale") and t.scale.dim() == 2:
+        kb, n = t.scale.shape
+        wide = torch.full((kb, n + 68), float("nan"), device="cuda")
+        wide[:, :n] = t.scale
+        scale = {"scale": wide[:, :n]}
+    return dataclasses.replace(t, q=q[:, :k], **scale)
+
+
+# few rows; tiles; tiles of which K is split; more tiles than run at once
+@pytest.mark.parametrize("recipe", RECIPES)
+@pytest.mark.parametrize("M,N,K", [(3, 384, 512), (50, 256, 4096), (300, 512, 384), (257, 128, 2048), (1300, 2176, 384)])
+def test_forward_of_operands_with_gaps(fp8, recipe, M, N, K):
+    A = cast(fp8, recipe, workloads.normal_bf16((M, K), 3, "a").cuda(), E4M3)
+    W = cast(fp8, recipe, weights(N, K, 3).cuda(), E4M3)
+    want = forward(fp8, recipe)(A, W, want_aux=True)
+    for a, w in ((spaced(A), W), (A, spaced(W)), (spaced(A), spaced(W))):
+        for got, packed in zip(forward(fp8, recipe)(a, w, want_aux=True), want):
+            assert torch.equal(got, packed) and not bool(got.isnan().any())
+
+
+# B's rows ordered (1x128: over 384) and not; K split
+@pytest.mark.parametrize("recipe", RECIPES)
+@pytest.mark.parametrize("M,N,K", [(1300, 2176, 384), (1250, 2176, 3200), (300, 384, 384), (300, 512, 2048), (1000, 896, 1024)])
+def test_gradient_of_operands_with_gaps(fp8, recipe, M, N, K):
+    A = cast(fp8, recipe, workloads.normal_bf16((M, K), 4, "a", std=0.02).cuda(), E5M2)
+    W = cast(fp8, recipe, workloads.normal_bf16((N, K), 4, "b", std=0.05).cuda(), E4M3)
+    z = workloads.normal_bf16((M, 2 * N), 4, "z").cuda()
+    want = gradient(fp8, recipe)(A, W, z)
+    for a, w in ((spaced(A), W), (A, spaced(W)), (spaced(A), spaced(W))):
+        got = gradient(fp8, recipe)(a, w, z)
+        assert torch.equal(got, want) and not bool(got.isnan().any())
