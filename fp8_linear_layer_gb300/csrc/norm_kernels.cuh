@@ -513,9 +513,10 @@ int launch_cols(const NormParams& p, cudaStream_t stream, int num_sms) {
 }
 
 // threads and vectors per thread of a row of nv 16-byte vectors
+constexpr int64_t kOneVectorCols = 1024, kTwoVectorCols = 4096;  // most columns with so many
 void row_shape(int64_t cols, int& T, int& V) {
     const int64_t nv = cols / 8;
-    V = nv <= 128 ? 1 : nv <= 512 ? 2 : 4;
+    V = cols <= kOneVectorCols ? 1 : cols <= kTwoVectorCols ? 2 : 4;
     T = static_cast<int>(((nv + V - 1) / V + 31) / 32 * 32);
 }
 
@@ -536,8 +537,8 @@ void row_shape(int64_t cols, int& T, int& V) {
 // behind it as run at once, in L2: 16384 x 7168 on 1x128 141 us without, 134 with it,
 // 8192 x 4096 41.5 and 40.6 (as far behind as run at once: 135 and 42.2, twice as far 140;
 // 8192 x 2048 23.1 either way).
-inline bool row_alone(int64_t cols, int recipe) {
-    return cols > (recipe == kRecipeBlock ? 512 : 4096);
+constexpr bool row_alone(int64_t cols, int recipe) {
+    return cols > (recipe == kRecipeBlock ? 512 : kTwoVectorCols);
 }
 
 template <bool CENTER, int FMT, int RECIPE>
@@ -569,9 +570,13 @@ int launch_norm(const NormParams& given, cudaStream_t stream, int num_sms) {
             const unsigned all = static_cast<unsigned>(grid_rows);
             rc = T <= 512 ? launch_dependent(norm_rows_kernel<CENTER, FMT, RECIPE, 4, 512, false, false, 2>, all, T, 0, stream, p)
                           : launch_dependent(norm_rows_kernel<CENTER, FMT, RECIPE, 4, 1024, false, false, 1>, all, T, 0, stream, p);
+        } else if (V == 1) {
+            rc = launch_dependent(norm_rows_kernel<CENTER, FMT, RECIPE, 1, 128, true, true, 0>, g, T, 0, stream, p);
+        } else if constexpr (!row_alone(kOneVectorCols + 1, RECIPE)) {
+            static_assert(row_alone(kTwoVectorCols + 1, RECIPE), "wider rows have a CTA of their own");
+            rc = launch_dependent(norm_rows_kernel<CENTER, FMT, RECIPE, 2, 256, true, true, 3>, g, T, 0, stream, p);
         } else {
-            rc = V == 1 ? launch_dependent(norm_rows_kernel<CENTER, FMT, RECIPE, 1, 128, true, true, 0>, g, T, 0, stream, p)
-                        : launch_dependent(norm_rows_kernel<CENTER, FMT, RECIPE, 2, 256, true, true, 3>, g, T, 0, stream, p);
+            return -3;  // not reached: the rule above gives every such row a CTA of its own
         }
     } else {
         switch (V) {
