@@ -16,9 +16,11 @@
 // (a mask in memory would cost a byte or a bit an element twice more).  Each thread
 // has four 16-byte vectors of both inputs in flight, or one where there are too few
 // to give every SM as many: the generator's chain of twenty products per group is
-// hidden by other threads.  CTAs are not persistent; each asks for the inputs of the CTA
-// half as many behind it as run at once, in L2 (34.1 us without; 16384 x 7168 108.7, with it
-// 102.8; as far behind as run at once 34.3, twice as far 37.1).  129 x 1001 takes 1.6 us.
+// hidden by other threads.  CTAs are not persistent; in large matrices without gaps each
+// asks for the inputs of the CTA half as many behind it as run at once, in L2 (34.1 us
+// without; 16384 x 7168 108.7, with it 102.8; as far behind as run at once 34.3, twice as
+// far 37.1).  129 x 1001 takes 1.9 us.  Rows with gaps take the same vectors where
+// addresses and rows are multiples of 16 bytes; anything else goes element by element.
 #include <cuda_runtime.h>
 
 #include "common.cuh"

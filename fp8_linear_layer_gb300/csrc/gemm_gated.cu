@@ -13,8 +13,8 @@
 // 1013 us (1899 TFLOP/s), with Z 1071; MXFP8 597 and 624, per tensor 556 and 640.
 // Gradient: four bytes read and four written per output of the product, which an
 // epilogue of two warps per scheduler handles a step at a time (7.5 us a tile, of 26):
-// 8192 x 14336 over 4096, 629 us (1530 TFLOP/s), MXFP8 387.  With B's rows ordered it
-// needs no shuffles: per tensor 351 (with them 376).
+// 8192 x 14336 over 4096, 628 us (1532 TFLOP/s), MXFP8 387.  With B's rows ordered it
+// needs no shuffles: per tensor 347 (with them 376).
 #include "gemm_kernel.cuh"
 
 namespace fp8ll {
@@ -48,10 +48,13 @@ int gemm_gated_grad_parts(const GemmParams& p) { return gemm_parts(p, kGatesSpli
 
 // The ordered epilogue takes 5 us a tile instead of 7.5, but the K loop in front of it
 // comes out with 296 instructions a warp and block instead of 280: 0.66 us for 0.58.
-// 8192 x 14336, us, ordered / not:
-//   over 128    156 / 214        over 2048   384 / 403
-//   over 1024   259 / 294        over 4096   640 / 628
-// (epilogues of other shapes moved these by a few per cent and not the crossing point)
+// us, ordered / not (8192 x 14336 over 128: 156 / 214):
+//   K blocks         8            16            20            24            28            32
+//   8192 x 14336  256 / 293     382 / 403     446 / 459     508 / 513     573 / 570     637 / 627
+//   8192 x 4096   80.7 / 88.0  117.4 / 120.7 136.4 / 137.1 155.2 / 153.1 174.5 / 169.7 193.2 / 186.1
+//   2048 x 5632   36.5 / 40.6   52.0 / 54.5   59.7 / 61.3   67.8 / 68.3   75.9 / 75.2   83.6 / 82.3
+// They cross between 20 and 28 blocks; at 24 the one taken is at most 1.4% behind.
+// (Epilogues of other shapes moved these by a few per cent and not the crossing point.)
 bool gemm_gated_grad_ordered(const GemmParams& p) { return p.groups[0].nkb <= 24; }
 
 int launch_gemm_gated(const TensorMaps& maps, const GemmParams& p, int epi, int parts, cudaStream_t stream, int grid) {

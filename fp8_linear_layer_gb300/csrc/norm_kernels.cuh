@@ -524,19 +524,30 @@ void row_shape(int64_t cols, int& T, int& V) {
 // without a row loaded ahead.  Its 62 to 64 registers let 1024 threads run on an SM
 // where the next row's would leave 512, and other rows' CTAs hide what a row waits
 // for (its loads, two sums).  us, this / persistent CTAs with the next row ahead
-// (rows x cols, with residual; 1x128 | MXFP8 | per tensor):
-//   4096 x 8192  41.9 / 48.8 | 46.2 / 53.7 | 42.9 / 56.5
-//   777 x 7168   10.6 / 13.0 | 11.7 / 15.1 | 12.0 / 14.2
+// (rows x cols, with residual; 1x128 | MXFP8 | per tensor; later rows asked for in L2
+// by this one, as below, in all its figures):
+//   4096 x 8192  41.9 / 55.2 | 46.1 / 61.8 | 42.8 / 54.6
+//   777 x 7168   10.5 / 13.3 | 11.8 / 16.0 | 11.9 / 14.2
 // where those have two vectors a thread or one, and 768 or more threads on an SM:
-//   8192 x 4096  40.6 / 43.8 | 45.4 / 47.4 | 43.0 / 41.0
-//   16384 x 1024 22.6 / 24.3 | 24.9 / 27.0 | 23.8 / 24.0
-//   777 x 2048    4.2 /  4.3 |  5.0 /  4.7 |  5.6 /  4.6
-//   400 x 4096    4.2 /  4.0 |  5.8 /  4.6 |  5.4 /  4.6
-// The number of rows does not count: a row's sums are added in one order in any batch.
-// From 128 threads a row on, a CTA asks for the inputs of the row half as many CTAs
-// behind it as run at once, in L2: 16384 x 7168 on 1x128 141 us without, 134 with it,
-// 8192 x 4096 41.5 and 40.6 (as far behind as run at once: 135 and 42.2, twice as far 140;
-// 8192 x 2048 23.1 either way).
+//   8192 x 4096  40.5 / 43.9 | 45.1 / 47.5 | 41.5 / 41.1
+//   2000 x 4096  13.6 / 14.0 | 14.6 / 15.1 | 14.3 / 12.4
+//   400 x 4096    4.3 /  4.1 |  5.8 /  4.6 |  5.6 /  4.7
+//   8192 x 2048  23.6 / 23.5 | 25.8 / 25.2 | 24.3 / 22.9
+//   777 x 2048    4.3 /  4.3 |  4.9 /  4.7 |  5.9 /  4.6
+//   16384 x 1024 23.2 / 24.4 | 24.7 / 27.1 | 23.5 / 23.9
+//   2000 x 1024   4.4 /  5.2 |  4.9 /  6.2 |  6.7 /  5.5
+// So 1x128 takes it for all of these and per tensor for none.  MXFP8 up to 4096
+// columns could go either way: a CTA per row gains 3 to 20% in four of them and
+// loses 2 to 25% in three, and the rule is for the short call of wide rows (400 x
+// 4096).  The number of rows may not decide: the two forms add a row's sums in
+// different orders, and a row's result is to be the same in any batch.
+//
+// From 128 threads a row on, a CTA asks for the inputs of a later row in L2: the one
+// half as many CTAs behind it as run at once, and above 16384 columns, where one CTA
+// fits an SM, as many as run at once.  1x128: 16384 x 7168 141 us without, 134 with
+// it, 8192 x 4096 41.5 and 40.6 (as far behind as run at once: 135 and 42.2, twice as
+// far 140; 8192 x 2048 23.1 either way); 2048 x 24576 83 without, 76.2 with it, half
+// as far 75.3, and 4096 x 16512 132, 120.0 and 119.9.
 constexpr bool row_alone(int64_t cols, int recipe) {
     return cols > (recipe == kRecipeBlock ? 512 : kTwoVectorCols);
 }
@@ -598,9 +609,9 @@ int launch_norm(const NormParams& given, cudaStream_t stream, int num_sms) {
 // and CENTER, with xhat = (h - mean) rstd and m0 = mean_c d:
 //   dx = rstd (d - m0 - xhat m) + dres   dbeta_c = sum_r dy
 //
-// Bound by HBM: 16384 x 7168 with the residual's gradient 159 us, 0.87 of the copy
-// rate; 0.49 at 32768 columns, where a thread holds eight vectors and loads
-// nothing ahead.
+// Bound by HBM: 16384 x 7168 with the residual's gradient 159 us (CENTER: 169), 0.87
+// (0.83) of the copy rate; the RMS norm's 0.49 at 32768 columns, where a thread holds
+// eight vectors and loads nothing ahead.
 // T threads walk rows together; a thread keeps the same columns for all of
 // them, so dgamma is summed in its registers (SMEM: in shared memory, where a
 // row is too wide for them) and written once per CTA as a band of partial sums,
