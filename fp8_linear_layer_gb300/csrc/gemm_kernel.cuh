@@ -932,7 +932,7 @@ __device__ __forceinline__ void store_gated(const GemmParams& p, int row0, int c
 // vectors of the next 32 columns are on their way while the ones before are used.
 // (Z and dZ by TMA through shared memory, in the accumulators' order, take half of
 // the instructions, 8192 x 14336 over 128 169 us instead of 214, but the K loop comes
-// out slower: over 4096 671 instead of 628.  Rows together instead of one by one: 746.
+// out slower: over 4096 671 instead of 629.  Rows together instead of one by one: 746.
 // Z in words, without the shuffles in front: 725.)
 template <bool GELU, int ROWS = 4>
 __device__ __forceinline__ void store_gated_grad(const GemmParams& p, int row0, int col0,
