@@ -123,9 +123,11 @@ class GatedFeedForwardBlock:
     """tokens m, width k, hidden width n, in the 1x128 recipe; m, k and n multiples
     of 128.  act: B.ACT_SILU or B.ACT_GELU.  p: the probability with which an element
     of x is dropped, by masks of ``seed`` (of the run) and ``site`` (this block's
-    number in the model); ``step`` (int64, on the device) counts the calls of
-    ``backward``, so a forward pass and its backward pass draw the same mask, and
-    the replays of a captured step different ones.  Gradients accumulate in fp32
+    number in the model: blocks with the same seed and site, the defaults among them,
+    draw the same mask, so each block of a model needs a site of its own); ``step``
+    (int64, on the device) counts the calls of ``backward``, so a forward pass and its
+    backward pass draw the same mask, and the replays of a captured step different
+    ones.  Without dropout: ``decode``, or ``p`` set to 0.  Gradients accumulate in fp32
     over calls of ``backward`` until ``zero_grad``; ``clip`` scales them in place."""
 
     def __init__(self, m: int, k: int, n: int, p: float = 0.1, act: int = B.ACT_SILU, eps: float = 1e-5, seed: int = 0,
